@@ -56,15 +56,19 @@ struct LinArgs {
   const float* s_in;       // [B][H][dk][dv] ([dv][dk] when s_trans), or null
   float* s_out;            // or null
   bool s_trans;
+  // bf16: what is added to the state is exact to 24 bits (a state that is given
+  // out) instead of 16 (one that only meets bf16 operands).
+  bool exact_state;
   int64_t B, T, H, dk, dv;
   float scale_o, scale_p, scale_u;
   int32_t late;
   bool reverse;
+  // The segments' states are in the workspace already, left there by the pass
+  // with k and v exchanged (same sequences, lengths and direction).
+  bool seg_trans;
   Dtype dt;
 };
-// Segments a chunked pass splits each sequence into, and the bytes of their
-// states (0: one segment).
-int64_t linattn_segments(int64_t B, int64_t H, int64_t T);
+// Bytes of the states that a chunked pass keeps between its launches (0: none).
 size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv);
 hipError_t launch_linattn_chunked(const LinArgs& a, float* seg, hipStream_t s);
 // The recurrent form, T <= kLinStepTokens (forward direction, late = 1, out in

@@ -121,6 +121,16 @@ ttt_status_t linattn_dims(const ttt_linattn_desc_t* d) {
   return TTT_OK;
 }
 
+// The chunked kernels reach a chunk's rows by 32-bit offsets from its first.
+constexpr int64_t kMaxTokenBytes = (int64_t)1 << 27;
+ttt_status_t check_token_strides(const ttt_linattn_desc_t* d, bool with_do) {
+  const int64_t es = (int64_t)ttt::dtype_bytes(to_dtype(d->dtype));
+  for (const int64_t* st : {d->q_stride, d->k_stride, d->v_stride, with_do ? d->o_stride : d->q_stride})
+    if (d->seq_len > 1 && st[1] * es > kMaxTokenBytes)
+      return fail(TTT_ERR_UNSUPPORTED, "the token strides of q, k, v and dO must be at most 2^27 bytes");
+  return TTT_OK;
+}
+
 // Whether a tensor that is written has one place for each element: every
 // dimension's stride is at least the extent of those with smaller ones.
 bool one_place_each(const ttt_linattn_desc_t* d, const int64_t st[3], int64_t heads, int64_t dim) {
@@ -268,6 +278,7 @@ ttt_status_t ttt_linattn_forward(const ttt_linattn_desc_t* desc, const void* q, 
     return fail(TTT_ERR_INVALID_ARGUMENT, "q, k, v, log_decay and o must be non-NULL");
   if (!aligned(lengths, 4) || !aligned(log_decay, 4))
     return fail(TTT_ERR_INVALID_ARGUMENT, "log_decay and lengths must be 4-byte aligned");
+  if (ttt_status_t st = check_token_strides(desc, false)) return st;
   if (!one_place_each(desc, desc->o_stride, desc->heads, desc->d_value))
     return fail(TTT_ERR_INVALID_ARGUMENT, "o_stride gives two elements of o one place");
   const size_t need = forward_bytes(desc);
@@ -295,7 +306,7 @@ ttt_status_t ttt_linattn_forward(const ttt_linattn_desc_t* desc, const void* q, 
   a.out = o;
   a.osb = desc->o_stride[0], a.ost = desc->o_stride[1], a.osh = desc->o_stride[2];
   a.log_decay = log_decay, a.lengths = lengths;
-  a.s_in = state_in, a.s_out = state_out;
+  a.s_in = state_in, a.s_out = state_out, a.exact_state = true;
   a.B = desc->batch, a.T = desc->seq_len, a.H = H, a.dk = desc->d_key, a.dv = desc->d_value;
   a.scale_o = a.scale_p = desc->scale, a.scale_u = 1.0f, a.late = 1;
   a.dt = to_dtype(desc->dtype);
@@ -317,6 +328,7 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
                 "q, k, v, log_decay, dO, dq, dk and dv must be non-NULL");
   if (!aligned(lengths, 4) || !aligned(log_decay, 4))
     return fail(TTT_ERR_INVALID_ARGUMENT, "log_decay and lengths must be 4-byte aligned");
+  if (ttt_status_t st = check_token_strides(desc, true)) return st;
   const BackwardPlan plan = backward_plan(desc);
   if (ttt_status_t st = check_workspace(ws, ws_bytes, plan.total)) return st;
   const int64_t B = desc->batch, T = desc->seq_len, H = desc->heads, G = desc->kv_heads;
@@ -362,10 +374,13 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
   hipError_t e = ttt::launch_linattn_chunked(a, seg, s);
 
   // dk and dv run from the last token; their state starts from dstate_out and
-  // ends as dstate_in
+  // ends as dstate_in.  dk's is dv's transposed, also at the segments' starts.
+  // dstate_in may be dstate_out, so the pass that writes it is the last one
+  // that reads dstate_out: dv's, or with segments' states left by it, dk's.
+  const bool shared = ttt::linattn_segment_bytes(B, H, T, K, V) != 0;
   const auto from_end = [&](const ttt::LinOperand& x, const ttt::LinOperand& y,
                             const ttt::LinOperand& z, int64_t dx, int64_t dz, void* out,
-                            bool trans, float* s_out) {
+                            bool is_dk) {
     if (e != hipSuccess) return;
     a = base;
     a.q = x, a.k = y, a.v = z;
@@ -376,14 +391,17 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
     } else {
       a.out = out, a.osb = T * G * dz, a.ost = G * dz, a.osh = dz;
     }
-    a.s_in = dstate_out, a.s_trans = trans, a.s_out = s_out;
+    a.s_in = dstate_out, a.s_trans = is_dk, a.s_out = is_dk ? nullptr : dstate_in;
+    a.exact_state = !is_dk;
+    a.seg_trans = is_dk && shared;
     a.scale_o = 1.0f, a.scale_u = desc->scale, a.late = 0, a.reverse = true;
     e = ttt::launch_linattn_chunked(a, seg, s);
     if (e == hipSuccess && part)
       e = ttt::launch_linattn_sum_heads(part, out, T * G * dz, G * dz, dz, B, T, G, rep, dz, dt, s);
   };
-  from_end(ov, od, oq, V, K, dk, true, nullptr);
-  from_end(ok_, oq, od, K, V, dv, false, dstate_in);
+  if (!shared) from_end(ov, od, oq, V, K, dk, true);
+  from_end(ok_, oq, od, K, V, dv, false);
+  if (shared) from_end(ov, od, oq, V, K, dk, true);
   return e == hipSuccess ? ok() : hip_fail(e, "linattn_backward");
 }
 

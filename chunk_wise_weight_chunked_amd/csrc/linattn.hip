@@ -18,7 +18,7 @@
 //   S              lanes = value columns, registers = keys -> A operand of S^T Q^T
 //   O^T = S^T Q^T, scaled per query row = per lane, + V^T P^T
 //   S  += K^T (w V) with V's fragments, already read for V^T P^T, weighted and
-//                  split in registers
+//                  split into bf16 terms in registers
 // A 32x32 result holds rows 8 (r / 4) + 4 (lane / 32) + r % 4 in registers r,
 // an operand wants 8 consecutive k values 8 (lane / 32) + 0..7: the rows of
 // the A operands are fed in an order with bits 2 and 3 of the index swapped
@@ -26,19 +26,23 @@
 // runs.
 //
 // Few heads leave most CUs without work, so a sequence is split into segments
-// (linattn_segments): one pass computes every segment's end state from K and V
+// (split() below): one pass computes every segment's end state from K and V
 // alone, one adds them up along the sequence, and the main pass starts each
 // segment from its state.
 //
 // Rounding (bf16 operands): the decayed scores and the state's copy that
 // meets Q are rounded to bf16 once, like any bf16 operand of a product whose
-// result is bf16; S itself is fp32 and what is added to it is exact to about
-// 2^-17, since the weighted V goes in as two bf16 terms.  fp32 operands use
-// fp32 MFMAs and no rounding.
+// result is bf16.  S itself is fp32, and the weighted V goes into it as three
+// bf16 terms (24 bits), so that a state that is given out is as exact as fp32
+// sums make it; two terms (2^-17) where the pass's state only ever meets bf16
+// operands (the gradients of q and k).  The third term costs 3% to 4% (16
+// prompts of 8192 tokens: 636 us with two terms, 656 us with three).  fp32
+// operands use fp32 MFMAs and no rounding.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "block.h"
 #include "gemm_core.h"
@@ -49,13 +53,26 @@ namespace {
 constexpr int kC = kLinChunk;
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// g^n for n >= 0 from log2 g (g = 0 at -inf).
+// log2 of a decay of exp(lg), finite: below any decay that is not 0 in fp32, so
+// that a power of 0 is 1 and every other one 0.
+__device__ __forceinline__ float log2_decay(float lg) {
+  const float x = lg * kLog2e;
+  return x < -1e30f ? -1e30f : x;
+}
+// g^n for n >= 0.  The hardware's exp2: results below 2^-126 are 0.
 __device__ __forceinline__ float decay_pow(float lg2, int n) {
-  return n == 0 ? 1.0f : exp2f(lg2 * (float)n);
+  return __builtin_amdgcn_exp2f(lg2 * (float)n);
 }
 
 __device__ __forceinline__ int perm16(int i) {  // bits 2 and 3 swapped
   return (i & ~12) | ((i & 4) << 1) | ((i & 8) >> 1);
+}
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+// Two values rounded to bf16 in one instruction.
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, bf16x2_t{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
 }
 
 // ------------------------------------------------------- tiles and fragments
@@ -86,25 +103,87 @@ struct Frag<uint16_t> {
     return {lds_load<bf16x8_t>(t + Tile<uint16_t>::offset(row, 16 * step + 8 * (lane >> 5)))};
   }
   // k along the tile's rows (tokens): lane l takes column col0 + perm16(l % 32).
-  // The transposing read gives lane j of 16 the columns of the word that
-  // lanes j / 4 (mod 4) address, four rows of them; see read_a_tr.
-  __device__ __forceinline__ static Frag cols(const lds_char* t, int col0, int step, int lane) {
+  // A transposing read gives lane j of 16 the columns of the word that lanes
+  // j / 4 (mod 4) address, four rows of them (see read_a_tr); rows +4 and
+  // columns +32 change the swizzle, rows +16 and panels only the address.
+  // LDS address of the read of rows 4 h.., columns col0 .., k step 0.
+  __device__ __forceinline__ static uint32_t tr_addr(const lds_char* t, int col0, int h, int lane) {
     const int g = lane >> 4, j = lane & 15, w = j & 3;
     const int col = col0 + 16 * (g & 1) + 4 * (((w & 1) << 1) | (w >> 1));
-    const int row = 16 * step + 8 * (g >> 1) + (j >> 2);
-    bf16x4_t x[2];
+    return (uint32_t)(uintptr_t)(t + Tile<uint16_t>::offset(8 * (g >> 1) + (j >> 2) + 4 * h, col));
+  }
+  // Fragments of both k steps of columns col0 ...
+  __device__ __forceinline__ static void cols2(Frag (&f)[2], const lds_char* t, int col0, int lane) {
+    tr4<0, 16 * kRowBytes>(f, tr_addr(t, col0, 0, lane), tr_addr(t, col0, 1, lane));
+  }
+  // Fragments of k step `step` of the N tiles of 32 columns from column 0.
+  template <int step, int N>
+  __device__ __forceinline__ static void cols_all(Frag (&f)[N], const lds_char* t, int lane) {
+    constexpr int kStep = step * 16 * kRowBytes, kPanel = kC * kRowBytes;
+    const uint32_t a0 = tr_addr(t, 0, 0, lane), a1 = tr_addr(t, 0, 1, lane);
+    const uint32_t b0 = tr_addr(t, 32, 0, lane), b1 = tr_addr(t, 32, 1, lane);
+    if constexpr (N == 2) {
+      tr4(f, a0, a1, b0, b1, kStep);
+    } else {
+      static_assert(N == 4, "two or four tiles");
+      u32x2_t x[8];
+      asm volatile(
+          "ds_read_b64_tr_b16 %0, %8 offset:%12\n\t"
+          "ds_read_b64_tr_b16 %1, %9 offset:%12\n\t"
+          "ds_read_b64_tr_b16 %2, %10 offset:%12\n\t"
+          "ds_read_b64_tr_b16 %3, %11 offset:%12\n\t"
+          "ds_read_b64_tr_b16 %4, %8 offset:%13\n\t"
+          "ds_read_b64_tr_b16 %5, %9 offset:%13\n\t"
+          "ds_read_b64_tr_b16 %6, %10 offset:%13\n\t"
+          "ds_read_b64_tr_b16 %7, %11 offset:%13\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]),
+            "=&v"(x[6]), "=&v"(x[7])
+          : "v"(a0), "v"(a1), "v"(b0), "v"(b1), "n"(kStep), "n"(kStep + kPanel));
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      x[h] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-          (__attribute__((address_space(3))) bf16x4_t*)(t + Tile<uint16_t>::offset(row + 4 * h, col)));
-    return {bf16x8_t{x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]}};
+      for (int i = 0; i < 4; ++i) f[i] = join(x[2 * i], x[2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ static Frag join(u32x2_t lo, u32x2_t hi) {
+    return {__builtin_bit_cast(bf16x8_t, u32x4_t{lo[0], lo[1], hi[0], hi[1]})};
+  }
+  // The transposing reads are inline assembly, each block with its wait: the
+  // compiler lets the builtin wait for every direct-to-LDS load in flight,
+  // also those into the other buffer, which would end the prefetch.
+  template <int kOff0, int kOff1>
+  __device__ __forceinline__ static void tr4(Frag (&f)[2], uint32_t a0, uint32_t a1) {
+    u32x2_t x[4];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4 offset:%6\n\t"
+        "ds_read_b64_tr_b16 %1, %5 offset:%6\n\t"
+        "ds_read_b64_tr_b16 %2, %4 offset:%7\n\t"
+        "ds_read_b64_tr_b16 %3, %5 offset:%7\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+        : "v"(a0), "v"(a1), "n"(kOff0), "n"(kOff1));
+    f[0] = join(x[0], x[1]);
+    f[1] = join(x[2], x[3]);
+  }
+  __device__ __forceinline__ static void tr4(Frag (&f)[2], uint32_t a0, uint32_t a1, uint32_t b0,
+                                             uint32_t b1, int off) {
+    u32x2_t x[4];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4\n\t"
+        "ds_read_b64_tr_b16 %1, %5\n\t"
+        "ds_read_b64_tr_b16 %2, %6\n\t"
+        "ds_read_b64_tr_b16 %3, %7\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+        : "v"(a0 + off), "v"(a1 + off), "v"(b0 + off), "v"(b1 + off));
+    f[0] = join(x[0], x[1]);
+    f[1] = join(x[2], x[3]);
   }
   // registers 8 half .. of a result
   __device__ __forceinline__ static Frag result(const floatx16_t& c, int half) {
-    Frag f;
+    uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f.v[e] = static_cast<__bf16>(c[8 * half + e]);
-    return f;
+    for (int e = 0; e < 4; ++e) w[e] = cvt_bf16x2(c[8 * half + 2 * e], c[8 * half + 2 * e + 1]);
+    return {__builtin_bit_cast(bf16x8_t, u32x4_t{w[0], w[1], w[2], w[3]})};
   }
 };
 
@@ -130,6 +209,15 @@ struct Frag<float> {
           t + Tile<float>::offset(16 * step + 8 * (lane >> 5) + e, col0 + perm16(lane & 31)));
     return f;
   }
+  __device__ __forceinline__ static void cols2(Frag (&f)[2], const lds_char* t, int col0, int lane) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) f[s] = cols(t, col0, s, lane);
+  }
+  template <int step, int N>
+  __device__ __forceinline__ static void cols_all(Frag (&f)[N], const lds_char* t, int lane) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = cols(t, 32 * i, step, lane);
+  }
   __device__ __forceinline__ static Frag result(const floatx16_t& c, int half) {
     Frag f;
 #pragma unroll
@@ -146,58 +234,95 @@ __device__ __forceinline__ void mma(floatx16_t& c, const Frag<float>& a, const F
   for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[e], b.v[e], c, 0, 0, 0);
 }
 
-// c += a (w v), w[e] weighting the fragment's k values.
-__device__ __forceinline__ void weighted(Frag<uint16_t>* hi, Frag<uint16_t>* lo,
-                                         const Frag<uint16_t>& v, const float w[8], float base) {
+// w[e] v[e] as a sum of three bf16 terms, or in fp32.
+__device__ __forceinline__ void weighted(Frag<uint16_t> (&x3)[3], const Frag<uint16_t>& v,
+                                         const float* w) {
+  const u32x4_t in = __builtin_bit_cast(u32x4_t, v.v);
+  u32x4_t t[3];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float x = static_cast<float>(v.v[e]) * (w[e] * base);
-    hi->v[e] = static_cast<__bf16>(x);
-    lo->v[e] = static_cast<__bf16>(x - static_cast<float>(hi->v[e]));
+  for (int e = 0; e < 4; ++e) {
+    float x = __uint_as_float(in[e] << 16) * w[2 * e];
+    float y = __uint_as_float(in[e] & 0xffff0000u) * w[2 * e + 1];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      uint32_t top = cvt_bf16x2(x, y);
+      asm("" : "+v"(top));  // one paired conversion: seen through, the halves are converted again
+      t[i][e] = top;
+      x -= __uint_as_float(top << 16);
+      y -= __uint_as_float(top & 0xffff0000u);
+    }
   }
-}
-__device__ __forceinline__ void weighted(Frag<float>* hi, Frag<float>*, const Frag<float>& v,
-                                         const float w[8], float base) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) hi->v[e] = v.v[e] * (w[e] * base);
+  for (int i = 0; i < 3; ++i) x3[i].v = __builtin_bit_cast(bf16x8_t, t[i]);
+}
+__device__ __forceinline__ void weighted(Frag<float> (&x3)[3], const Frag<float>& v, const float* w) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x3[0].v[e] = v.v[e] * w[e];
 }
 
 // 8 results in a row, to the operands' type or fp32.
 __device__ __forceinline__ void store8(uint16_t* p, const float* f) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                            pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  *reinterpret_cast<uint4*>(p) = make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]),
+                                            cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
 }
 __device__ __forceinline__ void store8(float* p, const float* f) {
   *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// The pieces of one operand's tile that a thread carries from memory to LDS.
-template <typename T, int kCols, int kThreads>
-struct Stage {
-  static constexpr int kPerRow = kCols / Tile<T>::kPerPiece;
-  static constexpr int kCount = kC * kPerRow / kThreads;
-  static_assert(kC * kPerRow % kThreads == 0, "whole pieces per thread");
-  uint4 v[kCount];
-  // Rows [skip, kC) of the tile are tokens first, first + 1, ... (first - 1, ...
-  // when step is negative) of `base`; other rows and columns from d on are 0.
-  __device__ __forceinline__ void load(const T* base, int64_t step, int skip, int d) {
+// Direct-to-LDS loads of one operand's tile: an instruction moves 8 rows of a
+// panel (1 KB, lane l to byte 16 l), NW waves share a tile's instructions.  The
+// lane's source piece is chosen so that the tile comes out swizzled.  Offsets
+// are from the lowest row of the chunk; columns that the head does not have, and
+// rows in front of a last chunk's tokens, lie outside the descriptor's range,
+// which makes their values zero.
+constexpr uint32_t kRange = 0xffffff00u, kOutside = 0xffffff80u;
+
+template <typename T, int kCols, int NW>
+struct Loader {
+  static constexpr int kPer = kC / 8 * (kCols / Tile<T>::kPerPanel) / NW;
+  static_assert(kC / 8 * (kCols / Tile<T>::kPerPanel) % NW == 0, "whole instructions per wave");
+  const char* base;     // the lowest row of the next chunk
+  int64_t chunk_bytes;  // to the chunk after it
+  uint32_t off[kPer];
+  int row0;
+
+  // `first`: the head's row of the walk's first token; rows of the walk are
+  // `st` values apart, downwards if `reverse`.
+  __device__ __forceinline__ void init(const T* first, int64_t st, bool reverse, int d, int wave,
+                                       int lane) {
+    const int64_t bytes = st * (int64_t)sizeof(T);
+    base = reinterpret_cast<const char*>(first) - (reverse ? (kC - 1) * bytes : 0);
+    chunk_bytes = reverse ? -kC * bytes : kC * bytes;
+    row0 = lane >> 3;
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) {
-      const int p = (int)threadIdx.x + i * kThreads;
-      const int row = p / kPerRow, col = (p % kPerRow) * Tile<T>::kPerPiece;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (row >= skip && col < d)
-        v[i] = *reinterpret_cast<const uint4*>(base + (int64_t)(row - skip) * step + col);
+    for (int q = 0; q < kPer; ++q) {
+      const int row = row_of(q, wave);
+      const int col = panel_of(q, wave) * Tile<T>::kPerPanel +
+                      ((lane & 7) ^ lds_swz_tr(row)) * Tile<T>::kPerPiece;
+      off[q] = col < d ? (uint32_t)((reverse ? kC - 1 - row : row) * bytes + col * (int)sizeof(T))
+                       : kOutside;
     }
   }
-  __device__ __forceinline__ void store(lds_char* t) const {
+  __device__ __forceinline__ int row_of(int q, int wave) const {
+    return (wave * kPer + q) % (kC / 8) * 8 + row0;
+  }
+  __device__ __forceinline__ static int panel_of(int q, int wave) {
+    return (wave * kPer + q) / (kC / 8);
+  }
+  // The next chunk into `tile`; its tokens are the tile's last kC - skip rows.
+  // shift: bytes from `base` to the first of these rows' place.
+  __device__ __forceinline__ void issue(lds_char* tile, int skip, int64_t shift, int wave) {
+    const rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base + shift), (short)0,
+                                                       (int)kRange, 0x00020000);
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) {
-      const int p = (int)threadIdx.x + i * kThreads;
-      lds_store<u32x4_t>(
-          t + Tile<T>::offset(p / kPerRow, (p % kPerRow) * Tile<T>::kPerPiece), as_u32x4(v[i]));
+    for (int q = 0; q < kPer; ++q) {
+      const uint32_t o = row_of(q, wave) >= skip ? off[q] : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          r, (__attribute__((address_space(3))) void*)(tile + (wave * kPer + q) * 8 * kRowBytes), 16,
+          o, 0, 0, 0);
     }
+    base += chunk_bytes;
   }
 };
 
@@ -212,31 +337,67 @@ __device__ __forceinline__ int64_t live_tokens(const int32_t* lengths, int64_t b
   return n < 0 ? 0 : n > T ? T : n;
 }
 
+// Up to so many segments the main pass adds their ends up itself.
+constexpr int kScanInPlace = 8;
+
 // DK: key columns of the tiles (64 or 128, at least dk); NW waves of 32 value
 // columns.  kOut: the main pass; otherwise the pass that leaves each segment's
 // end state in `seg`, which holds a start state per segment: slot g + 1 gets
 // segment g's end, slot 0 the state the sequence starts from (the main pass
 // reads it from there, since s_out may be s_in).
-template <typename T, int DK, int NW, bool kOut>
-__global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, float* seg,
+template <typename T, int DK, int NW, bool kOut, bool kF32Out = false>
+__global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, float4* seg,
                                                                      int64_t seg_len, int nseg) {
   constexpr int kThreads = 64 * NW, DV = 32 * NW, KT = DK / 32;
   constexpr bool kSplit = sizeof(T) == 2;
-  __shared__ __attribute__((aligned(16))) char smem[kC * (2 * DK + DV) * sizeof(T)];
-  lds_char* sK = (lds_char*)smem;
-  lds_char* sV = sK + kC * DK * sizeof(T);
-  lds_char* sQ = sV + kC * DV * sizeof(T);
+  constexpr int kOffV = kC * DK * sizeof(T), kOffQ = kOffV + kC * DV * sizeof(T);
+  constexpr int kBuf = kOffQ + (kOut ? kC * DK * (int)sizeof(T) : 0);
+  // Two buffers, two objects: reads of one are seen not to depend on the loads
+  // that are filling the other.
+  __shared__ __attribute__((aligned(16))) char smem0[kBuf], smem1[kBuf];
 
   const int per = kOut ? nseg : nseg - 1;  // nobody starts from the last segment's end
   const int g = (int)(blockIdx.x % per);
   const int64_t bh = blockIdx.x / per, b = bh / a.H, h = bh % a.H;
   const int64_t n = live_tokens(a.lengths, b, a.T);
-  const int64_t t_lo = g * seg_len, t_hi = min(t_lo + seg_len, n);
+  const float lg = a.log_decay[h];
+  int64_t t_lo = g * seg_len;
+  const int64_t t_hi = min(t_lo + seg_len, n);
+  if constexpr (!kOut) {
+    // tokens whose decay to the segment's end is 0 in fp32 (below 2^-150) do
+    // not reach the state there
+    const float reach = -104.0f / lg;
+    if (lg < 0.0f && reach < (float)(t_hi - t_lo))
+      t_lo = max(t_lo, t_hi - ((int64_t)reach / kC + 1) * kC);
+  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
   const int dk = (int)a.dk, dv = (int)a.dv;
-  const int64_t slot_size = (int64_t)DK * DV;
-  float* slot = seg ? seg + (bh * nseg + g) * slot_size + (int64_t)wave * KT * 16 * 64 + lane
-                    : nullptr;
+  // ---- token rows: token t of the walk is row t, or row n - 1 - t of the tensors
+  const T* kp = head_base<T>(a.k, b, h);
+  const T* vp = head_base<T>(a.v, b, h);
+  const T* qp = head_base<T>(a.q, b, h);
+  const int64_t row0 = a.reverse ? n - 1 - t_lo : t_lo;
+  const int uwave = __builtin_amdgcn_readfirstlane(wave);
+  Loader<T, DK, NW> ldK, ldQ;
+  Loader<T, DV, NW> ldV;
+  ldK.init(kp + row0 * a.k.st, a.k.st, a.reverse, dk, uwave, lane);
+  ldV.init(vp + row0 * a.v.st, a.v.st, a.reverse, dv, uwave, lane);
+  if constexpr (kOut) ldQ.init(qp + row0 * a.q.st, a.q.st, a.reverse, dk, uwave, lane);
+  const auto issue = [&](int64_t t, lds_char* tiles_of) {
+    // a last chunk of m < kC tokens fills the tiles' last m rows, so that every
+    // weight above is the same as in a whole chunk
+    const int skip = (int)max((int64_t)0, kC - (t_hi - t));
+    const int64_t back = (a.reverse ? skip : -skip) * (int64_t)sizeof(T);
+    ldK.issue(tiles_of, skip, back * a.k.st, uwave);
+    ldV.issue(tiles_of + kOffV, skip, back * a.v.st, uwave);
+    if constexpr (kOut) ldQ.issue(tiles_of + kOffQ, skip, back * a.q.st, uwave);
+  };
+  if (t_lo < t_hi) issue(t_lo, (lds_char*)smem0);  // on its way while the rest is set up
+
+  // a slot of the workspace: register 4 r.. of tile i of wave w at float4
+  // ((w KT + i) 4 + r) 64 + lane
+  const int64_t slot4 = (int64_t)DK * DV / 4;
+  float4* slot = seg ? seg + bh * nseg * slot4 : nullptr;
 
   // ---- the state: registers r of tile i hold key row 32 i + 16 (r / 8) + 8 half
   // + r % 8 of value column 32 wave + perm16(lane % 32)
@@ -247,46 +408,73 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
     if (row >= dk || col >= dv) return -1;
     return bh * dk * dv + (a.s_trans ? (int64_t)col * dk + row : (int64_t)row * dv + col);
   };
-  if (g > 0 && t_lo < n && kOut) {
+  const auto from_slot = [&](int64_t j, float f) {  // S = f S + slot j
+    const float4* p = slot + j * slot4;
+    if (a.seg_trans) {
+      // written by the pass with keys and values exchanged: this lane's key row
+      // is its value column, in tile `wave` of the wave that has it
+      const int w = col & 31, lane_bits = ((w >> 3) & 1) * 32;
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int other = perm16(16 * (r >> 3) + 8 * half + (r & 7)) + lane_bits;
+          const float x = reinterpret_cast<const float*>(
+              p + ((i * NW + wave) * 4 + 2 * (w >> 4) + ((w & 7) >> 2)) * 64 + other)[w & 3];
+          S[i][r] = fmaf(f, S[i][r], x);
+        }
+      return;
+    }
+    p += wave * KT * 4 * 64 + lane;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) S[i][r] = slot[(i * 16 + r) * 64];
-  } else if (g == 0 && kOut && slot) {
+      for (int r = 0; r < 4; ++r) {
+        const float4 x = p[(i * 4 + r) * 64];
+        S[i][4 * r] = fmaf(f, S[i][4 * r], x.x), S[i][4 * r + 1] = fmaf(f, S[i][4 * r + 1], x.y);
+        S[i][4 * r + 2] = fmaf(f, S[i][4 * r + 2], x.z), S[i][4 * r + 3] = fmaf(f, S[i][4 * r + 3], x.w);
+      }
+  };
+  const auto to_slot = [&](int64_t j) {
+    float4* p = slot + j * slot4 + wave * KT * 4 * 64 + lane;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) S[i][r] = slot[(i * 16 + r) * 64];
-  } else {
+      for (int r = 0; r < 4; ++r)
+        p[(i * 4 + r) * 64] =
+            make_float4(S[i][4 * r], S[i][4 * r + 1], S[i][4 * r + 2], S[i][4 * r + 3]);
+  };
+#pragma unroll
+  for (int i = 0; i < KT; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) S[i][r] = 0.0f;
+  if (kOut && slot) {
+    if (t_lo < n || g == 0) {
+      // few segments: their ends are added up here, otherwise by linattn_scan_kernel
+      const float f = exp2f(log2_decay(lg) * (float)seg_len);
+      if (nseg <= kScanInPlace)
+        for (int j = min(g, 1); j < g; ++j) from_slot(j, f);
+      from_slot(g, nseg <= kScanInPlace ? f : 0.0f);
+    }
+  } else if (g == 0 && a.s_in) {
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        S[i][r] = 0.0f;
-        if (g == 0 && a.s_in) {
-          const int64_t at = state_at(i, r);
-          if (at >= 0) S[i][r] = a.s_in[at];
-        }
+        const int64_t at = state_at(i, r);
+        if (at >= 0) S[i][r] = a.s_in[at];
       }
-    if (!kOut && g == 0) {
-#pragma unroll
-      for (int i = 0; i < KT; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) slot[(i * 16 + r) * 64] = S[i][r];
-    }
   }
+  if (!kOut && g == 0) to_slot(0);
 
   // ---- decay factors
-  const float lg2 = a.log_decay[h] * kLog2e;
+  const float lg2 = log2_decay(lg);
   const int qrow = lane & 31;
-  float w8[8];       // g^(7-e)
-  float w_base[2];   // update: scale_u g^(kC - late - 16 step - 8 half - 7), times w8 = the token's
-  float d_in[16];    // scores: scale_p g^(query - key), register = key
+  float w_up[16];  // update: scale_u g^(kC - late - token), token 16 (r / 8) + 8 half + r % 8
+  float d_in[16];  // scores: scale_p g^(query - key), the same keys
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w8[e] = decay_pow(lg2, 7 - e);
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-    w_base[s] = a.scale_u * decay_pow(lg2, kC - a.late - 16 * s - 8 * half - 7);
+  for (int r = 0; r < 16; ++r)
+    w_up[r] = a.scale_u * decay_pow(lg2, kC - a.late - (16 * (r >> 3) + 8 * half + (r & 7)));
   if constexpr (kOut) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
@@ -295,119 +483,158 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
     }
   }
   float f_out = a.scale_o * decay_pow(lg2, qrow + a.late);  // query row's factor on Q S
-  // g^kC as 1 + (g^kC - 1) where it is near 1: the rounded factor is applied
-  // once per chunk, and its error would grow with the number of chunks that
-  // the state remembers
-  float step_m1 = expm1f(a.log_decay[h] * (float)kC), step = decay_pow(lg2, kC);
-  const auto decay_state = [&] {
-    if (step > 0.5f) {
+  // g^kC is applied once per chunk, so the error of a rounded factor would grow
+  // with the chunks that the state remembers: the two floats around g^kC take
+  // turns so that their product stays within one rounding of the power.
+  const double step64 = exp((double)lg * kC);
+  const float step_lo = __double2float_rd(step64), step_hi = __double2float_ru(step64);
+  const float err_lo = step_lo > 0.0f ? (float)(step_lo / step64 - 1.0) : 0.0f;
+  const float err_hi = step_lo > 0.0f ? (float)(step_hi / step64 - 1.0) : 0.0f;
+  float err = 0.0f;
+
+  // A chunk's outputs pass through LDS, where the waves' columns become whole
+  // rows: stored from the registers, 16 neighbouring lanes would write 16 bytes
+  // of 16 rows.  They are stored at the next chunk's start, together with the
+  // loads of the chunk after it, so that both have a chunk's time before the
+  // wait that ends it.
+  using TO = std::conditional_t<kF32Out, float, T>;
+  constexpr int kRowPieces = DV * (int)sizeof(TO) / 16, kSwz = kRowPieces < 16 ? 7 : 15;
+  __shared__ __attribute__((aligned(16))) char out0[kOut ? kC * DV * sizeof(TO) : 16];
+  __shared__ __attribute__((aligned(16))) char out1[kOut ? kC * DV * sizeof(TO) : 16];
+  const auto out_at = [&](int row, int piece) {
+    return (uint32_t)(row * kRowPieces + (piece ^ (row & kSwz))) * 16;
+  };
+  TO* op = static_cast<TO*>(a.out) + b * a.osb + h * a.osh;
+  const auto put = [&](int64_t t, int skip, const lds_char* tile) {
 #pragma unroll
-      for (int i = 0; i < KT; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[i][r] = fmaf(S[i][r], step_m1, S[i][r]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < KT; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[i][r] *= step;
+    for (int i = 0; i < kC * kRowPieces / kThreads; ++i) {
+      const int p = (int)threadIdx.x + i * kThreads, row = p / kRowPieces, piece = p % kRowPieces;
+      const u32x4_t x = lds_load<u32x4_t>(tile + out_at(row, piece));
+      const int c = piece * (16 / (int)sizeof(TO));
+      const int64_t tok = t + row - skip;
+      if (row >= skip && c < dv)
+        *reinterpret_cast<u32x4_t*>(op + (a.reverse ? n - 1 - tok : tok) * a.ost + c) = x;
     }
   };
-
-  // ---- token rows: token t of the walk is row t, or row n - 1 - t of the tensors
-  const T* kp = head_base<T>(a.k, b, h);
-  const T* vp = head_base<T>(a.v, b, h);
-  const T* qp = head_base<T>(a.q, b, h);
-  const int64_t dir = a.reverse ? -1 : 1;
-  Stage<T, DK, kThreads> stK, stQ;
-  Stage<T, DV, kThreads> stV;
-  const auto load = [&](int64_t t) {
-    // a last chunk of m < kC tokens fills the tile's last m rows, so that every
-    // weight above is the same as in a whole chunk
-    const int skip = (int)max((int64_t)0, kC - (t_hi - t));
-    const int64_t row = a.reverse ? n - 1 - t : t;
-    stK.load(kp + row * a.k.st, dir * a.k.st, skip, dk);
-    stV.load(vp + row * a.v.st, dir * a.v.st, skip, dv);
-    if constexpr (kOut) stQ.load(qp + row * a.q.st, dir * a.q.st, skip, dk);
-  };
-  if (t_lo < t_hi) load(t_lo);
-
-  for (int64_t t = t_lo; t < t_hi; t += kC) {
-    __syncthreads();  // every wave is done with the last chunk's tiles
-    stK.store(sK);
-    stV.store(sV);
-    if constexpr (kOut) stQ.store(sQ);
-    __syncthreads();
+  wait_vmcnt<0>();
+  lds_barrier();
+  const auto chunk = [&](int64_t t, const lds_char* sK, lds_char* other, lds_char* out,
+                         const lds_char* out_before) {
+    const lds_char* sV = sK + kOffV;
+    const lds_char* sQ = sK + kOffQ;
     const int m = (int)min((int64_t)kC, t_hi - t), skip = kC - m;
-    if (t + kC < t_hi) load(t + kC);
-    if (skip) {  // the last chunk
-      f_out = a.scale_o * decay_pow(lg2, max(0, qrow - skip) + a.late);
-      step_m1 = expm1f(a.log_decay[h] * (float)m);
-      step = decay_pow(lg2, m);
-    }
-    Frag<T> vf[2];  // V^T: value column col, tokens
-#pragma unroll
-    for (int s = 0; s < 2; ++s) vf[s] = Frag<T>::cols(sV, 32 * wave, s, lane);
-
     if constexpr (kOut) {
-      floatx16_t P, O;
+      if (t > t_lo) put(t - kC, 0, out_before);
+    }
+    if (t + kC < t_hi) issue(t + kC, other);
+    if (skip) f_out = a.scale_o * decay_pow(lg2, max(0, qrow - skip) + a.late);  // the last chunk
+    // Fragments are read from LDS ahead of the products that use them, and
+    // products that follow each other go to different accumulators; the
+    // scheduling barriers keep that order.
+    Frag<T> vf[2];  // V^T: value column col, tokens
+    Frag<T>::cols2(vf, sV, 32 * wave, lane);
+    floatx16_t P, O;
+    Frag<T> kc[KT];  // K^T: key rows of tile i, 16 tokens
+    if constexpr (kOut) {
+      constexpr int kSteps = DK / 16, kAhead = sizeof(T) == 2 ? 2 : 1;
+      Frag<T> qf[kAhead + 1], kf[kAhead + 1];
+      const auto read = [&](int s) {
+        qf[s % (kAhead + 1)] = Frag<T>::rows(sQ, qrow, s, lane);
+        kf[s % (kAhead + 1)] = Frag<T>::rows(sK, perm16(qrow), s, lane);
+      };
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) read(s);
 #pragma unroll
       for (int r = 0; r < 16; ++r) P[r] = O[r] = 0.0f;
 #pragma unroll
-      for (int s = 0; s < DK / 16; ++s) {
-        const Frag<T> qf = Frag<T>::rows(sQ, qrow, s, lane);
-        const Frag<T> kf = Frag<T>::rows(sK, perm16(qrow), s, lane);
-        mma(P, kf, qf);
-        mma(O, Frag<T>::result(S[s >> 1], s & 1), qf);
+      for (int s = 0; s < kSteps; ++s) {
+        if (s + kAhead < kSteps) read(s + kAhead);
+        const Frag<T> sf = Frag<T>::result(S[s >> 1], s & 1);
+        __builtin_amdgcn_sched_barrier(0);
+        mma(P, kf[s % (kAhead + 1)], qf[s % (kAhead + 1)]);
+        mma(O, sf, qf[s % (kAhead + 1)]);
       }
+    }
+    Frag<T>::template cols_all<0>(kc, sK, lane);
+    __builtin_amdgcn_sched_barrier(0);
+
+    // ---- S <- g^m S + K^T (w V)
+    const float step = skip ? decay_pow(lg2, m) : err < 0.0f ? step_hi : step_lo;
+    err += err < 0.0f ? err_hi : err_lo;
+    Frag<T> wv[2][3];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) weighted(wv[s], vf[s], w_up + 8 * s);
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) S[i][r] *= step;
+    __builtin_amdgcn_sched_barrier(0);
+    const auto update = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < KT; ++i) mma(S[i], kc[i], wv[s][0]);
+      if constexpr (kSplit) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) mma(S[i], kc[i], wv[s][1]);
+        if (a.exact_state) {
+#pragma unroll
+          for (int i = 0; i < KT; ++i) mma(S[i], kc[i], wv[s][2]);
+        }
+      }
+    };
+    update(0);
+    Frag<T>::template cols_all<1>(kc, sK, lane);
+    if constexpr (kOut) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         O[r] *= f_out;
-        P[r] = qrow >= 16 * (r >> 3) + 8 * half + (r & 7) ? P[r] * d_in[r] : 0.0f;
+        float p = qrow >= 16 * (r >> 3) + 8 * half + (r & 7) ? P[r] * d_in[r] : 0.0f;
+        asm("" : "+v"(p));  // selected, then converted in pairs
+        P[r] = p;
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s) mma(O, vf[s], Frag<T>::result(P, s));
-      // registers 8 i .. of O: columns 32 wave + 16 i + 8 half .. of the lane's token
-      const int64_t tok = t + qrow - skip;
-      if (qrow >= skip) {
-        const int64_t row = a.reverse ? n - 1 - tok : tok;
-        const int64_t at = b * a.osb + row * a.ost + h * a.osh;
+    }
+    update(1);
+
+    if constexpr (kOut) {
+      // registers 8 i .. of the result: the lane's token, columns 32 wave + 16 i + 8 half ..
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = 32 * wave + 16 * i + 8 * half;
-          float f[8];
+      for (int i = 0; i < 2; ++i) {
+        const int piece = (32 * wave + 16 * i + 8 * half) * (int)sizeof(TO) / 16;
+        if constexpr (sizeof(TO) == 2) {
+          lds_store<u32x4_t>(out + out_at(qrow, piece),
+                             u32x4_t{cvt_bf16x2(O[8 * i], O[8 * i + 1]),
+                                     cvt_bf16x2(O[8 * i + 2], O[8 * i + 3]),
+                                     cvt_bf16x2(O[8 * i + 4], O[8 * i + 5]),
+                                     cvt_bf16x2(O[8 * i + 6], O[8 * i + 7])});
+        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = O[8 * i + e];
-          if (c < dv) {
-            if (a.out_f32)
-              store8(static_cast<float*>(a.out) + at + c, f);
-            else
-              store8(static_cast<T*>(a.out) + at + c, f);
-          }
+          for (int q = 0; q < 2; ++q)
+            lds_store<floatx4_t>(out + out_at(qrow, piece + q),
+                                 floatx4_t{O[8 * i + 4 * q], O[8 * i + 4 * q + 1],
+                                           O[8 * i + 4 * q + 2], O[8 * i + 4 * q + 3]});
         }
       }
     }
-
-    // ---- S <- g^m S + K^T (w V)
-    decay_state();
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      Frag<T> hi, lo;
-      weighted(&hi, &lo, vf[s], w8, w_base[s]);
-#pragma unroll
-      for (int i = 0; i < KT; ++i) {
-        const Frag<T> kf = Frag<T>::cols(sK, 32 * i, s, lane);
-        mma(S[i], kf, hi);
-        if constexpr (kSplit) mma(S[i], kf, lo);
-      }
+    wait_vmcnt<0>();  // the next chunk's tiles are here, the last one's outputs gone
+    lds_barrier();
+  };
+  for (int64_t t = t_lo; t < t_hi; t += 2 * kC) {
+    chunk(t, (const lds_char*)smem0, (lds_char*)smem1, (lds_char*)out0, (const lds_char*)out1);
+    if (t + kC < t_hi)
+      chunk(t + kC, (const lds_char*)smem1, (lds_char*)smem0, (lds_char*)out1,
+            (const lds_char*)out0);
+  }
+  if constexpr (kOut) {
+    if (t_lo < t_hi) {
+      const int chunks = (int)((t_hi - t_lo + kC - 1) / kC);
+      const int64_t t = t_lo + (int64_t)(chunks - 1) * kC;
+      put(t, (int)(kC - (t_hi - t)), (const lds_char*)(chunks & 1 ? out0 : out1));
     }
   }
 
   if constexpr (!kOut) {
-    float* next = slot + slot_size;
-#pragma unroll
-    for (int i = 0; i < KT; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) next[(i * 16 + r) * 64] = S[i][r];
+    to_slot(g + 1);
   } else {
     const bool last = t_hi == n && (t_lo < n || g == 0);  // this segment holds the last token
     if (last && a.s_out) {
@@ -424,8 +651,9 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
     const int pieces = dv >> 3;
     const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int64_t p = threadIdx.x; p < (z_hi - z_lo) * pieces; p += kThreads) {
-      const int64_t at = b * a.osb + (z_lo + p / pieces) * a.ost + h * a.osh + (p % pieces) * 8;
-      if (a.out_f32)
+      const int64_t at =
+          b * a.osb + (z_lo + p / pieces) * a.ost + h * a.osh + (p % pieces) * 8;
+      if constexpr (kF32Out)
         store8(static_cast<float*>(a.out) + at, zero);
       else
         store8(static_cast<T*>(a.out) + at, zero);
@@ -433,7 +661,7 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
   }
 }
 
-// seg[bh][g] <- seg[bh][g] + g^seg_len seg[bh][g - 1] along the segments, so
+// seg[head][g] <- seg[head][g] + g^seg_len seg[head][g - 1] along the segments, so
 // that every slot is the state its segment starts from.  Slots of segments
 // behind a sequence's end are not used.
 __global__ __launch_bounds__(256) void linattn_scan_kernel(float4* seg,
@@ -442,9 +670,9 @@ __global__ __launch_bounds__(256) void linattn_scan_kernel(float4* seg,
                                                            int64_t seg_len, int nseg) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= total) return;
-  const int64_t bh = i / slot4, e = i % slot4;
-  const float f = exp2f(log_decay[bh % H] * kLog2e * (float)seg_len);
-  float4* p = seg + bh * nseg * slot4 + e;
+  const int64_t head = i / slot4, e = i % slot4;
+  const float f = exp2f(log2_decay(log_decay[head % H]) * (float)seg_len);
+  float4* p = seg + head * nseg * slot4 + e;
   float4 acc = p[slot4];
 #pragma unroll 4
   for (int g = 2; g < nseg; ++g) {
@@ -553,62 +781,76 @@ __global__ __launch_bounds__(256) void linattn_sum_heads_kernel(
   store8(out + b * osb + t * ost + g * osh + c, f);
 }
 
+int64_t padded(int64_t d) { return d <= 64 ? 64 : 128; }
+
+// How a pass splits sequences into segments of whole chunks: into as many as
+// have their workgroups resident together (two waves a SIMD on 256 CUs), of two
+// chunks at least.  Twice as many segments cost more in states than they gain
+// (backward over 32768 tokens, 20 heads of 128: 629 us with 2048 waves, 716 us
+// with 4096); one segment of 128 tokens at least leaves small calls slower (4
+// heads, 1024 tokens, fp32: 29 us, 37 us).
+constexpr int64_t kResidentWaves = 2048, kMinSegment = 64;
+struct Split {
+  int64_t seg_len;
+  int nseg;
+};
+
+Split split(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
+  const int64_t heads = B * H, waves = std::max(padded(dk), padded(dv)) / 32;
+    int64_t nseg = std::max<int64_t>(1, std::min<int64_t>(kResidentWaves / waves / heads, T / kMinSegment));
+  // whole chunks per segment may need fewer segments
+  Split p;
+  p.seg_len = ((T + nseg - 1) / nseg + kC - 1) / kC * kC;
+  p.nseg = (int)((T + p.seg_len - 1) / p.seg_len);
+  return p;
+}
+
 template <typename T, int DK, int NW>
-hipError_t chunked(const LinArgs& a, float* seg, int64_t seg_len, int nseg, hipStream_t s) {
+hipError_t chunked(const LinArgs& a, float4* seg, const Split& p, hipStream_t s) {
   const int64_t heads = a.B * a.H;
-  if (nseg > 1) {
+  if (p.nseg > 1 && !a.seg_trans) {
     linattn_chunked_kernel<T, DK, NW, false>
-        <<<dim3((unsigned)(heads * (nseg - 1))), 64 * NW, 0, s>>>(a, seg, seg_len, nseg);
+        <<<dim3((unsigned)(heads * (p.nseg - 1))), 64 * NW, 0, s>>>(a, seg, p.seg_len, p.nseg);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (nseg > 2) {
+    if (p.nseg > kScanInPlace) {
       const int64_t slot4 = DK * 32 * NW / 4, total = heads * slot4;
       linattn_scan_kernel<<<dim3((unsigned)((total + 255) / 256)), 256, 0, s>>>(
-          reinterpret_cast<float4*>(seg), a.log_decay, a.H, slot4, total, seg_len, nseg);
+          seg, a.log_decay, a.H, slot4, total, p.seg_len, p.nseg);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
   }
-  linattn_chunked_kernel<T, DK, NW, true><<<dim3((unsigned)(heads * nseg)), 64 * NW, 0, s>>>(
-      a, nseg > 1 ? seg : nullptr, seg_len, nseg);
+  const dim3 grid((unsigned)(heads * p.nseg));
+  float4* start = p.nseg > 1 ? seg : nullptr;
+  if (a.out_f32 && sizeof(T) == 2)
+    linattn_chunked_kernel<T, DK, NW, true, true>
+        <<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
+  else
+    linattn_chunked_kernel<T, DK, NW, true><<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t chunked_shape(const LinArgs& a, float* seg, int64_t seg_len, int nseg, hipStream_t s) {
+hipError_t chunked_shape(const LinArgs& a, float4* seg, hipStream_t s) {
+  const Split p = split(a.B, a.H, a.T, a.dk, a.dv);
   if (a.dk <= 64)
-    return a.dv <= 64 ? chunked<T, 64, 2>(a, seg, seg_len, nseg, s)
-                      : chunked<T, 64, 4>(a, seg, seg_len, nseg, s);
-  return a.dv <= 64 ? chunked<T, 128, 2>(a, seg, seg_len, nseg, s)
-                    : chunked<T, 128, 4>(a, seg, seg_len, nseg, s);
-}
-
-int64_t segment_tokens(int64_t T, int64_t nseg) {
-  return (((T + nseg - 1) / nseg) + kC - 1) / kC * kC;
+    return a.dv <= 64 ? chunked<T, 64, 2>(a, seg, p, s) : chunked<T, 64, 4>(a, seg, p, s);
+  return a.dv <= 64 ? chunked<T, 128, 2>(a, seg, p, s) : chunked<T, 128, 4>(a, seg, p, s);
 }
 
 }  // namespace
 
-int64_t linattn_segments(int64_t B, int64_t H, int64_t T) {
-  const int64_t heads = B * H;
-  int64_t nseg = std::min<int64_t>((512 + heads - 1) / heads, T / 256);
-  if (heads >= 256 || nseg <= 1) return 1;
-  // whole chunks per segment may need fewer segments
-  const int64_t len = segment_tokens(T, nseg);
-  return (T + len - 1) / len;
-}
-
 size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
-  const int64_t nseg = linattn_segments(B, H, T);
-  if (nseg == 1) return 0;
-  return (size_t)(B * H * nseg) * (dk <= 64 ? 64 : 128) * (dv <= 64 ? 64 : 128) * sizeof(float);
+  const Split p = split(B, H, T, dk, dv);
+  if (p.nseg == 1) return 0;
+  return (size_t)(B * H * p.nseg) * padded(dk) * padded(dv) * sizeof(float);
 }
 
 hipError_t launch_linattn_chunked(const LinArgs& a, float* seg, hipStream_t s) {
-  const int64_t nseg = linattn_segments(a.B, a.H, a.T);
-  const int64_t seg_len = segment_tokens(a.T, nseg);
-  return a.dt == Dtype::BF16 ? chunked_shape<uint16_t>(a, seg, seg_len, (int)nseg, s)
-                             : chunked_shape<float>(a, seg, seg_len, (int)nseg, s);
+  float4* slots = reinterpret_cast<float4*>(seg);
+  return a.dt == Dtype::BF16 ? chunked_shape<uint16_t>(a, slots, s)
+                             : chunked_shape<float>(a, slots, s);
 }
 
 hipError_t launch_linattn_step(const LinArgs& a, hipStream_t s) {

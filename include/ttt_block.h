@@ -109,7 +109,7 @@ ttt_status_t ttt_addnorm_backward(const ttt_addnorm_desc_t* desc, const void* dy
  *   scale     finite
  *   q_stride, k_stride, v_stride, o_stride  values between sequences, tokens
  *             and heads of q, k, v and o ({batch, token, head}), multiples of 8
- *             and >= 0, so that slices of one projection's output can be
+ *             and >= 0, token strides of q, k, v and dO at most 2^27 bytes, so that slices of one projection's output can be
  *             passed as they are; a head's d values are contiguous.  A stride
  *             of 0 in q, k, v or dO repeats a value; o must have no two elements
  *             at one place.  dO has the strides of o; dq, dk and dv are contiguous
@@ -151,9 +151,8 @@ ttt_status_t ttt_linattn_backward_workspace_size(const ttt_linattn_desc_t* desc,
  * Tokens of up to 8 per call run in the recurrent form (state read and
  * written once, all arithmetic in fp32), longer calls in the chunked form on
  * the matrix cores: bf16 products with fp32 accumulation, in which the decayed
- * scores and the state's copy that meets q are rounded to bf16 and the state's
- * own update is carried in two bf16 terms (relative error about 1e-6); fp32
- * inputs use fp32 products throughout. */
+ * scores and the state's copy that meets q are rounded to bf16 while the state
+ * itself is exact to fp32 sums; fp32 inputs use fp32 products throughout. */
 ttt_status_t ttt_linattn_forward(const ttt_linattn_desc_t* desc, const void* q, const void* k,
                                  const void* v, const float* log_decay, const int32_t* lengths,
                                  const float* state_in, float* state_out, void* o, void* ws,

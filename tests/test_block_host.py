@@ -157,6 +157,8 @@ BAD_ATTN = [
     (dict(k_stride=(4096, 100, 64)), UNSUPPORTED, "multiples of 8"),
     (dict(v_stride=(1 << 41, 128, 64)), UNSUPPORTED, "2^40"),
     (dict(seq_len=1 << 20, k_stride=(0, 1 << 40, 64)), UNSUPPORTED, "2^56"),
+    (dict(q_stride=(64, (1 << 26) + 8, 64)), UNSUPPORTED, "2^27"),
+    (dict(dtype=torch.float32, v_stride=(64, (1 << 25) + 8, 64)), UNSUPPORTED, "2^27"),
     (dict(o_stride=(64 * 256, 256, 32)), INVALID, "one place"),
     (dict(o_stride=(0, 256, 64)), INVALID, "one place"),
     (dict(o_stride=(64 * 256, 128, 64)), INVALID, "one place"),
@@ -168,7 +170,7 @@ def test_attention_refuses_descriptors(kw, status, word):
     d = attn_desc(**kw)
     refused(lambda: block.ttt_linattn_forward(d, at(1), at(2), at(3), at(4), None, None, None,
                                               at(5), at(6), 1 << 29, 0), status, word)
-    if "o_stride" not in kw:
+    if word not in ("one place", "2^27"):
         refused(lambda: block.ttt_linattn_workspace_size(d), status, word)
 
 
