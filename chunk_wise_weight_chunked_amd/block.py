@@ -93,6 +93,13 @@ def _strided(t):
     return t.data_ptr()
 
 
+def _current(stream, like):
+    """The stream given, or the current one of the tensor's device as a raw handle."""
+    if stream is None and isinstance(like, torch.Tensor) and like.is_cuda:
+        return torch._C._cuda_getCurrentRawStream(like.get_device())
+    return _stream(stream)
+
+
 # ------------------------------------------------ residual addition and norm
 def make_addnorm_desc(rows, d, dtype, res_dtype=None, x_stride=None, y_stride=None, eps=NORM_EPS,
                       out=TTT_NORM_SAME, scale_group=0) -> ttt_addnorm_desc_t:
@@ -104,7 +111,7 @@ def make_addnorm_desc(rows, d, dtype, res_dtype=None, x_stride=None, y_stride=No
 
 def ttt_addnorm_forward(desc, x, res, w, r, y, y_scale=None, stream=None) -> None:
     _check(_load().ttt_addnorm_forward(ctypes.byref(desc), _strided(x), _ptr(res), _ptr(w),
-                                       _ptr(r), _strided(y), _ptr(y_scale), _stream(stream)))
+                                       _ptr(r), _strided(y), _ptr(y_scale), _current(stream, x)))
 
 
 def ttt_addnorm_backward_workspace_size(desc) -> int:
@@ -120,7 +127,7 @@ def ttt_addnorm_backward(desc, dy, r, w, dr_out, dr, dx, dw, ws=None, ws_bytes=N
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(_load().ttt_addnorm_backward(ctypes.byref(desc), _strided(dy), _ptr(r), _ptr(w),
                                         _ptr(dr_out), _ptr(dr), _strided(dx), _ptr(dw), _ptr(ws),
-                                        int(ws_bytes), _stream(stream)))
+                                        int(ws_bytes), _current(stream, dy)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -142,8 +149,9 @@ def _rows(t):
 
 
 def _same_device(like, *tensors):
+    where = like.get_device()
     for t in tensors:
-        if t is not None and t.device != like.device:
+        if t is not None and t.get_device() != where:
             raise ValueError(f"tensors on {like.device} and on {t.device}")
 
 
@@ -243,7 +251,7 @@ def ttt_linattn_forward(desc, q, k, v, log_decay, lengths, state_in, state_out, 
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(_load().ttt_linattn_forward(
         ctypes.byref(desc), _strided(q), _strided(k), _strided(v), _ptr(log_decay), _ptr(lengths),
-        _ptr(state_in), _ptr(state_out), _strided(o), _ptr(ws), int(ws_bytes), _stream(stream)))
+        _ptr(state_in), _ptr(state_out), _strided(o), _ptr(ws), int(ws_bytes), _current(stream, q)))
 
 
 def ttt_linattn_backward(desc, q, k, v, log_decay, lengths, state_in, dO, dstate_out, dq, dk, dv,
@@ -253,7 +261,7 @@ def ttt_linattn_backward(desc, q, k, v, log_decay, lengths, state_in, dO, dstate
     _check(_load().ttt_linattn_backward(
         ctypes.byref(desc), _strided(q), _strided(k), _strided(v), _ptr(log_decay), _ptr(lengths),
         _ptr(state_in), _strided(dO), _ptr(dstate_out), _ptr(dq), _ptr(dk), _ptr(dv),
-        _ptr(dstate_in), _ptr(ws), int(ws_bytes), _stream(stream)))
+        _ptr(dstate_in), _ptr(ws), int(ws_bytes), _current(stream, q)))
 
 
 @functools.lru_cache(maxsize=256)

@@ -98,8 +98,9 @@ ttt_status_t linattn_dims(const ttt_linattn_desc_t* d) {
     return fail(TTT_ERR_INVALID_ARGUMENT, "heads must be a multiple of kv_heads");
   if (d->heads > 65535 || d->batch > ((int64_t)1 << 24) / d->heads)
     return fail(TTT_ERR_UNSUPPORTED, "heads must be <= 65535 and batch * heads <= 2^24");
-  if (d->seq_len > INT32_MAX || d->seq_len > ((int64_t)1 << 34) / (d->batch * d->heads))
-    return fail(TTT_ERR_UNSUPPORTED, "seq_len must be < 2^31 and batch * heads * seq_len <= 2^34");
+  if (d->seq_len > ((int64_t)1 << 30) ||
+      d->seq_len > ((int64_t)1 << 34) / (d->batch * d->heads))
+    return fail(TTT_ERR_UNSUPPORTED, "seq_len must be <= 2^30 and batch * heads * seq_len <= 2^34");
   if (d->d_key < 1 || d->d_value < 1)
     return fail(TTT_ERR_INVALID_ARGUMENT, "d_key and d_value must be >= 1");
   if (d->d_key % 8 || d->d_value % 8 || d->d_key > ttt::kLinMaxHead || d->d_value > ttt::kLinMaxHead)

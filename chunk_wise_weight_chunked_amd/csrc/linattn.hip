@@ -234,30 +234,29 @@ __device__ __forceinline__ void mma(floatx16_t& c, const Frag<float>& a, const F
   for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[e], b.v[e], c, 0, 0, 0);
 }
 
-// w[e] v[e] as a sum of three bf16 terms, or in fp32.
-__device__ __forceinline__ void weighted(Frag<uint16_t> (&x3)[3], const Frag<uint16_t>& v,
-                                         const float* w) {
-  const u32x4_t in = __builtin_bit_cast(u32x4_t, v.v);
-  u32x4_t t[3];
+// Values 2 e and 2 e + 1 of a fragment, weighted, as a sum of kTerms bf16 terms
+// (or in fp32).
+template <int kTerms>
+__device__ __forceinline__ void weighted(Frag<uint16_t> (&out)[kTerms], const Frag<uint16_t>& v,
+                                         const float* w, int e) {
+  const uint32_t in = __builtin_bit_cast(u32x4_t, v.v)[e];
+  float x = __uint_as_float(in << 16) * w[2 * e];
+  float y = __uint_as_float(in & 0xffff0000u) * w[2 * e + 1];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float x = __uint_as_float(in[e] << 16) * w[2 * e];
-    float y = __uint_as_float(in[e] & 0xffff0000u) * w[2 * e + 1];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      uint32_t top = cvt_bf16x2(x, y);
-      asm("" : "+v"(top));  // one paired conversion: seen through, the halves are converted again
-      t[i][e] = top;
-      x -= __uint_as_float(top << 16);
-      y -= __uint_as_float(top & 0xffff0000u);
-    }
+  for (int i = 0; i < kTerms; ++i) {
+    uint32_t top = cvt_bf16x2(x, y);
+    asm("" : "+v"(top));  // one paired conversion: seen through, the halves are converted again
+    u32x4_t all = __builtin_bit_cast(u32x4_t, out[i].v);
+    all[e] = top;
+    out[i].v = __builtin_bit_cast(bf16x8_t, all);
+    x -= __uint_as_float(top << 16);
+    y -= __uint_as_float(top & 0xffff0000u);
   }
-#pragma unroll
-  for (int i = 0; i < 3; ++i) x3[i].v = __builtin_bit_cast(bf16x8_t, t[i]);
 }
-__device__ __forceinline__ void weighted(Frag<float> (&x3)[3], const Frag<float>& v, const float* w) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x3[0].v[e] = v.v[e] * w[e];
+__device__ __forceinline__ void weighted(Frag<float> (&out)[1], const Frag<float>& v,
+                                         const float* w, int e) {
+  out[0].v[2 * e] = v.v[2 * e] * w[2 * e];
+  out[0].v[2 * e + 1] = v.v[2 * e + 1] * w[2 * e + 1];
 }
 
 // 8 results in a row, to the operands' type or fp32.
@@ -310,19 +309,25 @@ struct Loader {
   __device__ __forceinline__ static int panel_of(int q, int wave) {
     return (wave * kPer + q) / (kC / 8);
   }
-  // The next chunk into `tile`; its tokens are the tile's last kC - skip rows.
-  // shift: bytes from `base` to the first of these rows' place.
-  __device__ __forceinline__ void issue(lds_char* tile, int skip, int64_t shift, int wave) {
-    const rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base + shift), (short)0,
+  __device__ __forceinline__ void move(lds_char* tile, const char* from, int q, uint32_t o,
+                                       int wave) const {
+    const rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), (short)0,
                                                        (int)kRange, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r, (__attribute__((address_space(3))) void*)(tile + (wave * kPer + q) * 8 * kRowBytes), 16,
+        o, 0, 0, 0);
+  }
+  __device__ __forceinline__ void issue(lds_char* tile, int wave) {  // a whole chunk
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      const uint32_t o = row_of(q, wave) >= skip ? off[q] : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          r, (__attribute__((address_space(3))) void*)(tile + (wave * kPer + q) * 8 * kRowBytes), 16,
-          o, 0, 0, 0);
-    }
+    for (int q = 0; q < kPer; ++q) move(tile, base, q, off[q], wave);
     base += chunk_bytes;
+  }
+  // A last chunk, whose tokens are the tile's last kC - skip rows.
+  __device__ __forceinline__ void issue_last(lds_char* tile, int skip, int wave) {
+    const char* from = base - chunk_bytes / kC * skip;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q)
+      move(tile, from, q, row_of(q, wave) >= skip ? off[q] : kOutside, wave);
   }
 };
 
@@ -331,10 +336,8 @@ __device__ __forceinline__ const T* head_base(const LinOperand& o, int64_t b, in
   return static_cast<const T*>(o.p) + b * o.sb + (h / o.rep) * o.sh;
 }
 
-__device__ __forceinline__ int64_t live_tokens(const int32_t* lengths, int64_t b, int64_t T) {
-  if (!lengths) return T;
-  const int64_t n = lengths[b];
-  return n < 0 ? 0 : n > T ? T : n;
+__device__ __forceinline__ int live_tokens(const int32_t* lengths, int64_t b, int64_t T) {
+  return lengths ? max(0, min(lengths[b], (int)T)) : (int)T;
 }
 
 // Up to so many segments the main pass adds their ends up itself.
@@ -345,30 +348,27 @@ constexpr int kScanInPlace = 8;
 // end state in `seg`, which holds a start state per segment: slot g + 1 gets
 // segment g's end, slot 0 the state the sequence starts from (the main pass
 // reads it from there, since s_out may be s_in).
-template <typename T, int DK, int NW, bool kOut, bool kF32Out = false>
+template <typename T, int DK, int NW, bool kOut, int kTerms, bool kF32Out = false>
 __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, float4* seg,
-                                                                     int64_t seg_len, int nseg) {
+                                                                     int seg_len, int nseg) {
   constexpr int kThreads = 64 * NW, DV = 32 * NW, KT = DK / 32;
-  constexpr bool kSplit = sizeof(T) == 2;
   constexpr int kOffV = kC * DK * sizeof(T), kOffQ = kOffV + kC * DV * sizeof(T);
   constexpr int kBuf = kOffQ + (kOut ? kC * DK * (int)sizeof(T) : 0);
-  // Two buffers, two objects: reads of one are seen not to depend on the loads
-  // that are filling the other.
-  __shared__ __attribute__((aligned(16))) char smem0[kBuf], smem1[kBuf];
+  __shared__ __attribute__((aligned(16))) char smem[2 * kBuf];
 
   const int per = kOut ? nseg : nseg - 1;  // nobody starts from the last segment's end
   const int g = (int)(blockIdx.x % per);
   const int64_t bh = blockIdx.x / per, b = bh / a.H, h = bh % a.H;
-  const int64_t n = live_tokens(a.lengths, b, a.T);
+  const int n = live_tokens(a.lengths, b, a.T);
   const float lg = a.log_decay[h];
-  int64_t t_lo = g * seg_len;
-  const int64_t t_hi = min(t_lo + seg_len, n);
+  int t_lo = g * seg_len;
+  const int t_hi = min(t_lo + seg_len, n);
   if constexpr (!kOut) {
     // tokens whose decay to the segment's end is 0 in fp32 (below 2^-150) do
     // not reach the state there
     const float reach = -104.0f / lg;
     if (lg < 0.0f && reach < (float)(t_hi - t_lo))
-      t_lo = max(t_lo, t_hi - ((int64_t)reach / kC + 1) * kC);
+      t_lo = max(t_lo, t_hi - ((int)reach / kC + 1) * kC);
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
   const int dk = (int)a.dk, dv = (int)a.dv;
@@ -383,16 +383,21 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
   ldK.init(kp + row0 * a.k.st, a.k.st, a.reverse, dk, uwave, lane);
   ldV.init(vp + row0 * a.v.st, a.v.st, a.reverse, dv, uwave, lane);
   if constexpr (kOut) ldQ.init(qp + row0 * a.q.st, a.q.st, a.reverse, dk, uwave, lane);
-  const auto issue = [&](int64_t t, lds_char* tiles_of) {
+  const auto issue = [&](int t, lds_char* tiles_of) {
     // a last chunk of m < kC tokens fills the tiles' last m rows, so that every
-    // weight above is the same as in a whole chunk
-    const int skip = (int)max((int64_t)0, kC - (t_hi - t));
-    const int64_t back = (a.reverse ? skip : -skip) * (int64_t)sizeof(T);
-    ldK.issue(tiles_of, skip, back * a.k.st, uwave);
-    ldV.issue(tiles_of + kOffV, skip, back * a.v.st, uwave);
-    if constexpr (kOut) ldQ.issue(tiles_of + kOffQ, skip, back * a.q.st, uwave);
+    // weight below is the same as in a whole chunk
+    const int skip = kC - (t_hi - t);
+    if (skip <= 0) {
+      ldK.issue(tiles_of, uwave);
+      ldV.issue(tiles_of + kOffV, uwave);
+      if constexpr (kOut) ldQ.issue(tiles_of + kOffQ, uwave);
+    } else {
+      ldK.issue_last(tiles_of, skip, uwave);
+      ldV.issue_last(tiles_of + kOffV, skip, uwave);
+      if constexpr (kOut) ldQ.issue_last(tiles_of + kOffQ, skip, uwave);
+    }
   };
-  if (t_lo < t_hi) issue(t_lo, (lds_char*)smem0);  // on its way while the rest is set up
+  if (t_lo < t_hi) issue(t_lo, (lds_char*)smem);  // on its way while the rest is set up
 
   // a slot of the workspace: register 4 r.. of tile i of wave w at float4
   // ((w KT + i) 4 + r) 64 + lane
@@ -403,11 +408,11 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
   // + r % 8 of value column 32 wave + perm16(lane % 32)
   const int col = 32 * wave + perm16(lane & 31);
   floatx16_t S[KT];
-  const auto state_at = [&](int i, int r) -> int64_t {
-    const int row = 32 * i + 16 * (r >> 3) + 8 * half + (r & 7);
-    if (row >= dk || col >= dv) return -1;
-    return bh * dk * dv + (a.s_trans ? (int64_t)col * dk + row : (int64_t)row * dv + col);
-  };
+  const int rs = a.s_trans ? 1 : dv, cs = a.s_trans ? dk : 1;  // steps of a key row, a value column
+  const int64_t head_state = bh * dk * dv;
+  const auto state_row = [&](int i, int r) { return 32 * i + 16 * (r >> 3) + 8 * half + (r & 7); };
+  const int at0 = 8 * half * rs + col * cs;
+  const auto state_off = [&](int i, int r) { return at0 + (32 * i + 16 * (r >> 3) + (r & 7)) * rs; };
   const auto from_slot = [&](int64_t j, float f) {  // S = f S + slot j
     const float4* p = slot + j * slot4;
     if (a.seg_trans) {
@@ -452,17 +457,15 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
     if (t_lo < n || g == 0) {
       // few segments: their ends are added up here, otherwise by linattn_scan_kernel
       const float f = exp2f(log2_decay(lg) * (float)seg_len);
-      if (nseg <= kScanInPlace)
-        for (int j = min(g, 1); j < g; ++j) from_slot(j, f);
-      from_slot(g, nseg <= kScanInPlace ? f : 0.0f);
+      const int first = nseg <= kScanInPlace ? min(g, 1) : g;
+      for (int j = first; j <= g; ++j) from_slot(j, j == first ? 0.0f : f);
     }
   } else if (g == 0 && a.s_in) {
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int64_t at = state_at(i, r);
-        if (at >= 0) S[i][r] = a.s_in[at];
+        if (state_row(i, r) < dk && col < dv) S[i][r] = a.s_in[head_state + state_off(i, r)];
       }
   }
   if (!kOut && g == 0) to_slot(0);
@@ -499,88 +502,95 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
   // wait that ends it.
   using TO = std::conditional_t<kF32Out, float, T>;
   constexpr int kRowPieces = DV * (int)sizeof(TO) / 16, kSwz = kRowPieces < 16 ? 7 : 15;
-  __shared__ __attribute__((aligned(16))) char out0[kOut ? kC * DV * sizeof(TO) : 16];
-  __shared__ __attribute__((aligned(16))) char out1[kOut ? kC * DV * sizeof(TO) : 16];
+  constexpr int kOutB = kOut ? kC * DV * sizeof(TO) : 16;
+  __shared__ __attribute__((aligned(16))) char out_smem[2 * kOutB];
   const auto out_at = [&](int row, int piece) {
     return (uint32_t)(row * kRowPieces + (piece ^ (row & kSwz))) * 16;
   };
-  TO* op = static_cast<TO*>(a.out) + b * a.osb + h * a.osh;
-  const auto put = [&](int64_t t, int skip, const lds_char* tile) {
+  constexpr int kPutRows = kThreads / kRowPieces;  // rows of a store instruction
+  const int put_row = (int)threadIdx.x / kRowPieces, put_piece = (int)threadIdx.x % kRowPieces;
+  const bool put_col = put_piece * (16 / (int)sizeof(TO)) < dv;
+  const int64_t put_step = a.reverse ? -a.ost : a.ost;  // values to the next token of the walk
+  TO* op = static_cast<TO*>(a.out) + b * a.osb + h * a.osh + row0 * a.ost + put_row * put_step +
+           put_piece * (16 / (int)sizeof(TO));
+  const auto put = [&](int skip, const lds_char* tile) {  // and on to the next chunk
 #pragma unroll
-    for (int i = 0; i < kC * kRowPieces / kThreads; ++i) {
-      const int p = (int)threadIdx.x + i * kThreads, row = p / kRowPieces, piece = p % kRowPieces;
-      const u32x4_t x = lds_load<u32x4_t>(tile + out_at(row, piece));
-      const int c = piece * (16 / (int)sizeof(TO));
-      const int64_t tok = t + row - skip;
-      if (row >= skip && c < dv)
-        *reinterpret_cast<u32x4_t*>(op + (a.reverse ? n - 1 - tok : tok) * a.ost + c) = x;
+    for (int i = 0; i < kC / kPutRows; ++i) {
+      const int row = put_row + i * kPutRows;
+      const u32x4_t x = lds_load<u32x4_t>(tile + out_at(row, put_piece));
+      if (put_col && row >= skip)
+        *reinterpret_cast<u32x4_t*>(op + (i * kPutRows - skip) * put_step) = x;
     }
+    op += kC * put_step;
   };
   wait_vmcnt<0>();
   lds_barrier();
-  const auto chunk = [&](int64_t t, const lds_char* sK, lds_char* other, lds_char* out,
+  const auto chunk = [&](int t, const lds_char* sK, lds_char* other, lds_char* out,
                          const lds_char* out_before) {
     const lds_char* sV = sK + kOffV;
     const lds_char* sQ = sK + kOffQ;
-    const int m = (int)min((int64_t)kC, t_hi - t), skip = kC - m;
+    const int m = min(kC, t_hi - t), skip = kC - m;
     if constexpr (kOut) {
-      if (t > t_lo) put(t - kC, 0, out_before);
+      if (t > t_lo) put(0, out_before);
     }
     if (t + kC < t_hi) issue(t + kC, other);
     if (skip) f_out = a.scale_o * decay_pow(lg2, max(0, qrow - skip) + a.late);  // the last chunk
-    // Fragments are read from LDS ahead of the products that use them, and
-    // products that follow each other go to different accumulators; the
-    // scheduling barriers keep that order.
+    const float step = skip ? decay_pow(lg2, m) : err < 0.0f ? step_hi : step_lo;
+    err += err < 0.0f ? err_hi : err_lo;
+    const auto decay = [&](int i) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) S[i][r] *= step;
+    };
     Frag<T> vf[2];  // V^T: value column col, tokens
     Frag<T>::cols2(vf, sV, 32 * wave, lane);
+    Frag<T> wv[2][kTerms];  // the same weighted
+    const auto weigh = [&](int pair) { weighted(wv[pair >> 2], vf[pair >> 2], w_up + 8 * (pair >> 2), pair & 3); };
     floatx16_t P, O;
-    Frag<T> kc[KT];  // K^T: key rows of tile i, 16 tokens
     if constexpr (kOut) {
-      constexpr int kSteps = DK / 16, kAhead = sizeof(T) == 2 ? 2 : 1;
-      Frag<T> qf[kAhead + 1], kf[kAhead + 1];
+      // O = S^T Q^T and P^T = K Q^T.  A matrix instruction takes as long as eight
+      // vector instructions: the weighting of V, the state's conversion and its
+      // decay run beside the products.  Fragments are read from LDS ahead of
+      // their use, and products that follow each other go to different
+      // accumulators; the scheduling barriers keep this order.
+      constexpr int kSteps = DK / 16, kAhead = 1;
+      Frag<T> qf[2], kf[2], sf[2];
       const auto read = [&](int s) {
-        qf[s % (kAhead + 1)] = Frag<T>::rows(sQ, qrow, s, lane);
-        kf[s % (kAhead + 1)] = Frag<T>::rows(sK, perm16(qrow), s, lane);
+        qf[s & 1] = Frag<T>::rows(sQ, qrow, s, lane);
+        kf[s & 1] = Frag<T>::rows(sK, perm16(qrow), s, lane);
       };
 #pragma unroll
       for (int s = 0; s < kAhead; ++s) read(s);
 #pragma unroll
       for (int r = 0; r < 16; ++r) P[r] = O[r] = 0.0f;
+      sf[0] = Frag<T>::result(S[0], 0);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        if (s + kAhead < kSteps) read(s + kAhead);
-        const Frag<T> sf = Frag<T>::result(S[s >> 1], s & 1);
         __builtin_amdgcn_sched_barrier(0);
-        mma(P, kf[s % (kAhead + 1)], qf[s % (kAhead + 1)]);
-        mma(O, sf, qf[s % (kAhead + 1)]);
+        if (s + kAhead < kSteps) read(s + kAhead);
+        mma(P, kf[s & 1], qf[s & 1]);
+        mma(O, sf[s & 1], qf[s & 1]);
+        if (s + 1 < kSteps) sf[(s + 1) & 1] = Frag<T>::result(S[(s + 1) >> 1], (s + 1) & 1);
+#pragma unroll
+        for (int p = 8 * s / kSteps; p < 8 * (s + 1) / kSteps; ++p) weigh(p);
+        if (s & 1) decay(s >> 1);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+#pragma unroll
+      for (int p = 0; p < 8; ++p) weigh(p);
+#pragma unroll
+      for (int i = 0; i < KT; ++i) decay(i);
     }
-    Frag<T>::template cols_all<0>(kc, sK, lane);
-    __builtin_amdgcn_sched_barrier(0);
 
-    // ---- S <- g^m S + K^T (w V)
-    const float step = skip ? decay_pow(lg2, m) : err < 0.0f ? step_hi : step_lo;
-    err += err < 0.0f ? err_hi : err_lo;
-    Frag<T> wv[2][3];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) weighted(wv[s], vf[s], w_up + 8 * s);
-#pragma unroll
-    for (int i = 0; i < KT; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) S[i][r] *= step;
-    __builtin_amdgcn_sched_barrier(0);
+    // ---- S <- g^m S + K^T (w V), and O <- f O + V^T P^T
+    Frag<T> kc[KT];  // K^T: key rows of tile i, 16 tokens
     const auto update = [&](int s) {
 #pragma unroll
-      for (int i = 0; i < KT; ++i) mma(S[i], kc[i], wv[s][0]);
-      if constexpr (kSplit) {
+      for (int j = 0; j < kTerms; ++j)
 #pragma unroll
-        for (int i = 0; i < KT; ++i) mma(S[i], kc[i], wv[s][1]);
-        if (a.exact_state) {
-#pragma unroll
-          for (int i = 0; i < KT; ++i) mma(S[i], kc[i], wv[s][2]);
-        }
-      }
+        for (int i = 0; i < KT; ++i) mma(S[i], kc[i], wv[s][j]);
     };
+    Frag<T>::template cols_all<0>(kc, sK, lane);
     update(0);
     Frag<T>::template cols_all<1>(kc, sK, lane);
     if constexpr (kOut) {
@@ -619,18 +629,13 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
     wait_vmcnt<0>();  // the next chunk's tiles are here, the last one's outputs gone
     lds_barrier();
   };
-  for (int64_t t = t_lo; t < t_hi; t += 2 * kC) {
-    chunk(t, (const lds_char*)smem0, (lds_char*)smem1, (lds_char*)out0, (const lds_char*)out1);
-    if (t + kC < t_hi)
-      chunk(t + kC, (const lds_char*)smem1, (lds_char*)smem0, (lds_char*)out1,
-            (const lds_char*)out0);
-  }
+  int buf = 0;
+  for (int t = t_lo; t < t_hi; t += kC, buf ^= 1)
+    chunk(t, (const lds_char*)smem + buf * kBuf, (lds_char*)smem + (buf ^ 1) * kBuf,
+          (lds_char*)out_smem + buf * kOutB, (const lds_char*)out_smem + (buf ^ 1) * kOutB);
   if constexpr (kOut) {
-    if (t_lo < t_hi) {
-      const int chunks = (int)((t_hi - t_lo + kC - 1) / kC);
-      const int64_t t = t_lo + (int64_t)(chunks - 1) * kC;
-      put(t, (int)(kC - (t_hi - t)), (const lds_char*)(chunks & 1 ? out0 : out1));
-    }
+    if (t_lo < t_hi)
+      put((kC - (t_hi - t_lo) % kC) % kC, (const lds_char*)out_smem + (buf ^ 1) * kOutB);
   }
 
   if constexpr (!kOut) {
@@ -642,15 +647,15 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
       for (int i = 0; i < KT; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int64_t at = state_at(i, r);
-          if (at >= 0) a.s_out[at] = S[i][r];
+          if (state_row(i, r) < dk && col < dv)
+            a.s_out[head_state + state_off(i, r)] = S[i][r];
         }
     }
     // rows behind the sequence's end
-    const int64_t z_lo = max(t_lo, n), z_hi = min(t_lo + seg_len, a.T);
+    const int z_lo = max(t_lo, n), z_hi = min(t_lo + seg_len, (int)a.T);
     const int pieces = dv >> 3;
     const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int64_t p = threadIdx.x; p < (z_hi - z_lo) * pieces; p += kThreads) {
+    for (int64_t p = threadIdx.x; p < (int64_t)(z_hi - z_lo) * pieces; p += kThreads) {
       const int64_t at =
           b * a.osb + (z_lo + p / pieces) * a.ost + h * a.osh + (p % pieces) * 8;
       if constexpr (kF32Out)
@@ -664,22 +669,29 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
 // seg[head][g] <- seg[head][g] + g^seg_len seg[head][g - 1] along the segments, so
 // that every slot is the state its segment starts from.  Slots of segments
 // behind a sequence's end are not used.
-__global__ __launch_bounds__(256) void linattn_scan_kernel(float4* seg,
+__global__ __launch_bounds__(64) void linattn_scan_kernel(float4* seg,
                                                            const float* __restrict__ log_decay,
                                                            int64_t H, int64_t slot4, int64_t total,
-                                                           int64_t seg_len, int nseg) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+                                                           int seg_len, int nseg) {
+  const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x;
   if (i >= total) return;
   const int64_t head = i / slot4, e = i % slot4;
   const float f = exp2f(log2_decay(log_decay[head % H]) * (float)seg_len);
   float4* p = seg + head * nseg * slot4 + e;
   float4 acc = p[slot4];
-#pragma unroll 4
-  for (int g = 2; g < nseg; ++g) {
-    float4 x = p[g * slot4];
-    x.x = fmaf(f, acc.x, x.x), x.y = fmaf(f, acc.y, x.y);
-    x.z = fmaf(f, acc.z, x.z), x.w = fmaf(f, acc.w, x.w);
-    p[g * slot4] = acc = x;
+  constexpr int kBatch = 8;  // loads in flight
+  for (int g = 2; g < nseg; g += kBatch) {
+    float4 x[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (g + j < nseg) x[j] = p[(g + j) * slot4];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (g + j < nseg) {
+        acc.x = fmaf(f, acc.x, x[j].x), acc.y = fmaf(f, acc.y, x[j].y);
+        acc.z = fmaf(f, acc.z, x[j].z), acc.w = fmaf(f, acc.w, x[j].w);
+        p[(g + j) * slot4] = acc;
+      }
   }
 }
 
@@ -791,8 +803,7 @@ int64_t padded(int64_t d) { return d <= 64 ? 64 : 128; }
 // heads, 1024 tokens, fp32: 29 us, 37 us).
 constexpr int64_t kResidentWaves = 2048, kMinSegment = 64;
 struct Split {
-  int64_t seg_len;
-  int nseg;
+  int seg_len, nseg;
 };
 
 Split split(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
@@ -800,22 +811,22 @@ Split split(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
     int64_t nseg = std::max<int64_t>(1, std::min<int64_t>(kResidentWaves / waves / heads, T / kMinSegment));
   // whole chunks per segment may need fewer segments
   Split p;
-  p.seg_len = ((T + nseg - 1) / nseg + kC - 1) / kC * kC;
+  p.seg_len = (int)(((T + nseg - 1) / nseg + kC - 1) / kC * kC);
   p.nseg = (int)((T + p.seg_len - 1) / p.seg_len);
   return p;
 }
 
-template <typename T, int DK, int NW>
+template <typename T, int DK, int NW, int kTerms>
 hipError_t chunked(const LinArgs& a, float4* seg, const Split& p, hipStream_t s) {
   const int64_t heads = a.B * a.H;
   if (p.nseg > 1 && !a.seg_trans) {
-    linattn_chunked_kernel<T, DK, NW, false>
+    linattn_chunked_kernel<T, DK, NW, false, kTerms>
         <<<dim3((unsigned)(heads * (p.nseg - 1))), 64 * NW, 0, s>>>(a, seg, p.seg_len, p.nseg);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (p.nseg > kScanInPlace) {
       const int64_t slot4 = DK * 32 * NW / 4, total = heads * slot4;
-      linattn_scan_kernel<<<dim3((unsigned)((total + 255) / 256)), 256, 0, s>>>(
+      linattn_scan_kernel<<<dim3((unsigned)((total + 63) / 64)), 64, 0, s>>>(
           seg, a.log_decay, a.H, slot4, total, p.seg_len, p.nseg);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
@@ -824,19 +835,22 @@ hipError_t chunked(const LinArgs& a, float4* seg, const Split& p, hipStream_t s)
   const dim3 grid((unsigned)(heads * p.nseg));
   float4* start = p.nseg > 1 ? seg : nullptr;
   if (a.out_f32 && sizeof(T) == 2)
-    linattn_chunked_kernel<T, DK, NW, true, true>
+    linattn_chunked_kernel<T, DK, NW, true, kTerms, sizeof(T) == 2>
         <<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
   else
-    linattn_chunked_kernel<T, DK, NW, true><<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
+    linattn_chunked_kernel<T, DK, NW, true, kTerms>
+        <<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
   return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, int kTerms>
 hipError_t chunked_shape(const LinArgs& a, float4* seg, hipStream_t s) {
   const Split p = split(a.B, a.H, a.T, a.dk, a.dv);
   if (a.dk <= 64)
-    return a.dv <= 64 ? chunked<T, 64, 2>(a, seg, p, s) : chunked<T, 64, 4>(a, seg, p, s);
-  return a.dv <= 64 ? chunked<T, 128, 2>(a, seg, p, s) : chunked<T, 128, 4>(a, seg, p, s);
+    return a.dv <= 64 ? chunked<T, 64, 2, kTerms>(a, seg, p, s)
+                      : chunked<T, 64, 4, kTerms>(a, seg, p, s);
+  return a.dv <= 64 ? chunked<T, 128, 2, kTerms>(a, seg, p, s)
+                    : chunked<T, 128, 4, kTerms>(a, seg, p, s);
 }
 
 }  // namespace
@@ -849,8 +863,9 @@ size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_
 
 hipError_t launch_linattn_chunked(const LinArgs& a, float* seg, hipStream_t s) {
   float4* slots = reinterpret_cast<float4*>(seg);
-  return a.dt == Dtype::BF16 ? chunked_shape<uint16_t>(a, slots, s)
-                             : chunked_shape<float>(a, slots, s);
+  if (a.dt == Dtype::F32) return chunked_shape<float, 1>(a, slots, s);
+  return a.exact_state ? chunked_shape<uint16_t, 3>(a, slots, s)
+                       : chunked_shape<uint16_t, 2>(a, slots, s);
 }
 
 hipError_t launch_linattn_step(const LinArgs& a, hipStream_t s) {
