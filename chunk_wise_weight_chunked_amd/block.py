@@ -267,37 +267,37 @@ def ttt_linattn_backward(desc, q, k, v, log_decay, lengths, state_in, dO, dstate
 @functools.lru_cache(maxsize=256)
 def _linattn_plan(q, qs, k, ks, v, vs, os, dtype, scale, backward):
     """(descriptor, workspace bytes) of a call's shapes and strides."""
+    if len(q) != 4 or len(k) != 4 or len(v) != 4:
+        raise ValueError("q, k and v must be [B][T][heads][d]")
+    if k[:2] != q[:2] or v[:3] != k[:3] or k[3] != q[3]:
+        raise ValueError(f"shapes do not match: q {tuple(q)}, k {tuple(k)}, v {tuple(v)}")
+    if qs[3] != 1 or ks[3] != 1 or vs[3] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    if dtype not in _DTYPES:
+        raise ValueError("q, k and v must be of one type, bfloat16 or float32")
     # a dimension of one element has no stride to speak of (torch may give any)
     real = lambda shape, st: [0 if n == 1 else x for n, x in zip(shape, st[:3])]  # noqa: E731
-    desc = make_linattn_desc(q[0], q[1], q[2], k[2], q[3], v[3], dtype, scale, real(q, qs),
-                             real(k, ks), real(v, vs), None if os is None else real(q, os))
+    desc = make_linattn_desc(q[0], q[1], q[2], k[2], q[3], v[3], dtype,
+                             q[3] ** -0.5 if scale is None else scale, real(q, qs), real(k, ks),
+                             real(v, vs), None if os is None else real(q, os))
     size = ttt_linattn_backward_workspace_size if backward else ttt_linattn_workspace_size
     return desc, size(desc)
 
 
-def _linattn_checks(q, k, v, log_decay, state, lengths):
-    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
-        raise ValueError("q, k and v must be [B][T][heads][d]")
-    if q.dtype not in _DTYPES or k.dtype != q.dtype or v.dtype != q.dtype:
+def _linattn_checks(q, k, v, log_decay, lengths, *states):
+    """What the plan does not look at: types, devices, and the small and the fp32 tensors."""
+    if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must be of one type, bfloat16 or float32")
-    B, T, H, dk = q.shape
-    if k.shape[:2] != q.shape[:2] or v.shape[:3] != k.shape[:3] or k.shape[3] != dk:
-        raise ValueError(f"shapes do not match: q {tuple(q.shape)}, k {tuple(k.shape)}, "
-                         f"v {tuple(v.shape)}")
-    for t in (q, k, v):
-        if t.stride(3) != 1:
-            raise ValueError("the last dimension must be contiguous")
+    B, H = q.shape[0], q.shape[2]
     if log_decay.shape != (H,) or log_decay.dtype != torch.float32:
         raise ValueError(f"log_decay must be [{H}] float32")
     if lengths is not None and (lengths.shape != (B,) or lengths.dtype != torch.int32):
         raise ValueError(f"lengths must be [{B}] int32")
-    _state_check("state", state, B, H, dk, v.shape[3])
-    _same_device(q, k, v, log_decay, state, lengths)
-
-
-def _state_check(name, s, B, H, dk, dv):
-    if s is not None and (s.shape != (B, H, dk, dv) or s.dtype != torch.float32):
-        raise ValueError(f"{name} must be [{B}][{H}][{dk}][{dv}] float32")
+    for s in states:
+        if s is not None and (s.shape != (B, H, q.shape[3], v.shape[3])
+                              or s.dtype != torch.float32):
+            raise ValueError(f"states must be [{B}][{H}][{q.shape[3]}][{v.shape[3]}] float32")
+    _same_device(q, k, v, log_decay, lengths, *states)
 
 
 def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, lengths=None,
@@ -309,13 +309,11 @@ def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, 
     [B][H][dk][dv] fp32 or None (zeros), lengths [B] int32 or None.  scale: dk^-0.5 unless
     given.  Returns (o [B][T][H][dv], the state behind the last token); pass
     state_out=state to update a session's state in place."""
-    _linattn_checks(q, k, v, log_decay, state, lengths)
+    desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
+                               None, q.dtype, scale, False)
+    _linattn_checks(q, k, v, log_decay, lengths, state, state_out)
     B, T, H, dk = q.shape
     dv = v.shape[3]
-    _state_check("state_out", state_out, B, H, dk, dv)
-    _same_device(q, state_out, ws)
-    desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
-                               None, q.dtype, dk ** -0.5 if scale is None else scale, False)
     o = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
     if state_out is None:
         state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
@@ -330,16 +328,13 @@ def linattn_backward(q, k, v, log_decay, dO, scale=None, state=None, dstate_out=
     """Gradients of <dO, o> + <dstate_out, final state> for linattn_forward from `state`.
     Returns a dict: q, k, v (their shapes, contiguous) and state (fp32; None when no state was
     given)."""
-    _linattn_checks(q, k, v, log_decay, state, lengths)
-    B, T, H, dk = q.shape
-    dv = v.shape[3]
-    _state_check("dstate_out", dstate_out, B, H, dk, dv)
-    if dO.shape != (B, T, H, dv) or dO.dtype != q.dtype or dO.stride(3) != 1:
-        raise ValueError(f"dO must be [{B}][{T}][{H}][{dv}] of {q.dtype}, last dimension contiguous")
-    _same_device(q, dO, dstate_out, ws)
     desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
-                               dO.stride(), q.dtype, dk ** -0.5 if scale is None else scale,
-                               True)
+                               dO.stride(), q.dtype, scale, True)
+    _linattn_checks(q, k, v, log_decay, lengths, state, dstate_out)
+    want = (*q.shape[:3], v.shape[3])
+    if dO.shape != want or dO.dtype != q.dtype or dO.stride(3) != 1:
+        raise ValueError(f"dO must be {want} of {q.dtype}, last dimension contiguous")
+    _same_device(q, dO)
     new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
     g = {"q": new(q), "k": new(k), "v": new(v), "state": None if state is None else new(state)}
     if ws is None and need:

@@ -5,7 +5,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <vector>
 
 #include "../../include/ttt_block.h"
 #include "api_common.h"
@@ -30,24 +29,32 @@ struct Buffers {
     bool out;
     const void* may_be;  // an input this output may share its address with
   };
-  std::vector<Item> items;
+  Item items[16];  // more than any call has
+  int count = 0;
   void in(const char* name, const void* p, size_t bytes) {
-    if (p) items.push_back({range(name, p, bytes), p, false, nullptr});
+    if (p) items[count++] = {range(name, p, bytes), p, false, nullptr};
   }
   void out(const char* name, const void* p, size_t bytes, const void* may_be = nullptr) {
-    if (p) items.push_back({range(name, p, bytes), p, true, may_be});
+    if (p) items[count++] = {range(name, p, bytes), p, true, may_be};
   }
   ttt_status_t check() const {
-    for (const Item& a : items)
-      if (!aligned(a.p, 16))
-        return fail(TTT_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", a.r.name);
-    for (size_t i = 0; i < items.size(); ++i)
-      for (size_t j = 0; j < items.size(); ++j) {
+    for (int i = 0; i < count; ++i)
+      if (!aligned(items[i].p, 16))
+        return fail(TTT_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", items[i].r.name);
+    for (int i = 0; i < count; ++i)
+      for (int j = 0; j < count; ++j) {
         const Item &a = items[i], &b = items[j];
         if (i == j || !a.out || (b.out && j < i) || !overlaps(a.r, b.r)) continue;
         if (a.may_be && a.may_be == b.p && a.p == b.p && !b.out) continue;
         return fail(TTT_ERR_INVALID_ARGUMENT, "%s overlaps %s", a.r.name, b.r.name);
       }
+    return TTT_OK;
+  }
+  // A small input that needs no 16-byte alignment.
+  ttt_status_t check_against(const Range& in) const {
+    for (int i = 0; i < count; ++i)
+      if (items[i].out && in.hi > in.lo && overlaps(in, items[i].r))
+        return fail(TTT_ERR_INVALID_ARGUMENT, "%s overlaps %s", items[i].r.name, in.name);
     return TTT_OK;
   }
 };
@@ -294,12 +301,11 @@ ttt_status_t ttt_linattn_forward(const ttt_linattn_desc_t* desc, const void* q, 
   b.out("state_out", state_out, state_bytes(desc), state_in);
   if (need) b.out("ws", ws, need);
   if (ttt_status_t st = b.check()) return st;
-  // the small device arrays, which need 4-byte alignment only
-  for (const Range& in : {range("log_decay", log_decay, H * sizeof(float)),
-                          range("lengths", lengths, lengths ? desc->batch * sizeof(int32_t) : 0)})
-    for (const Buffers::Item& it : b.items)
-      if (it.out && in.hi > in.lo && overlaps(in, it.r))
-        return fail(TTT_ERR_INVALID_ARGUMENT, "%s overlaps %s", it.r.name, in.name);
+  if (ttt_status_t st = b.check_against(range("log_decay", log_decay, H * sizeof(float))))
+    return st;
+  if (ttt_status_t st = b.check_against(
+          range("lengths", lengths, lengths ? desc->batch * sizeof(int32_t) : 0)))
+    return st;
   ttt::LinArgs a{};
   a.q = operand(q, desc->q_stride, 1);
   a.k = operand(k, desc->k_stride, H / G);
@@ -349,11 +355,11 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
   b.out("dstate_in", dstate_in, state_bytes(desc), dstate_out);
   if (plan.total) b.out("ws", ws, plan.total);
   if (ttt_status_t st = b.check()) return st;
-  for (const Range& in : {range("log_decay", log_decay, H * sizeof(float)),
-                          range("lengths", lengths, lengths ? B * sizeof(int32_t) : 0)})
-    for (const Buffers::Item& it : b.items)
-      if (it.out && in.hi > in.lo && overlaps(in, it.r))
-        return fail(TTT_ERR_INVALID_ARGUMENT, "%s overlaps %s", it.r.name, in.name);
+  if (ttt_status_t st = b.check_against(range("log_decay", log_decay, H * sizeof(float))))
+    return st;
+  if (ttt_status_t st =
+          b.check_against(range("lengths", lengths, lengths ? B * sizeof(int32_t) : 0)))
+    return st;
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   float* seg = static_cast<float*>(ws);
