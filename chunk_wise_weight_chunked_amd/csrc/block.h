@@ -66,8 +66,17 @@ struct LinArgs {
   // The segments' states are in the workspace already, left there by the pass
   // with k and v exchanged (same sequences, lengths and direction).
   bool seg_trans;
+  // Two passes in one: this one and the one with (w, v, k) for (q, k, v), whose
+  // state is this one's transposed; its outputs go to out2 by their strides.
+  bool pair;
+  LinOperand w;
+  void* out2;
+  int64_t osb2, ost2, osh2;
   Dtype dt;
 };
+// Whether two passes of these shapes can run as one (bf16, and d_key and d_value
+// on tiles of one size).
+bool linattn_pairs(int64_t dk, int64_t dv, Dtype dt);
 // Bytes of the states that a chunked pass keeps between its launches (0: none).
 size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv);
 hipError_t launch_linattn_chunked(const LinArgs& a, float* seg, hipStream_t s);

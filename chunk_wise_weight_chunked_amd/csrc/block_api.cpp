@@ -171,18 +171,17 @@ size_t forward_bytes(const ttt_linattn_desc_t* d) {
 }
 
 // Backward workspace: the segments' states of a pass, and where heads share
-// keys and values one fp32 gradient per query head.
+// keys and values the fp32 gradients of k and v of every query head.
 struct BackwardPlan {
-  size_t part_off, total;
+  size_t dv_off, dk_off, total;
 };
 BackwardPlan backward_plan(const ttt_linattn_desc_t* d) {
   BackwardPlan p;
-  p.part_off = align256(ttt::linattn_segment_bytes(d->batch, d->heads, d->seq_len, d->d_key,
-                                                   d->d_value));
-  const size_t rows = (size_t)(d->batch * d->heads * d->seq_len);
-  p.total = p.part_off + (d->heads == d->kv_heads
-                              ? 0
-                              : rows * std::max(d->d_key, d->d_value) * sizeof(float));
+  p.dv_off = align256(ttt::linattn_segment_bytes(d->batch, d->heads, d->seq_len, d->d_key,
+                                                 d->d_value));
+  const size_t rows = d->heads == d->kv_heads ? 0 : (size_t)(d->batch * d->heads * d->seq_len);
+  p.dk_off = p.dv_off + align256(rows * d->d_value * sizeof(float));
+  p.total = p.dk_off + rows * d->d_key * sizeof(float);
   return p;
 }
 
@@ -363,7 +362,8 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
 
   hipStream_t s = static_cast<hipStream_t>(stream);
   float* seg = static_cast<float*>(ws);
-  float* part = rep > 1 ? reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part_off) : nullptr;
+  const bool shared_heads = rep > 1;
+  char* const wsb = static_cast<char*>(ws);
   const ttt::LinOperand oq = operand(q, desc->q_stride, 1), ok_ = operand(k, desc->k_stride, rep),
                         ov = operand(v, desc->v_stride, rep), od = operand(dO, desc->o_stride, 1);
   ttt::LinArgs base{};
@@ -381,34 +381,55 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
   hipError_t e = ttt::launch_linattn_chunked(a, seg, s);
 
   // dk and dv run from the last token; their state starts from dstate_out and
-  // ends as dstate_in.  dk's is dv's transposed, also at the segments' starts.
-  // dstate_in may be dstate_out, so the pass that writes it is the last one
-  // that reads dstate_out: dv's, or with segments' states left by it, dk's.
-  const bool shared = ttt::linattn_segment_bytes(B, H, T, K, V) != 0;
-  const auto from_end = [&](const ttt::LinOperand& x, const ttt::LinOperand& y,
-                            const ttt::LinOperand& z, int64_t dx, int64_t dz, void* out,
-                            bool is_dk) {
-    if (e != hipSuccess) return;
-    a = base;
-    a.q = x, a.k = y, a.v = z;
-    a.dk = dx, a.dv = dz;
-    if (part) {
-      a.out = part, a.out_f32 = true;
-      a.osb = H * T * dz, a.ost = dz, a.osh = T * dz;
-    } else {
-      a.out = out, a.osb = T * G * dz, a.ost = G * dz, a.osh = dz;
-    }
-    a.s_in = dstate_out, a.s_trans = is_dk, a.s_out = is_dk ? nullptr : dstate_in;
-    a.exact_state = !is_dk;
-    a.seg_trans = is_dk && shared;
-    a.scale_o = 1.0f, a.scale_u = desc->scale, a.late = 0, a.reverse = true;
-    e = ttt::launch_linattn_chunked(a, seg, s);
-    if (e == hipSuccess && part)
-      e = ttt::launch_linattn_sum_heads(part, out, T * G * dz, G * dz, dz, B, T, G, rep, dz, dt, s);
+  // ends as dstate_in, dk's being dv's transposed.  With shared heads they go to
+  // the workspace per query head and are summed from there.
+  struct Out {
+    void* p;
+    int64_t sb, st, sh;
   };
-  if (!shared) from_end(ov, od, oq, V, K, dk, true);
-  from_end(ok_, oq, od, K, V, dv, false);
-  if (shared) from_end(ov, od, oq, V, K, dk, true);
+  const auto out_of = [&](void* out, size_t part_off, int64_t d) {
+    return shared_heads ? Out{wsb + part_off, H * T * d, d, T * d} : Out{out, T * G * d, G * d, d};
+  };
+  const Out out_v = out_of(dv, plan.dv_off, V), out_k = out_of(dk, plan.dk_off, K);
+  a = base;
+  a.out_f32 = shared_heads, a.s_in = dstate_out, a.scale_o = 1.0f, a.scale_u = desc->scale;
+  a.late = 0, a.reverse = true;
+  const auto run = [&] {
+    if (e == hipSuccess) e = ttt::launch_linattn_chunked(a, seg, s);
+  };
+  const auto dv_pass = [&] {
+    a.q = ok_, a.k = oq, a.v = od, a.dk = K, a.dv = V;
+    a.out = out_v.p, a.osb = out_v.sb, a.ost = out_v.st, a.osh = out_v.sh;
+    a.s_trans = false, a.seg_trans = false, a.s_out = dstate_in, a.exact_state = true;
+  };
+  const auto dk_pass = [&](bool states_there) {
+    a.q = ov, a.k = od, a.v = oq, a.dk = V, a.dv = K;
+    a.out = out_k.p, a.osb = out_k.sb, a.ost = out_k.st, a.osh = out_k.sh;
+    a.s_trans = true, a.seg_trans = states_there, a.s_out = nullptr, a.exact_state = false;
+  };
+  if (ttt::linattn_pairs(K, V, dt)) {
+    dv_pass();
+    a.pair = true, a.w = ov;
+    a.out2 = out_k.p, a.osb2 = out_k.sb, a.ost2 = out_k.st, a.osh2 = out_k.sh;
+    run();
+  } else if (ttt::linattn_segment_bytes(B, H, T, K, V) != 0) {
+    // dk takes the segments' states that dv's pass leaves, and so reads no
+    // dstate_out, which dv's pass may have replaced
+    dv_pass(), run();
+    dk_pass(true), run();
+  } else {
+    dk_pass(false), run();  // reads dstate_out, which dv's pass may replace
+    dv_pass(), run();
+  }
+  if (shared_heads) {
+    const auto sum = [&](const Out& part, void* out, int64_t d) {
+      if (e == hipSuccess)
+        e = ttt::launch_linattn_sum_heads(static_cast<const float*>(part.p), out, T * G * d, G * d,
+                                          d, B, T, G, rep, d, dt, s);
+    };
+    sum(out_v, dv, V);
+    sum(out_k, dk, K);
+  }
   return e == hipSuccess ? ok() : hip_fail(e, "linattn_backward");
 }
 

@@ -348,12 +348,22 @@ constexpr int kScanInPlace = 8;
 // end state in `seg`, which holds a start state per segment: slot g + 1 gets
 // segment g's end, slot 0 the state the sequence starts from (the main pass
 // reads it from there, since s_out may be s_in).
-template <typename T, int DK, int NW, bool kOut, int kTerms, bool kF32Out = false>
-__global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, float4* seg,
-                                                                     int seg_len, int nseg) {
-  constexpr int kThreads = 64 * NW, DV = 32 * NW, KT = DK / 32;
+// kPair: two passes side by side that share their operands, each with NW waves of
+// its own: the one that `a` describes, and the one with q = w, k = v, v = k and
+// its outputs in out2, whose state is the first one's transposed (the gradients
+// of v and k: k, q, dO and v, dO, q).
+template <typename T, int DK, int NW, bool kOut, int kTerms, bool kF32Out = false,
+          bool kPair = false>
+__global__ __launch_bounds__(64 * NW * (kPair ? 2 : 1),
+                             sizeof(T) == 2 ? 2 : 1) void linattn_chunked_kernel(LinArgs a,
+                                                                                 float4* seg,
+                                                                                 int seg_len,
+                                                                                 int nseg) {
+  constexpr int kThreads = 64 * NW, DV = 32 * NW, KT = DK / 32, kAllWaves = NW * (kPair ? 2 : 1);
   constexpr int kOffV = kC * DK * sizeof(T), kOffQ = kOffV + kC * DV * sizeof(T);
-  constexpr int kBuf = kOffQ + (kOut ? kC * DK * (int)sizeof(T) : 0);
+  constexpr int kOffW = kOffQ + (kOut ? kC * DK * (int)sizeof(T) : 0);
+  constexpr int kBuf = kOffW + (kPair ? kC * DV * (int)sizeof(T) : 0);
+  static_assert(!kPair || (kOut && DK == DV), "the two passes have tiles of one shape");
   __shared__ __attribute__((aligned(16))) char smem[2 * kBuf];
 
   const int per = kOut ? nseg : nseg - 1;  // nobody starts from the last segment's end
@@ -370,19 +380,19 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
     if (lg < 0.0f && reach < (float)(t_hi - t_lo))
       t_lo = max(t_lo, t_hi - ((int)reach / kC + 1) * kC);
   }
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-  const int dk = (int)a.dk, dv = (int)a.dv;
+  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int uwave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int pass = kPair ? uwave / NW : 0, wave = uwave % NW, tid = wave * 64 + lane;
+  const int dk = (int)(pass ? a.dv : a.dk), dv = (int)(pass ? a.dk : a.dv);
   // ---- token rows: token t of the walk is row t, or row n - 1 - t of the tensors
-  const T* kp = head_base<T>(a.k, b, h);
-  const T* vp = head_base<T>(a.v, b, h);
-  const T* qp = head_base<T>(a.q, b, h);
   const int64_t row0 = a.reverse ? n - 1 - t_lo : t_lo;
-  const int uwave = __builtin_amdgcn_readfirstlane(wave);
-  Loader<T, DK, NW> ldK, ldQ;
-  Loader<T, DV, NW> ldV;
-  ldK.init(kp + row0 * a.k.st, a.k.st, a.reverse, dk, uwave, lane);
-  ldV.init(vp + row0 * a.v.st, a.v.st, a.reverse, dv, uwave, lane);
-  if constexpr (kOut) ldQ.init(qp + row0 * a.q.st, a.q.st, a.reverse, dk, uwave, lane);
+  Loader<T, DK, kAllWaves> ldK, ldQ;
+  Loader<T, DV, kAllWaves> ldV, ldW;
+  const auto first = [&](const LinOperand& o) { return head_base<T>(o, b, h) + row0 * o.st; };
+  ldK.init(first(a.k), a.k.st, a.reverse, (int)a.dk, uwave, lane);
+  ldV.init(first(a.v), a.v.st, a.reverse, (int)a.dv, uwave, lane);
+  if constexpr (kOut) ldQ.init(first(a.q), a.q.st, a.reverse, (int)a.dk, uwave, lane);
+  if constexpr (kPair) ldW.init(first(a.w), a.w.st, a.reverse, (int)a.dv, uwave, lane);
   const auto issue = [&](int t, lds_char* tiles_of) {
     // a last chunk of m < kC tokens fills the tiles' last m rows, so that every
     // weight below is the same as in a whole chunk
@@ -391,10 +401,12 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
       ldK.issue(tiles_of, uwave);
       ldV.issue(tiles_of + kOffV, uwave);
       if constexpr (kOut) ldQ.issue(tiles_of + kOffQ, uwave);
+      if constexpr (kPair) ldW.issue(tiles_of + kOffW, uwave);
     } else {
       ldK.issue_last(tiles_of, skip, uwave);
       ldV.issue_last(tiles_of + kOffV, skip, uwave);
       if constexpr (kOut) ldQ.issue_last(tiles_of + kOffQ, skip, uwave);
+      if constexpr (kPair) ldW.issue_last(tiles_of + kOffW, skip, uwave);
     }
   };
   if (t_lo < t_hi) issue(t_lo, (lds_char*)smem);  // on its way while the rest is set up
@@ -408,14 +420,15 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
   // + r % 8 of value column 32 wave + perm16(lane % 32)
   const int col = 32 * wave + perm16(lane & 31);
   floatx16_t S[KT];
-  const int rs = a.s_trans ? 1 : dv, cs = a.s_trans ? dk : 1;  // steps of a key row, a value column
+  const bool s_trans = a.s_trans != (pass == 1);
+  const int rs = s_trans ? 1 : dv, cs = s_trans ? dk : 1;  // steps of a key row, a value column
   const int64_t head_state = bh * dk * dv;
   const auto state_row = [&](int i, int r) { return 32 * i + 16 * (r >> 3) + 8 * half + (r & 7); };
   const int at0 = 8 * half * rs + col * cs;
   const auto state_off = [&](int i, int r) { return at0 + (32 * i + 16 * (r >> 3) + (r & 7)) * rs; };
   const auto from_slot = [&](int64_t j, float f) {  // S = f S + slot j
     const float4* p = slot + j * slot4;
-    if (a.seg_trans) {
+    if (kPair ? pass == 1 : a.seg_trans) {
       // written by the pass with keys and values exchanged: this lane's key row
       // is its value column, in tile `wave` of the wave that has it
       const int w = col & 31, lane_bits = ((w >> 3) & 1) * 32;
@@ -503,16 +516,19 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
   using TO = std::conditional_t<kF32Out, float, T>;
   constexpr int kRowPieces = DV * (int)sizeof(TO) / 16, kSwz = kRowPieces < 16 ? 7 : 15;
   constexpr int kOutB = kOut ? kC * DV * sizeof(TO) : 16;
-  __shared__ __attribute__((aligned(16))) char out_smem[2 * kOutB];
+  __shared__ __attribute__((aligned(16))) char out_smem[(kPair ? 4 : 2) * kOutB];
+  lds_char* const out_tiles = (lds_char*)out_smem + pass * 2 * kOutB;
   const auto out_at = [&](int row, int piece) {
     return (uint32_t)(row * kRowPieces + (piece ^ (row & kSwz))) * 16;
   };
   constexpr int kPutRows = kThreads / kRowPieces;  // rows of a store instruction
-  const int put_row = (int)threadIdx.x / kRowPieces, put_piece = (int)threadIdx.x % kRowPieces;
+  const int put_row = tid / kRowPieces, put_piece = tid % kRowPieces;
   const bool put_col = put_piece * (16 / (int)sizeof(TO)) < dv;
-  const int64_t put_step = a.reverse ? -a.ost : a.ost;  // values to the next token of the walk
-  TO* op = static_cast<TO*>(a.out) + b * a.osb + h * a.osh + row0 * a.ost + put_row * put_step +
-           put_piece * (16 / (int)sizeof(TO));
+  const int64_t ost = pass ? a.ost2 : a.ost;
+  const int64_t out_head = pass ? b * a.osb2 + h * a.osh2 : b * a.osb + h * a.osh;
+  TO* const out_base = static_cast<TO*>(pass ? a.out2 : a.out) + out_head;
+  const int64_t put_step = a.reverse ? -ost : ost;  // values to the next token of the walk
+  TO* op = out_base + row0 * ost + put_row * put_step + put_piece * (16 / (int)sizeof(TO));
   const auto put = [&](int skip, const lds_char* tile) {  // and on to the next chunk
 #pragma unroll
     for (int i = 0; i < kC / kPutRows; ++i) {
@@ -525,10 +541,11 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
   };
   wait_vmcnt<0>();
   lds_barrier();
-  const auto chunk = [&](int t, const lds_char* sK, lds_char* other, lds_char* out,
+  const auto chunk = [&](int t, const lds_char* tiles, lds_char* other, lds_char* out,
                          const lds_char* out_before) {
-    const lds_char* sV = sK + kOffV;
-    const lds_char* sQ = sK + kOffQ;
+    const lds_char* sK = tiles + (pass ? kOffV : 0);
+    const lds_char* sV = tiles + (pass ? 0 : kOffV);
+    const lds_char* sQ = tiles + (pass ? kOffW : kOffQ);
     const int m = min(kC, t_hi - t), skip = kC - m;
     if constexpr (kOut) {
       if (t > t_lo) put(0, out_before);
@@ -632,17 +649,17 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
   int buf = 0;
   for (int t = t_lo; t < t_hi; t += kC, buf ^= 1)
     chunk(t, (const lds_char*)smem + buf * kBuf, (lds_char*)smem + (buf ^ 1) * kBuf,
-          (lds_char*)out_smem + buf * kOutB, (const lds_char*)out_smem + (buf ^ 1) * kOutB);
+          out_tiles + buf * kOutB, out_tiles + (buf ^ 1) * kOutB);
   if constexpr (kOut) {
     if (t_lo < t_hi)
-      put((kC - (t_hi - t_lo) % kC) % kC, (const lds_char*)out_smem + (buf ^ 1) * kOutB);
+      put((kC - (t_hi - t_lo) % kC) % kC, out_tiles + (buf ^ 1) * kOutB);
   }
 
   if constexpr (!kOut) {
     to_slot(g + 1);
   } else {
     const bool last = t_hi == n && (t_lo < n || g == 0);  // this segment holds the last token
-    if (last && a.s_out) {
+    if (last && a.s_out && pass == 0) {
 #pragma unroll
       for (int i = 0; i < KT; ++i)
 #pragma unroll
@@ -655,14 +672,8 @@ __global__ __launch_bounds__(64 * NW, 2) void linattn_chunked_kernel(LinArgs a, 
     const int z_lo = max(t_lo, n), z_hi = min(t_lo + seg_len, (int)a.T);
     const int pieces = dv >> 3;
     const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int64_t p = threadIdx.x; p < (int64_t)(z_hi - z_lo) * pieces; p += kThreads) {
-      const int64_t at =
-          b * a.osb + (z_lo + p / pieces) * a.ost + h * a.osh + (p % pieces) * 8;
-      if constexpr (kF32Out)
-        store8(static_cast<float*>(a.out) + at, zero);
-      else
-        store8(static_cast<T*>(a.out) + at, zero);
-    }
+    for (int64_t p = tid; p < (int64_t)(z_hi - z_lo) * pieces; p += kThreads)
+      store8(out_base + (z_lo + p / pieces) * ost + (p % pieces) * 8, zero);
   }
 }
 
@@ -834,12 +845,31 @@ hipError_t chunked(const LinArgs& a, float4* seg, const Split& p, hipStream_t s)
   }
   const dim3 grid((unsigned)(heads * p.nseg));
   float4* start = p.nseg > 1 ? seg : nullptr;
-  if (a.out_f32 && sizeof(T) == 2)
-    linattn_chunked_kernel<T, DK, NW, true, kTerms, sizeof(T) == 2>
-        <<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
-  else
-    linattn_chunked_kernel<T, DK, NW, true, kTerms>
-        <<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
+  // fp32 outputs of bf16 passes are gradients on their way to a sum over heads,
+  // which come from a pair where the tiles are of one size
+  constexpr bool kBf16 = sizeof(T) == 2, kSquare = DK == 32 * NW;
+  if (a.pair) {
+    if constexpr (kBf16 && kSquare && kTerms == 3) {
+      if (a.out_f32)
+        linattn_chunked_kernel<T, DK, NW, true, kTerms, true, true>
+            <<<grid, 128 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
+      else
+        linattn_chunked_kernel<T, DK, NW, true, kTerms, false, true>
+            <<<grid, 128 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
+      return hipGetLastError();
+    }
+    return hipErrorInvalidValue;
+  }
+  if (kBf16 && a.out_f32) {
+    if constexpr (kBf16 && !kSquare) {
+      linattn_chunked_kernel<T, DK, NW, true, kTerms, true>
+          <<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
+      return hipGetLastError();
+    }
+    return hipErrorInvalidValue;
+  }
+  linattn_chunked_kernel<T, DK, NW, true, kTerms>
+      <<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
   return hipGetLastError();
 }
 
@@ -854,6 +884,10 @@ hipError_t chunked_shape(const LinArgs& a, float4* seg, hipStream_t s) {
 }
 
 }  // namespace
+
+bool linattn_pairs(int64_t dk, int64_t dv, Dtype dt) {
+  return dt == Dtype::BF16 && padded(dk) == padded(dv);
+}
 
 size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
   const Split p = split(B, H, T, dk, dv);
