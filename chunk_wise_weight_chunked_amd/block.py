@@ -185,8 +185,12 @@ def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_o
         raise ValueError("x has no rows")
     desc = _norm_plan(rows, d, xs, x.dtype, x.dtype if res is None else res.dtype, eps, fp8,
                       scale_group)
-    y = torch.empty(x.shape, dtype=out_dtype if fp8 else x.dtype, device=x.device)
-    r = None if res is None else torch.empty_like(res) if r_out is None else r_out
+    # contiguous outputs, whatever the rows of x are apart
+    y = (torch.empty(x.shape, dtype=out_dtype, device=x.device) if fp8
+         else torch.empty_like(x, memory_format=torch.contiguous_format))
+    r = (None if res is None
+         else torch.empty_like(res, memory_format=torch.contiguous_format) if r_out is None
+         else r_out)
     scale = None
     if fp8:
         shape = x.shape[:-1] + (d // scale_group if scale_group else 1,)

@@ -5,12 +5,10 @@
 //
 // Both directions are bound by HBM: every input is read once and every output
 // written once, a row stays in registers between the two uses of its values,
-// and the only exchange is the sum over a row.  LPR lanes share a row (16 lanes
-// for rows of up to 128 values, a wave for up to 4096, a workgroup beyond, and
-// a workgroup also where there are too few rows to fill the CUs with waves), so
-// that the sum is a few lane shuffles; lane l holds the 8-value pieces l,
-// l + LPR, ... of its row (NV of them), one or two 16-byte loads each, all
-// issued before the first is used.
+// and the only exchange is the sum over a row.  LPR lanes share a row (16 lanes,
+// a wave or a workgroup: row_shape below), so that the sum is a few lane
+// shuffles; lane l holds the 8-value pieces l, l + LPR, ... of its row (NV of
+// them), one or two 16-byte loads each, all issued before the first is used.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -325,27 +323,37 @@ struct RowShape {
   int lpr, nv;
 };
 
-// A wave holds rows of up to 8 pieces a lane (4096 values); below 512 rows (two
-// waves a CU) a workgroup takes a row instead, which shortens the chain of
-// loads and shuffles of a call of a few rows.
-RowShape row_shape(const NormArgs& a) {
+// 16 lanes take rows of up to 128 values; rows of up to 512 a wave.  Longer ones
+// (bf16, us with a wave a row / with a workgroup a row):
+//   forward   512 x 1024 3.3 / 3.0,  512 x 2560 4.8 / 3.9,  32768 x 1024 41 / 45,
+//             32768 x 1536 77 / 71,  32768 x 2560 129 / 121,  32768 x 4096 209 / 190
+//   backward  256 x 2560 9.0 / 7.9,  512 x 2560 9.8 / 10.9,  32768 x 1024 38 / 80,
+//             32768 x 2560 102 / 125,  4096 x 4096 38 / 25
+// The workgroup shortens the chain of a few rows and has fewer values in a
+// lane's registers; the wave needs no barrier and, in the backward, adds four
+// rows' sums before they leave the workgroup.
+RowShape row_shape(const NormArgs& a, bool backward) {
   const int pieces = (int)(a.d / 8);
-  const int lpr = pieces <= 16 ? 16 : (pieces <= 512 && (a.rows >= 512 || pieces <= 64)) ? 64 : 256;
+  const bool wave = pieces <= 64 || (backward ? pieces <= 320 && a.rows >= 384
+                                              : pieces <= 128 && a.rows >= 2048);
+  const int lpr = pieces <= 16 ? 16 : wave ? 64 : 256;
   const int need = (pieces + lpr - 1) / lpr;
   const int nv = need <= 1 ? 1 : need <= 2 ? 2 : need <= 3 ? 3 : need <= 5 ? 5 : 8;
   return {lpr, nv};
 }
 
-template <typename F>
+// Calls f with the shape as constants: what row_shape gives in the direction.
+template <bool kBackward, typename F>
 hipError_t with_shape(const RowShape& s, F&& f) {
 #define TTT_SHAPE(L, N) \
   if (s.lpr == L && s.nv == N) return f(std::integral_constant<int, L>{}, std::integral_constant<int, N>{});
   TTT_SHAPE(16, 1)
   TTT_SHAPE(64, 1)
   TTT_SHAPE(64, 2)
-  TTT_SHAPE(64, 3)
-  TTT_SHAPE(64, 5)
-  TTT_SHAPE(64, 8)
+  if constexpr (kBackward) {
+    TTT_SHAPE(64, 3)
+    TTT_SHAPE(64, 5)
+  }
   TTT_SHAPE(256, 1)
   TTT_SHAPE(256, 2)
   TTT_SHAPE(256, 3)
@@ -368,7 +376,7 @@ hipError_t launch_addnorm_forward(const NormArgs& a, const void* x, const void* 
   return with_types(a, [&](auto tx, auto tr) {
     using TX = decltype(tx);
     using TR = decltype(tr);
-    return with_shape(row_shape(a), [&](auto lpr, auto nv) {
+    return with_shape<false>(row_shape(a, false), [&](auto lpr, auto nv) {
       constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
       const int64_t per = kBlock / L;
       const dim3 grid((unsigned)((a.rows + per - 1) / per));
@@ -387,7 +395,7 @@ hipError_t launch_addnorm_forward(const NormArgs& a, const void* x, const void* 
 // Two workgroups a CU: the partial sums stay small (512 rows of d) and each
 // workgroup walks enough rows to hide them.
 int64_t addnorm_backward_blocks(const NormArgs& a) {
-  const int64_t per = kBlock / row_shape(a).lpr;
+  const int64_t per = kBlock / row_shape(a, true).lpr;
   return std::min<int64_t>((a.rows + per - 1) / per, 512);
 }
 
@@ -398,7 +406,7 @@ hipError_t launch_addnorm_backward(const NormArgs& a, const void* dy, const void
   hipError_t e = with_types(a, [&](auto tx, auto tr) {
     using TX = decltype(tx);
     using TR = decltype(tr);
-    return with_shape(row_shape(a), [&](auto lpr, auto nv) {
+    return with_shape<true>(row_shape(a, true), [&](auto lpr, auto nv) {
       constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
       const size_t lds = L < kBlock ? (size_t)a.d * sizeof(float) : 0;
       addnorm_backward_kernel<TX, TR, L, N><<<dim3((unsigned)blocks), kBlock, lds, s>>>(

@@ -32,7 +32,7 @@ hipError_t launch_addnorm_backward(const NormArgs& a, const void* dy, const void
 // ------------------------------------------- linear attention with a decay
 constexpr int kLinChunk = 32;      // tokens per chunk of the chunked form
 constexpr int kLinMaxHead = 128;   // values per head, keys and values
-constexpr int kLinStepTokens = 8;  // tokens a call of the recurrent form takes at most
+constexpr int kLinStepTokens = 4;  // tokens a call of the recurrent form takes at most
 
 // One [B][T][heads][d] operand; query head h reads head h / rep.
 struct LinOperand {

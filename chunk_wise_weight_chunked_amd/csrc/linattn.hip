@@ -708,10 +708,14 @@ __global__ __launch_bounds__(64) void linattn_scan_kernel(float4* seg,
 
 // ------------------------------------------------------------ recurrent form
 // Bound by reading and writing the state once.  A workgroup takes 32 value
-// columns of one head: 8 threads of 4 columns by 32 row groups of 4 key rows
-// (rows group, group + 32, ...), all four 16-byte loads of a thread issued
-// together; its tokens then run in registers, and the sums over the key rows
-// end in LDS after the last token.
+// columns of one head: 8 threads of 4 columns by 32 groups of 4 key rows, all
+// four 16-byte loads of a thread issued together.  The tokens' q, k and v go to
+// LDS as fp32 while the state is on its way (read from memory token by token
+// they cost 1.4 us a token); the tokens then run in registers, and the sums over
+// the key rows end in LDS after the last token.  From 5 tokens on the chunked
+// form is faster (us for 1, 8 and 64 sessions of 20, 16 and 20 heads: 4 tokens
+// 6.4, 6.2, 38 here and 10.1, 7.4, 39 chunked; 8 tokens 9.3, 9.2, 50 and 10.1,
+// 7.4, 39).
 constexpr int kStepCols = 32;
 
 __device__ __forceinline__ float to_f32(uint16_t v) { return bf16_bits_to_f32(v); }
@@ -719,45 +723,47 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 
 template <typename T>
 __global__ __launch_bounds__(256) void linattn_step_kernel(LinArgs a) {
+  __shared__ __attribute__((aligned(16))) float q_s[kLinStepTokens][kLinMaxHead];
+  __shared__ __attribute__((aligned(16))) float k_s[kLinStepTokens][kLinMaxHead];
+  __shared__ __attribute__((aligned(16))) float v_s[kLinStepTokens][kStepCols];
   __shared__ float part[kLinStepTokens][4][kStepCols];
   const int slices = (int)((a.dv + kStepCols - 1) / kStepCols);
   const int64_t bh = blockIdx.x / slices, b = bh / a.H, h = bh % a.H;
-  const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;
-  const int col = (int)(blockIdx.x % slices) * kStepCols + 4 * cg;
-  const bool live_col = col < a.dv;
+  const int cg = threadIdx.x & 7, row0 = (threadIdx.x >> 3) * 4;
+  const int c0 = (int)(blockIdx.x % slices) * kStepCols, col = c0 + 4 * cg;
   const int dk = (int)a.dk, dv = (int)a.dv;
-  const int n = (int)live_tokens(a.lengths, b, a.T);
-  const int64_t base = bh * dk * dv + col;
-  float S[4][4];
+  const bool live = col < dv && row0 < dk;  // whole groups: d_key and d_value are multiples of 8
+  const int n = live_tokens(a.lengths, b, a.T);
+  const int64_t base = bh * dk * dv + (int64_t)row0 * dv + col;
+  float4 S[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int row = rg + 32 * i;
-    float4 x = make_float4(0, 0, 0, 0);
-    if (a.s_in && live_col && row < dk)
-      x = *reinterpret_cast<const float4*>(a.s_in + base + (int64_t)row * dv);
-    S[i][0] = x.x, S[i][1] = x.y, S[i][2] = x.z, S[i][3] = x.w;
+    S[i] = make_float4(0, 0, 0, 0);
+    if (a.s_in && live) S[i] = *reinterpret_cast<const float4*>(a.s_in + base + i * dv);
   }
-  const float lg = a.log_decay[h];
-  const float g = expf(lg);
   const T* qp = head_base<T>(a.q, b, h);
   const T* kp = head_base<T>(a.k, b, h);
   const T* vp = head_base<T>(a.v, b, h);
+  const float g = expf(a.log_decay[h]);
+  for (int p = threadIdx.x; p < n * kLinMaxHead; p += 256) {
+    const int t = p / kLinMaxHead, r = p % kLinMaxHead;
+    q_s[t][r] = r < dk ? to_f32(qp[t * a.q.st + r]) : 0.0f;
+    k_s[t][r] = r < dk ? to_f32(kp[t * a.k.st + r]) : 0.0f;
+    if (r < kStepCols) v_s[t][r] = c0 + r < dv ? to_f32(vp[t * a.v.st + c0 + r]) : 0.0f;
+  }
+  __syncthreads();
   for (int t = 0; t < n; ++t) {
-    float q[4], k[4], v[4], o[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = rg + 32 * i;
-      q[i] = row < dk ? to_f32(qp[t * a.q.st + row]) : 0.0f;
-      k[i] = row < dk ? to_f32(kp[t * a.k.st + row]) : 0.0f;
-      v[i] = live_col ? to_f32(vp[t * a.v.st + col + i]) : 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        S[i][j] = fmaf(g, S[i][j], k[i] * v[j]);
-        o[j] = fmaf(q[i], S[i][j], o[j]);
-      }
+    const float4 q = *reinterpret_cast<const float4*>(&q_s[t][row0]);
+    const float4 k = *reinterpret_cast<const float4*>(&k_s[t][row0]);
+    const float4 v = *reinterpret_cast<const float4*>(&v_s[t][4 * cg]);
+    float o[4] = {0, 0, 0, 0};
+    const auto row = [&](float4& x, float ki, float qi) {
+      x.x = fmaf(g, x.x, ki * v.x), x.y = fmaf(g, x.y, ki * v.y);
+      x.z = fmaf(g, x.z, ki * v.z), x.w = fmaf(g, x.w, ki * v.w);
+      o[0] = fmaf(qi, x.x, o[0]), o[1] = fmaf(qi, x.y, o[1]);
+      o[2] = fmaf(qi, x.z, o[2]), o[3] = fmaf(qi, x.w, o[3]);
+    };
+    row(S[0], k.x, q.x), row(S[1], k.y, q.y), row(S[2], k.z, q.z), row(S[3], k.w, q.w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -765,17 +771,11 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(LinArgs a) {
       if ((threadIdx.x & 63) < 8) part[t][threadIdx.x >> 6][4 * cg + j] = o[j];
     }
   }
-  if (a.s_out && live_col) {
+  if (a.s_out && live) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = rg + 32 * i;
-      if (row < dk)
-        *reinterpret_cast<float4*>(a.s_out + base + (int64_t)row * dv) =
-            make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
-    }
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(a.s_out + base + i * dv) = S[i];
   }
   __syncthreads();
-  const int64_t c0 = (blockIdx.x % slices) * kStepCols;
   for (int p = threadIdx.x; p < a.T * kStepCols; p += 256) {
     const int t = p / kStepCols, c = p % kStepCols;
     if (c0 + c >= dv) continue;

@@ -31,7 +31,7 @@ extern "C" {
  * out = TTT_NORM_FP8 writes y in 8 bits (OCP E4M3) with fp32 scales: for each
  * row, or each run of 128 values of a row, scale = max |y| / 448 (1 where every
  * y is 0) and the stored value is y / scale rounded to nearest even, so that
- * stored * scale is y.
+ * stored * scale is y.  A NaN is stored as NaN and left out of the maximum.
  *
  *   rows      >= 1
  *   d         a multiple of 8, 8 <= d <= 16384
@@ -148,7 +148,7 @@ ttt_status_t ttt_linattn_backward_workspace_size(const ttt_linattn_desc_t* desc,
  *   state_in   or NULL (0)
  *   state_out  the state behind each sequence's last token; may be state_in
  *              itself (a session's state updated in place); may be NULL
- * Tokens of up to 8 per call run in the recurrent form (state read and
+ * Calls of up to 4 tokens run in the recurrent form (state read and
  * written once, all arithmetic in fp32), longer calls in the chunked form on
  * the matrix cores: bf16 products with fp32 accumulation, in which the decayed
  * scores and the state's copy that meets q are rounded to bf16 while the state

@@ -168,9 +168,9 @@ def test_norm_backward_against_differences():
 
 
 # ---------------------------------------------------------- linear attention
-# (B, T, H, G, dk, dv): up to 8 tokens in the recurrent form; whole and partial
+# (B, T, H, G, dk, dv): up to 4 tokens in the recurrent form; whole and partial
 # chunks of 32; one or more segments; every tile width
-ATTN_SHAPES = [(1, 1, 1, 1, 8, 8), (3, 1, 4, 4, 128, 128), (2, 8, 4, 2, 72, 40), (1, 5, 2, 1, 64, 128),
+ATTN_SHAPES = [(1, 1, 1, 1, 8, 8), (3, 1, 4, 4, 128, 128), (2, 4, 4, 2, 72, 40), (3, 3, 2, 1, 40, 128), (2, 8, 4, 2, 72, 40), (1, 5, 2, 1, 64, 128),
                (1, 9, 1, 1, 16, 8), (2, 31, 2, 1, 64, 64), (1, 32, 3, 3, 128, 64),
                (2, 33, 4, 1, 64, 128), (1, 65, 2, 2, 128, 128), (1, 100, 2, 1, 80, 72),
                (1, 257, 2, 2, 96, 104), (2, 511, 1, 1, 128, 128), (1, 523, 4, 2, 64, 64),
