@@ -5,8 +5,8 @@ linear attention with a decay for each head, each with its gradients.
 Like ttt_mlp, this is argument marshalling only, over the same library
 (ttt_mlp.load()): the functions named as the C entry points take raw
 descriptors and buffers; add_rmsnorm, add_rmsnorm_backward, linattn_forward
-and linattn_backward allocate outputs and workspace with torch and call them.
-There is no fallback.
+and linattn_backward allocate outputs and workspace with torch and call them, on
+the current stream or on the one given as stream=.  There is no fallback.
 """
 from __future__ import annotations
 
@@ -100,6 +100,21 @@ def _current(stream, like):
     return _stream(stream)
 
 
+def _on_stream(fn):
+    """A tensor-level call with stream=s allocates on s as well: its outputs and its workspace
+    are that stream's, so no other stream's allocation can take their memory while s still
+    works on it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
 # ------------------------------------------------ residual addition and norm
 def make_addnorm_desc(rows, d, dtype, res_dtype=None, x_stride=None, y_stride=None, eps=NORM_EPS,
                       out=TTT_NORM_SAME, scale_group=0) -> ttt_addnorm_desc_t:
@@ -164,8 +179,8 @@ def _norm_checks(x, res, w, what):
         raise ValueError(f"the residual must have {what}'s shape and its type or float32")
 
 
-def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_out=None,
-                stream=None):
+@_on_stream
+def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_out=None):
     """r = x + res, y = r / sqrt(mean(r^2) + eps) * weight over the last dimension.
 
     x [..., d] bf16 or fp32 (2-dimensional with any row stride, or contiguous), weight [d] of
@@ -195,11 +210,12 @@ def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_o
     if fp8:
         shape = x.shape[:-1] + (d // scale_group if scale_group else 1,)
         scale = torch.empty(shape, dtype=torch.float32, device=x.device)
-    ttt_addnorm_forward(desc, x, res, weight, r, y, scale, stream=stream)
+    ttt_addnorm_forward(desc, x, res, weight, r, y, scale)
     return y, r, scale
 
 
-def add_rmsnorm_backward(dy, r, weight, eps=NORM_EPS, dr=None, stream=None):
+@_on_stream
+def add_rmsnorm_backward(dy, r, weight, eps=NORM_EPS, dr=None):
     """Gradients of <dy, y> + <dr, r> for y = norm(r) * weight: r is add_rmsnorm's (x itself where
     it had no residual), dr the gradient that reaches r from its other uses, or None.  Returns
     (dr, dx, dweight): the gradient of the sum in r's type, the same in dy's type (the same
@@ -217,7 +233,7 @@ def add_rmsnorm_backward(dy, r, weight, eps=NORM_EPS, dr=None, stream=None):
     dw = torch.empty(d, dtype=torch.float32, device=dy.device)
     ws = torch.empty(ttt_addnorm_backward_workspace_size(desc), dtype=torch.uint8,
                      device=dy.device)
-    ttt_addnorm_backward(desc, dy, r, weight, dr, out, dx, dw, ws, stream=stream)
+    ttt_addnorm_backward(desc, dy, r, weight, dr, out, dx, dw, ws)
     return out, out if dx is None else dx, dw
 
 
@@ -304,8 +320,9 @@ def _linattn_checks(q, k, v, log_decay, lengths, *states):
     _same_device(q, k, v, log_decay, lengths, *states)
 
 
+@_on_stream
 def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, lengths=None,
-                    ws=None, stream=None):
+                    ws=None):
     """S_t = exp(log_decay) S_{t-1} + k_t v_t^T, o_t = scale q_t S_t for each head.
 
     q [B][T][H][dk], k [B][T][G][dk], v [B][T][G][dv] (bf16 or fp32; any strides in multiples
@@ -323,12 +340,13 @@ def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, 
         state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
     if ws is None and need:
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ttt_linattn_forward(desc, q, k, v, log_decay, lengths, state, state_out, o, ws, stream=stream)
+    ttt_linattn_forward(desc, q, k, v, log_decay, lengths, state, state_out, o, ws)
     return o, state_out
 
 
+@_on_stream
 def linattn_backward(q, k, v, log_decay, dO, scale=None, state=None, dstate_out=None,
-                     lengths=None, ws=None, stream=None) -> dict:
+                     lengths=None, ws=None) -> dict:
     """Gradients of <dO, o> + <dstate_out, final state> for linattn_forward from `state`.
     Returns a dict: q, k, v (their shapes, contiguous) and state (fp32; None when no state was
     given)."""
@@ -344,5 +362,5 @@ def linattn_backward(q, k, v, log_decay, dO, scale=None, state=None, dstate_out=
     if ws is None and need:
         ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     ttt_linattn_backward(desc, q, k, v, log_decay, lengths, state, dO, dstate_out, g["q"], g["k"],
-                         g["v"], g["state"], ws, stream=stream)
+                         g["v"], g["state"], ws)
     return g

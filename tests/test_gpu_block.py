@@ -410,6 +410,32 @@ def test_another_stream():
     assert torch.equal(o1, o) and torch.equal(S1, S) and torch.equal(y1, y)
 
 
+def test_stream_argument_owns_its_allocations():
+    """stream=s: what the call allocates belongs to s, so that allocations of the stream around
+    it, filled at once, cannot land in memory that s still works on."""
+    g, q, k, v, lg, st = attn_inputs(1, 6000, 4, 4, 64, 64, BF16, 12)
+    dO = normal(g, 1, 6000, 4, 64, dtype=BF16)
+    r, w = normal(g, 4096, 2560, dtype=BF16), normal(g, 2560, dtype=BF16)
+    calls = (lambda **kw: block.linattn_forward(q, k, v, lg, state=st, **kw),
+             lambda **kw: tuple(block.linattn_backward(q, k, v, lg, dO, state=st, **kw).values()),
+             lambda **kw: block.add_rmsnorm_backward(r, r, w, **kw),
+             lambda **kw: block.add_rmsnorm(r, r, w, **kw)[:2])
+    s = torch.cuda.Stream()
+    busy = torch.ones(1 << 26, device="cuda")
+    for call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        for stream in (s, s.cuda_stream):
+            with torch.cuda.stream(s):
+                busy.mul_(1.0)  # s is behind the current stream
+            got = call(stream=stream)
+            junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+                    for n in (1 << 20, 1 << 22, 1 << 24) for _ in range(4)]
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+            del junk, got
+
+
 def test_graph_replays_equal_eager():
     g, q, k, v, lg, st = attn_inputs(1, 700, 4, 2, 64, 64, BF16, 3)
     dO = normal(g, 1, 700, 4, 64, dtype=BF16)
