@@ -63,9 +63,10 @@ struct LinArgs {
   float scale_o, scale_p, scale_u;
   int32_t late;
   bool reverse;
-  // The segments' states are in the workspace already, left there by the pass
-  // with k and v exchanged (same sequences, lengths and direction).
-  bool seg_trans;
+  // The segments' states are in the workspace already: left there by
+  // launch_linattn_starts, or (seg_trans) for the pass with k and v exchanged
+  // (same sequences, lengths and direction).
+  bool seg_ready, seg_trans;
   // Two passes in one: this one and the one with (w, v, k) for (q, k, v), whose
   // state is this one's transposed; its outputs go to out2 by their strides.
   bool pair;
@@ -74,12 +75,15 @@ struct LinArgs {
   int64_t osb2, ost2, osh2;
   Dtype dt;
 };
-// Whether two passes of these shapes can run as one (bf16, and d_key and d_value
-// on tiles of one size).
-bool linattn_pairs(int64_t dk, int64_t dv, Dtype dt);
+// Whether d_key and d_value have tiles of one size: passes with keys and values
+// exchanged can then share launches (bf16 passes with LinArgs::pair too).
+bool linattn_square(int64_t dk, int64_t dv);
 // Bytes of the states that a chunked pass keeps between its launches (0: none).
 size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv);
 hipError_t launch_linattn_chunked(const LinArgs& a, float* seg, hipStream_t s);
+// The segments' states of one or two passes of the same tiles and exact_state,
+// pass i's at i times linattn_segment_bytes behind seg.
+hipError_t launch_linattn_starts(const LinArgs* a, int count, float* seg, hipStream_t s);
 // The recurrent form, T <= kLinStepTokens (forward direction, late = 1, out in
 // the operands' type).
 hipError_t launch_linattn_step(const LinArgs& a, hipStream_t s);

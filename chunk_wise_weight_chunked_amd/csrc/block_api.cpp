@@ -170,15 +170,17 @@ size_t forward_bytes(const ttt_linattn_desc_t* d) {
                                                    d->d_value);
 }
 
-// Backward workspace: the segments' states of a pass, and where heads share
-// keys and values the fp32 gradients of k and v of every query head.
+// Backward workspace: the segments' states of dq's pass, behind them those of
+// dv's where the two are made together (elsewhere dv's take the place of dq's),
+// and where heads share keys and values the fp32 gradients of k and v of every
+// query head.
 struct BackwardPlan {
-  size_t dv_off, dk_off, total;
+  size_t seg_bytes, dv_off, dk_off, total;
 };
 BackwardPlan backward_plan(const ttt_linattn_desc_t* d) {
   BackwardPlan p;
-  p.dv_off = align256(ttt::linattn_segment_bytes(d->batch, d->heads, d->seq_len, d->d_key,
-                                                 d->d_value));
+  p.seg_bytes = ttt::linattn_segment_bytes(d->batch, d->heads, d->seq_len, d->d_key, d->d_value);
+  p.dv_off = align256(p.seg_bytes * (ttt::linattn_square(d->d_key, d->d_value) ? 2 : 1));
   const size_t rows = d->heads == d->kv_heads ? 0 : (size_t)(d->batch * d->heads * d->seq_len);
   p.dk_off = p.dv_off + align256(rows * d->d_value * sizeof(float));
   p.total = p.dk_off + rows * d->d_key * sizeof(float);
@@ -372,13 +374,11 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
   base.scale_p = desc->scale;
 
   // dq = the operator with (dO, v, k) for (q, k, v); its state is S transposed
-  ttt::LinArgs a = base;
-  a.q = od, a.k = ov, a.v = ok_;
-  a.dk = V, a.dv = K;
-  a.out = dq, a.osb = T * H * K, a.ost = H * K, a.osh = K;
-  a.s_in = state_in, a.s_trans = true;
-  a.scale_o = desc->scale, a.scale_u = 1.0f, a.late = 1;
-  hipError_t e = ttt::launch_linattn_chunked(a, seg, s);
+  ttt::LinArgs aq = base;
+  aq.q = od, aq.k = ov, aq.v = ok_, aq.dk = V, aq.dv = K;
+  aq.out = dq, aq.osb = T * H * K, aq.ost = H * K, aq.osh = K;
+  aq.s_in = state_in, aq.s_trans = true;
+  aq.scale_o = desc->scale, aq.scale_u = 1.0f, aq.late = 1;
 
   // dk and dv run from the last token; their state starts from dstate_out and
   // ends as dstate_in, dk's being dv's transposed.  With shared heads they go to
@@ -391,35 +391,43 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
     return shared_heads ? Out{wsb + part_off, H * T * d, d, T * d} : Out{out, T * G * d, G * d, d};
   };
   const Out out_v = out_of(dv, plan.dv_off, V), out_k = out_of(dk, plan.dk_off, K);
-  a = base;
-  a.out_f32 = shared_heads, a.s_in = dstate_out, a.scale_o = 1.0f, a.scale_u = desc->scale;
-  a.late = 0, a.reverse = true;
-  const auto run = [&] {
-    if (e == hipSuccess) e = ttt::launch_linattn_chunked(a, seg, s);
+  ttt::LinArgs av = base;
+  av.out_f32 = shared_heads, av.s_in = dstate_out, av.scale_o = 1.0f, av.scale_u = desc->scale;
+  av.late = 0, av.reverse = true;
+  ttt::LinArgs ak = av;
+  av.q = ok_, av.k = oq, av.v = od, av.dk = K, av.dv = V;
+  av.out = out_v.p, av.osb = out_v.sb, av.ost = out_v.st, av.osh = out_v.sh;
+  av.s_out = dstate_in, av.exact_state = true;
+  ak.q = ov, ak.k = od, ak.v = oq, ak.dk = V, ak.dv = K;
+  ak.out = out_k.p, ak.osb = out_k.sb, ak.ost = out_k.st, ak.osh = out_k.sh;
+  ak.s_trans = true;
+
+  hipError_t e = hipSuccess;
+  const auto run = [&](const ttt::LinArgs& a, float* states) {
+    if (e == hipSuccess) e = ttt::launch_linattn_chunked(a, states, s);
   };
-  const auto dv_pass = [&] {
-    a.q = ok_, a.k = oq, a.v = od, a.dk = K, a.dv = V;
-    a.out = out_v.p, a.osb = out_v.sb, a.ost = out_v.st, a.osh = out_v.sh;
-    a.s_trans = false, a.seg_trans = false, a.s_out = dstate_in, a.exact_state = true;
-  };
-  const auto dk_pass = [&](bool states_there) {
-    a.q = ov, a.k = od, a.v = oq, a.dk = V, a.dv = K;
-    a.out = out_k.p, a.osb = out_k.sb, a.ost = out_k.st, a.osh = out_k.sh;
-    a.s_trans = true, a.seg_trans = states_there, a.s_out = nullptr, a.exact_state = false;
-  };
-  if (ttt::linattn_pairs(K, V, dt)) {
-    dv_pass();
-    a.pair = true, a.w = ov;
-    a.out2 = out_k.p, a.osb2 = out_k.sb, a.ost2 = out_k.st, a.osh2 = out_k.sh;
-    run();
-  } else if (ttt::linattn_segment_bytes(B, H, T, K, V) != 0) {
+  float* seg_v = seg;
+  if (plan.seg_bytes && ttt::linattn_square(K, V)) {
+    seg_v = seg + plan.seg_bytes / sizeof(float);
+    ttt::LinArgs both[2] = {aq, av};
+    both[0].exact_state = true;
+    e = ttt::launch_linattn_starts(both, 2, seg, s);
+    aq.seg_ready = av.seg_ready = true;
+  }
+  run(aq, seg);
+  if (ttt::linattn_square(K, V) && dt == ttt::Dtype::BF16) {
+    av.pair = true, av.w = ov;
+    av.out2 = out_k.p, av.osb2 = out_k.sb, av.ost2 = out_k.st, av.osh2 = out_k.sh;
+    run(av, seg_v);
+  } else if (plan.seg_bytes) {
     // dk takes the segments' states that dv's pass leaves, and so reads no
     // dstate_out, which dv's pass may have replaced
-    dv_pass(), run();
-    dk_pass(true), run();
+    run(av, seg_v);
+    ak.seg_trans = true;
+    run(ak, seg_v);
   } else {
-    dk_pass(false), run();  // reads dstate_out, which dv's pass may replace
-    dv_pass(), run();
+    run(ak, nullptr);  // reads dstate_out, which dv's pass may replace
+    run(av, nullptr);
   }
   if (shared_heads) {
     const auto sum = [&](const Out& part, void* out, int64_t d) {

@@ -352,13 +352,8 @@ constexpr int kScanInPlace = 8;
 // its own: the one that `a` describes, and the one with q = w, k = v, v = k and
 // its outputs in out2, whose state is the first one's transposed (the gradients
 // of v and k: k, q, dO and v, dO, q).
-template <typename T, int DK, int NW, bool kOut, int kTerms, bool kF32Out = false,
-          bool kPair = false>
-__global__ __launch_bounds__(64 * NW * (kPair ? 2 : 1),
-                             sizeof(T) == 2 ? 2 : 1) void linattn_chunked_kernel(LinArgs a,
-                                                                                 float4* seg,
-                                                                                 int seg_len,
-                                                                                 int nseg) {
+template <typename T, int DK, int NW, bool kOut, int kTerms, bool kF32Out, bool kPair>
+__device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int seg_len, int nseg) {
   constexpr int kThreads = 64 * NW, DV = 32 * NW, KT = DK / 32, kAllWaves = NW * (kPair ? 2 : 1);
   constexpr int kOffV = kC * DK * sizeof(T), kOffQ = kOffV + kC * DV * sizeof(T);
   constexpr int kOffW = kOffQ + (kOut ? kC * DK * (int)sizeof(T) : 0);
@@ -677,6 +672,31 @@ __global__ __launch_bounds__(64 * NW * (kPair ? 2 : 1),
   }
 }
 
+// Two waves a SIMD need half the register file each; fp32 tiles leave LDS for one.
+template <typename T>
+constexpr int kMinWaves = sizeof(T) == 2 ? 2 : 1;
+
+template <typename T, int DK, int NW, int kTerms, bool kF32Out = false, bool kPair = false>
+__global__ __launch_bounds__(64 * NW * (kPair ? 2 : 1), kMinWaves<T>) void linattn_main_kernel(
+    LinArgs a, float4* seg, int seg_len, int nseg) {
+  chunked_pass<T, DK, NW, true, kTerms, kF32Out, kPair>(a, seg, seg_len, nseg);
+}
+
+// The ends of one or two passes' segments (gridDim.y), one region of slots each.
+struct LinTwo {
+  LinArgs a[2];
+};
+template <typename T, int DK, int NW, int kTerms>
+__global__ __launch_bounds__(64 * NW, kMinWaves<T>) void linattn_ends_kernel(LinTwo two,
+                                                                             float4* seg,
+                                                                             int seg_len,
+                                                                             int nseg) {
+  const LinArgs& a = two.a[blockIdx.y];
+  const int64_t region = a.B * a.H * nseg * (DK * NW * 32 / 4);
+  chunked_pass<T, DK, NW, false, kTerms, false, false>(a, seg + blockIdx.y * region, seg_len,
+                                                       nseg);
+}
+
 // seg[head][g] <- seg[head][g] + g^seg_len seg[head][g - 1] along the segments, so
 // that every slot is the state its segment starts from.  Slots of segments
 // behind a sequence's end are not used.
@@ -827,23 +847,30 @@ Split split(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
   return p;
 }
 
+// The states that the segments of `count` passes start from.
 template <typename T, int DK, int NW, int kTerms>
-hipError_t chunked(const LinArgs& a, float4* seg, const Split& p, hipStream_t s) {
-  const int64_t heads = a.B * a.H;
-  if (p.nseg > 1 && !a.seg_trans) {
-    linattn_chunked_kernel<T, DK, NW, false, kTerms>
-        <<<dim3((unsigned)(heads * (p.nseg - 1))), 64 * NW, 0, s>>>(a, seg, p.seg_len, p.nseg);
-    hipError_t e = hipGetLastError();
+hipError_t starts(const LinArgs* a, int count, float4* seg, const Split& p, hipStream_t s) {
+  if (p.nseg == 1) return hipSuccess;
+  const int64_t heads = a->B * a->H;
+  LinTwo two{{a[0], a[count - 1]}};
+  linattn_ends_kernel<T, DK, NW, kTerms>
+      <<<dim3((unsigned)(heads * (p.nseg - 1)), count), 64 * NW, 0, s>>>(two, seg, p.seg_len,
+                                                                        p.nseg);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.nseg <= kScanInPlace) return e;
+  const int64_t slot4 = DK * 32 * NW / 4, total = count * heads * slot4;
+  linattn_scan_kernel<<<dim3((unsigned)((total + 63) / 64)), 64, 0, s>>>(
+      seg, a->log_decay, a->H, slot4, total, p.seg_len, p.nseg);
+  return hipGetLastError();
+}
+
+template <typename T, int DK, int NW, int kTerms>
+hipError_t main_pass(const LinArgs& a, float4* seg, const Split& p, hipStream_t s) {
+  if (!a.seg_ready && !a.seg_trans) {
+    const hipError_t e = starts<T, DK, NW, kTerms>(&a, 1, seg, p, s);
     if (e != hipSuccess) return e;
-    if (p.nseg > kScanInPlace) {
-      const int64_t slot4 = DK * 32 * NW / 4, total = heads * slot4;
-      linattn_scan_kernel<<<dim3((unsigned)((total + 63) / 64)), 64, 0, s>>>(
-          seg, a.log_decay, a.H, slot4, total, p.seg_len, p.nseg);
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
   }
-  const dim3 grid((unsigned)(heads * p.nseg));
+  const dim3 grid((unsigned)(a.B * a.H * p.nseg));
   float4* start = p.nseg > 1 ? seg : nullptr;
   // fp32 outputs of bf16 passes are gradients on their way to a sum over heads,
   // which come from a pair where the tiles are of one size
@@ -851,10 +878,10 @@ hipError_t chunked(const LinArgs& a, float4* seg, const Split& p, hipStream_t s)
   if (a.pair) {
     if constexpr (kBf16 && kSquare && kTerms == 3) {
       if (a.out_f32)
-        linattn_chunked_kernel<T, DK, NW, true, kTerms, true, true>
+        linattn_main_kernel<T, DK, NW, kTerms, true, true>
             <<<grid, 128 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
       else
-        linattn_chunked_kernel<T, DK, NW, true, kTerms, false, true>
+        linattn_main_kernel<T, DK, NW, kTerms, false, true>
             <<<grid, 128 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
       return hipGetLastError();
     }
@@ -862,32 +889,35 @@ hipError_t chunked(const LinArgs& a, float4* seg, const Split& p, hipStream_t s)
   }
   if (kBf16 && a.out_f32) {
     if constexpr (kBf16 && !kSquare) {
-      linattn_chunked_kernel<T, DK, NW, true, kTerms, true>
+      linattn_main_kernel<T, DK, NW, kTerms, true>
           <<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
       return hipGetLastError();
     }
     return hipErrorInvalidValue;
   }
-  linattn_chunked_kernel<T, DK, NW, true, kTerms>
-      <<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
+  linattn_main_kernel<T, DK, NW, kTerms><<<grid, 64 * NW, 0, s>>>(a, start, p.seg_len, p.nseg);
   return hipGetLastError();
 }
 
-template <typename T, int kTerms>
-hipError_t chunked_shape(const LinArgs& a, float4* seg, hipStream_t s) {
-  const Split p = split(a.B, a.H, a.T, a.dk, a.dv);
-  if (a.dk <= 64)
-    return a.dv <= 64 ? chunked<T, 64, 2, kTerms>(a, seg, p, s)
-                      : chunked<T, 64, 4, kTerms>(a, seg, p, s);
-  return a.dv <= 64 ? chunked<T, 128, 2, kTerms>(a, seg, p, s)
-                    : chunked<T, 128, 4, kTerms>(a, seg, p, s);
+// Calls f with the pass's type, tile sizes and terms as constants.
+template <typename F>
+hipError_t with_tiles(const LinArgs& a, F&& f) {
+  const auto tiles = [&](auto t, auto terms) {
+    using std::integral_constant;
+    if (a.dk <= 64)
+      return a.dv <= 64 ? f(t, integral_constant<int, 64>{}, integral_constant<int, 2>{}, terms)
+                        : f(t, integral_constant<int, 64>{}, integral_constant<int, 4>{}, terms);
+    return a.dv <= 64 ? f(t, integral_constant<int, 128>{}, integral_constant<int, 2>{}, terms)
+                      : f(t, integral_constant<int, 128>{}, integral_constant<int, 4>{}, terms);
+  };
+  if (a.dt == Dtype::F32) return tiles(float{}, std::integral_constant<int, 1>{});
+  return a.exact_state ? tiles(uint16_t{}, std::integral_constant<int, 3>{})
+                       : tiles(uint16_t{}, std::integral_constant<int, 2>{});
 }
 
 }  // namespace
 
-bool linattn_pairs(int64_t dk, int64_t dv, Dtype dt) {
-  return dt == Dtype::BF16 && padded(dk) == padded(dv);
-}
+bool linattn_square(int64_t dk, int64_t dv) { return padded(dk) == padded(dv); }
 
 size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
   const Split p = split(B, H, T, dk, dv);
@@ -895,11 +925,19 @@ size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_
   return (size_t)(B * H * p.nseg) * padded(dk) * padded(dv) * sizeof(float);
 }
 
+hipError_t launch_linattn_starts(const LinArgs* a, int count, float* seg, hipStream_t s) {
+  return with_tiles(*a, [&](auto t, auto dk, auto nw, auto terms) {
+    return starts<decltype(t), decltype(dk)::value, decltype(nw)::value, decltype(terms)::value>(
+        a, count, reinterpret_cast<float4*>(seg), split(a->B, a->H, a->T, a->dk, a->dv), s);
+  });
+}
+
 hipError_t launch_linattn_chunked(const LinArgs& a, float* seg, hipStream_t s) {
-  float4* slots = reinterpret_cast<float4*>(seg);
-  if (a.dt == Dtype::F32) return chunked_shape<float, 1>(a, slots, s);
-  return a.exact_state ? chunked_shape<uint16_t, 3>(a, slots, s)
-                       : chunked_shape<uint16_t, 2>(a, slots, s);
+  return with_tiles(a, [&](auto t, auto dk, auto nw, auto terms) {
+    return main_pass<decltype(t), decltype(dk)::value, decltype(nw)::value,
+                     decltype(terms)::value>(a, reinterpret_cast<float4*>(seg),
+                                             split(a.B, a.H, a.T, a.dk, a.dv), s);
+  });
 }
 
 hipError_t launch_linattn_step(const LinArgs& a, hipStream_t s) {
