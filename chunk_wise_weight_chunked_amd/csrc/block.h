@@ -79,7 +79,7 @@ struct LinArgs {
 // exchanged can then share launches (bf16 passes with LinArgs::pair too).
 bool linattn_square(int64_t dk, int64_t dv);
 // Bytes of the states that a chunked pass keeps between its launches (0: none).
-size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv);
+size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv, Dtype dt);
 hipError_t launch_linattn_chunked(const LinArgs& a, float* seg, hipStream_t s);
 // The segments' states of one or two passes of the same tiles and exact_state,
 // pass i's at i times linattn_segment_bytes behind seg.

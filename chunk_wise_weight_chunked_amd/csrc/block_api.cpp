@@ -167,7 +167,7 @@ bool recurrent(const ttt_linattn_desc_t* d) { return d->seq_len <= ttt::kLinStep
 size_t forward_bytes(const ttt_linattn_desc_t* d) {
   return recurrent(d) ? 0
                       : ttt::linattn_segment_bytes(d->batch, d->heads, d->seq_len, d->d_key,
-                                                   d->d_value);
+                                                   d->d_value, to_dtype(d->dtype));
 }
 
 // Backward workspace: the segments' states of dq's pass, behind them those of
@@ -179,7 +179,8 @@ struct BackwardPlan {
 };
 BackwardPlan backward_plan(const ttt_linattn_desc_t* d) {
   BackwardPlan p;
-  p.seg_bytes = ttt::linattn_segment_bytes(d->batch, d->heads, d->seq_len, d->d_key, d->d_value);
+  p.seg_bytes = ttt::linattn_segment_bytes(d->batch, d->heads, d->seq_len, d->d_key, d->d_value,
+                                           to_dtype(d->dtype));
   p.dv_off = align256(p.seg_bytes * (ttt::linattn_square(d->d_key, d->d_value) ? 2 : 1));
   const size_t rows = d->heads == d->kv_heads ? 0 : (size_t)(d->batch * d->heads * d->seq_len);
   p.dk_off = p.dv_off + align256(rows * d->d_value * sizeof(float));

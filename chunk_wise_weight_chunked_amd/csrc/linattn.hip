@@ -22,13 +22,21 @@
 // A 32x32 result holds rows 8 (r / 4) + 4 (lane / 32) + r % 4 in registers r,
 // an operand wants 8 consecutive k values 8 (lane / 32) + 0..7: the rows of
 // the A operands are fed in an order with bits 2 and 3 of the index swapped
-// (perm below), which makes registers 0..7 and 8..15 of a result exactly these
+// (perm16 below), which makes registers 0..7 and 8..15 of a result exactly these
 // runs.
 //
 // Few heads leave most CUs without work, so a sequence is split into segments
 // (split() below): one pass computes every segment's end state from K and V
 // alone, one adds them up along the sequence, and the main pass starts each
-// segment from its state.
+// segment from its state.  A chunk of 32 tokens needs no larger intermediate
+// than one 32x32 tile of scores a wave, and leaves two workgroups a CU; 64
+// tokens would halve the state's conversions but need 96 KB of LDS a workgroup.
+//
+// What bounds it: 131072 tokens x 20 heads of 128 in bf16 take 830 us; reading q,
+// k and v and writing o is 2.7 GB (540 us at a copy's rate).  The ends' pass
+// reads K and V a second time (250 us), the main pass runs at 4.5 to 4.7 TB/s.
+// Back to back the clock falls to 1.7 from 2.2 GHz, which then costs more than
+// any one of the remaining waits: without loads the same passes take 600 us.
 //
 // Rounding (bf16 operands): the decayed scores and the state's copy that
 // meets Q are rounded to bf16 once, like any bf16 operand of a product whose
@@ -827,19 +835,22 @@ __global__ __launch_bounds__(256) void linattn_sum_heads_kernel(
 int64_t padded(int64_t d) { return d <= 64 ? 64 : 128; }
 
 // How a pass splits sequences into segments of whole chunks: into as many as
-// have their workgroups resident together (two waves a SIMD on 256 CUs), of two
-// chunks at least.  Twice as many segments cost more in states than they gain
-// (backward over 32768 tokens, 20 heads of 128: 629 us with 2048 waves, 716 us
-// with 4096); one segment of 128 tokens at least leaves small calls slower (4
-// heads, 1024 tokens, fp32: 29 us, 37 us).
-constexpr int64_t kResidentWaves = 2048, kMinSegment = 64;
+// have their workgroups resident together (256 CUs, two waves a SIMD in bf16 and
+// one in fp32, whose tiles leave LDS for no more), of two chunks at least.  More
+// of them cost more in states than they gain: gradients of 32768 tokens, 20
+// heads of 128, bf16: 629 us with 2048 waves, 716 us with 4096; 4096 tokens, 16
+// heads of 64, fp32: 112 us with 1024, 148 us with 2048 (32768 tokens, 20 heads
+// of 128 the other way round, 2.46 and 2.37 ms).  At least 128 tokens a segment
+// are slower for small calls (1024 tokens, 4 heads, fp32: 37 us, 29 us).
+constexpr int64_t kResidentWavesBf16 = 2048, kResidentWavesF32 = 1024, kMinSegment = 64;
 struct Split {
   int seg_len, nseg;
 };
 
-Split split(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
+Split split(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv, Dtype dt) {
   const int64_t heads = B * H, waves = std::max(padded(dk), padded(dv)) / 32;
-    int64_t nseg = std::max<int64_t>(1, std::min<int64_t>(kResidentWaves / waves / heads, T / kMinSegment));
+  const int64_t resident = dt == Dtype::BF16 ? kResidentWavesBf16 : kResidentWavesF32;
+  const int64_t nseg = std::max<int64_t>(1, std::min(resident / waves / heads, T / kMinSegment));
   // whole chunks per segment may need fewer segments
   Split p;
   p.seg_len = (int)(((T + nseg - 1) / nseg + kC - 1) / kC * kC);
@@ -919,8 +930,8 @@ hipError_t with_tiles(const LinArgs& a, F&& f) {
 
 bool linattn_square(int64_t dk, int64_t dv) { return padded(dk) == padded(dv); }
 
-size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv) {
-  const Split p = split(B, H, T, dk, dv);
+size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_t dv, Dtype dt) {
+  const Split p = split(B, H, T, dk, dv, dt);
   if (p.nseg == 1) return 0;
   return (size_t)(B * H * p.nseg) * padded(dk) * padded(dv) * sizeof(float);
 }
@@ -928,7 +939,7 @@ size_t linattn_segment_bytes(int64_t B, int64_t H, int64_t T, int64_t dk, int64_
 hipError_t launch_linattn_starts(const LinArgs* a, int count, float* seg, hipStream_t s) {
   return with_tiles(*a, [&](auto t, auto dk, auto nw, auto terms) {
     return starts<decltype(t), decltype(dk)::value, decltype(nw)::value, decltype(terms)::value>(
-        a, count, reinterpret_cast<float4*>(seg), split(a->B, a->H, a->T, a->dk, a->dv), s);
+        a, count, reinterpret_cast<float4*>(seg), split(a->B, a->H, a->T, a->dk, a->dv, a->dt), s);
   });
 }
 
@@ -936,7 +947,7 @@ hipError_t launch_linattn_chunked(const LinArgs& a, float* seg, hipStream_t s) {
   return with_tiles(a, [&](auto t, auto dk, auto nw, auto terms) {
     return main_pass<decltype(t), decltype(dk)::value, decltype(nw)::value,
                      decltype(terms)::value>(a, reinterpret_cast<float4*>(seg),
-                                             split(a.B, a.H, a.T, a.dk, a.dv), s);
+                                             split(a.B, a.H, a.T, a.dk, a.dv, a.dt), s);
   });
 }
 
