@@ -100,19 +100,13 @@ def _current(stream, like):
     return _stream(stream)
 
 
-def _on_stream(fn):
+def _on(stream):
     """A tensor-level call with stream=s allocates on s as well: its outputs and its workspace
     are that stream's, so no other stream's allocation can take their memory while s still
     works on it."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 # ------------------------------------------------ residual addition and norm
@@ -179,8 +173,8 @@ def _norm_checks(x, res, w, what):
         raise ValueError(f"the residual must have {what}'s shape and its type or float32")
 
 
-@_on_stream
-def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_out=None):
+def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_out=None,
+                stream=None):
     """r = x + res, y = r / sqrt(mean(r^2) + eps) * weight over the last dimension.
 
     x [..., d] bf16 or fp32 (2-dimensional with any row stride, or contiguous), weight [d] of
@@ -188,6 +182,9 @@ def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_o
     (written to r_out if given, which may be res itself; None without a residual); y has x's type and scale is None, or with
     out_dtype=torch.float8_e4m3fn y is 8-bit and scale holds one fp32 value for each row, or
     for each 128 values of a row (scale_group=128): y * scale is the norm."""
+    if stream is not None:
+        with _on(stream):
+            return add_rmsnorm(x, res, weight, eps, out_dtype, scale_group, r_out)
     _norm_checks(x, res, weight, "x")
     _same_device(x, res, weight, r_out)
     fp8 = out_dtype is torch.float8_e4m3fn
@@ -214,12 +211,14 @@ def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_o
     return y, r, scale
 
 
-@_on_stream
-def add_rmsnorm_backward(dy, r, weight, eps=NORM_EPS, dr=None):
+def add_rmsnorm_backward(dy, r, weight, eps=NORM_EPS, dr=None, stream=None):
     """Gradients of <dy, y> + <dr, r> for y = norm(r) * weight: r is add_rmsnorm's (x itself where
     it had no residual), dr the gradient that reaches r from its other uses, or None.  Returns
     (dr, dx, dweight): the gradient of the sum in r's type, the same in dy's type (the same
     tensor where the types are equal), and the fp32 gradient of the weight."""
+    if stream is not None:
+        with _on(stream):
+            return add_rmsnorm_backward(dy, r, weight, eps, dr)
     _norm_checks(dy, r, weight, "dy")
     _same_device(dy, r, weight, dr)
     if dr is not None and (dr.shape != r.shape or dr.dtype != r.dtype):
@@ -320,9 +319,8 @@ def _linattn_checks(q, k, v, log_decay, lengths, *states):
     _same_device(q, k, v, log_decay, lengths, *states)
 
 
-@_on_stream
 def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, lengths=None,
-                    ws=None):
+                    ws=None, stream=None):
     """S_t = exp(log_decay) S_{t-1} + k_t v_t^T, o_t = scale q_t S_t for each head.
 
     q [B][T][H][dk], k [B][T][G][dk], v [B][T][G][dv] (bf16 or fp32; any strides in multiples
@@ -330,6 +328,9 @@ def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, 
     [B][H][dk][dv] fp32 or None (zeros), lengths [B] int32 or None.  scale: dk^-0.5 unless
     given.  Returns (o [B][T][H][dv], the state behind the last token); pass
     state_out=state to update a session's state in place."""
+    if stream is not None:
+        with _on(stream):
+            return linattn_forward(q, k, v, log_decay, scale, state, state_out, lengths, ws)
     desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
                                None, q.dtype, scale, False)
     _linattn_checks(q, k, v, log_decay, lengths, state, state_out)
@@ -344,12 +345,14 @@ def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, 
     return o, state_out
 
 
-@_on_stream
 def linattn_backward(q, k, v, log_decay, dO, scale=None, state=None, dstate_out=None,
-                     lengths=None, ws=None) -> dict:
+                     lengths=None, ws=None, stream=None) -> dict:
     """Gradients of <dO, o> + <dstate_out, final state> for linattn_forward from `state`.
     Returns a dict: q, k, v (their shapes, contiguous) and state (fp32; None when no state was
     given)."""
+    if stream is not None:
+        with _on(stream):
+            return linattn_backward(q, k, v, log_decay, dO, scale, state, dstate_out, lengths, ws)
     desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
                                dO.stride(), q.dtype, scale, True)
     _linattn_checks(q, k, v, log_decay, lengths, state, dstate_out)

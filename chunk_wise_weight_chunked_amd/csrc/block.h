@@ -87,9 +87,10 @@ hipError_t launch_linattn_starts(const LinArgs* a, int count, float* seg, hipStr
 // The recurrent form, T <= kLinStepTokens (forward direction, late = 1, out in
 // the operands' type).
 hipError_t launch_linattn_step(const LinArgs& a, hipStream_t s);
-// out[b][t][g][:] = sum over r < rep of part[b][g rep + r][t][:] (fp32).
-hipError_t launch_linattn_sum_heads(const float* part, void* out, int64_t osb, int64_t ost,
-                                    int64_t osh, int64_t B, int64_t T, int64_t G, int64_t rep,
-                                    int64_t d, Dtype dt, hipStream_t s);
+// dk [B][T][G][d_key] and dv [B][T][G][d_value] as the sums of their rep query
+// heads' parts, [B][G rep][T][d] fp32, in head order.
+hipError_t launch_linattn_sum_heads(const float* part_k, void* dk, int64_t d_key,
+                                    const float* part_v, void* dv, int64_t d_value, int64_t B,
+                                    int64_t T, int64_t G, int64_t rep, Dtype dt, hipStream_t s);
 
 }  // namespace ttt

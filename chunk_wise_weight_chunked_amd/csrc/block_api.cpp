@@ -430,15 +430,10 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
     run(ak, nullptr);  // reads dstate_out, which dv's pass may replace
     run(av, nullptr);
   }
-  if (shared_heads) {
-    const auto sum = [&](const Out& part, void* out, int64_t d) {
-      if (e == hipSuccess)
-        e = ttt::launch_linattn_sum_heads(static_cast<const float*>(part.p), out, T * G * d, G * d,
-                                          d, B, T, G, rep, d, dt, s);
-    };
-    sum(out_v, dv, V);
-    sum(out_k, dk, K);
-  }
+  if (shared_heads && e == hipSuccess)
+    e = ttt::launch_linattn_sum_heads(static_cast<const float*>(out_k.p), dk, K,
+                                      static_cast<const float*>(out_v.p), dv, V, B, T, G, rep, dt,
+                                      s);
   return e == hipSuccess ? ok() : hip_fail(e, "linattn_backward");
 }
 

@@ -813,23 +813,30 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(LinArgs a) {
   }
 }
 
+// out[b][t][g][:] = sum over r < rep of part[b][g rep + r][t][:], a tensor for
+// each blockIdx.y.
+struct HeadSums {
+  const float* part[2];
+  void* out[2];
+  int64_t d[2];
+};
 template <typename T>
-__global__ __launch_bounds__(256) void linattn_sum_heads_kernel(
-    const float* __restrict__ part, T* __restrict__ out, int64_t osb, int64_t ost, int64_t osh,
-    int64_t B, int64_t T_, int64_t G, int64_t rep, int64_t d) {
-  const int64_t pieces = d >> 3;
+__global__ __launch_bounds__(256) void linattn_sum_heads_kernel(HeadSums h, int64_t B, int64_t T_,
+                                                                int64_t G, int64_t rep) {
+  const int y = blockIdx.y;
+  const int64_t d = h.d[y], pieces = d >> 3;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= B * G * T_ * pieces) return;
   const int64_t c = (i % pieces) * 8, t = i / pieces % T_, g = i / (pieces * T_) % G,
                 b = i / (pieces * T_ * G);
   float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (int64_t r = 0; r < rep; ++r) {
-    const float* p = part + (((b * G + g) * rep + r) * T_ + t) * d + c;
-    const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+    const float* p = h.part[y] + (((b * G + g) * rep + r) * T_ + t) * d + c;
+    const float4 x = *reinterpret_cast<const float4*>(p), z = *reinterpret_cast<const float4*>(p + 4);
     f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w;
-    f[4] += y.x, f[5] += y.y, f[6] += y.z, f[7] += y.w;
+    f[4] += z.x, f[5] += z.y, f[6] += z.z, f[7] += z.w;
   }
-  store8(out + b * osb + t * ost + g * osh + c, f);
+  store8(static_cast<T*>(h.out[y]) + ((b * T_ + t) * G + g) * d + c, f);
 }
 
 int64_t padded(int64_t d) { return d <= 64 ? 64 : 128; }
@@ -961,17 +968,16 @@ hipError_t launch_linattn_step(const LinArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_linattn_sum_heads(const float* part, void* out, int64_t osb, int64_t ost,
-                                    int64_t osh, int64_t B, int64_t T, int64_t G, int64_t rep,
-                                    int64_t d, Dtype dt, hipStream_t s) {
-  const int64_t n = B * G * T * (d / 8);
-  const dim3 grid((unsigned)((n + 255) / 256));
+hipError_t launch_linattn_sum_heads(const float* part_k, void* dk, int64_t d_key,
+                                    const float* part_v, void* dv, int64_t d_value, int64_t B,
+                                    int64_t T, int64_t G, int64_t rep, Dtype dt, hipStream_t s) {
+  const HeadSums h{{part_k, part_v}, {dk, dv}, {d_key, d_value}};
+  const int64_t n = B * G * T * (std::max(d_key, d_value) / 8);
+  const dim3 grid((unsigned)((n + 255) / 256), 2);
   if (dt == Dtype::BF16)
-    linattn_sum_heads_kernel<uint16_t><<<grid, 256, 0, s>>>(part, static_cast<uint16_t*>(out), osb,
-                                                            ost, osh, B, T, G, rep, d);
+    linattn_sum_heads_kernel<uint16_t><<<grid, 256, 0, s>>>(h, B, T, G, rep);
   else
-    linattn_sum_heads_kernel<float><<<grid, 256, 0, s>>>(part, static_cast<float*>(out), osb, ost,
-                                                         osh, B, T, G, rep, d);
+    linattn_sum_heads_kernel<float><<<grid, 256, 0, s>>>(h, B, T, G, rep);
   return hipGetLastError();
 }
 

@@ -5,12 +5,14 @@ GPU tests compare with are checked here against differences."""
 import ctypes
 import os
 import re
+import subprocess
 
 import numpy as np
 import pytest
 import torch
 
 from chunk_wise_weight_chunked_amd import block
+from chunk_wise_weight_chunked_amd import build as hipbuild
 from chunk_wise_weight_chunked_amd import ttt_mlp as tm
 
 import _block_ref as ref
@@ -286,3 +288,46 @@ def test_attention_reference_against_differences():
         hi, lo = list(a), list(a)
         hi[i], lo[i] = a[i] + u, a[i] - u
         assert abs((f(*hi) - f(*lo)) / 2 - (g * u).sum()) < 1e-9 * max(1, np.abs(g * u).sum())
+
+
+# ---------------------------------------------------- the waits of the compiled kernels
+VMEM = re.compile(r"^\s*(buffer|global|flat|scratch)_(load|store|atomic)\w*")
+
+
+@pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="hipcc not available")
+def test_no_load_into_lds_is_in_flight_at_a_barrier(tmp_path):
+    """The chunked kernels fill LDS tiles by direct loads and let other waves read them after a
+    barrier: in the gfx950 code that hipcc makes, every barrier of such a kernel has vmcnt(0)
+    in front of it with no vector memory operation in between."""
+    src = os.path.join(hipbuild.CSRC, "linattn.hip")
+    out = tmp_path / "linattn.s"
+    cmd = ["/opt/rocm/bin/hipcc", f"--offload-arch={hipbuild.ARCH}", "-O3", "-std=c++17",
+           "--cuda-device-only", "-S", "-Xclang", "-target-feature", "-Xclang",
+           "-packed-fp32-ops", src, "-o", str(out)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    functions, name = {}, None
+    for line in out.read_text().splitlines():
+        m = re.match(r"^(_Z\w+):", line)
+        if m:
+            name = m.group(1)
+            functions[name] = []
+        elif line.startswith(".Lfunc_end"):
+            name = None
+        elif name:
+            functions[name].append(line)
+    checked = 0
+    for name, lines in functions.items():
+        if not any("buffer_load" in x and x.rstrip().endswith("lds") for x in lines):
+            continue
+        assert not any("scratch_" in x for x in lines), name  # nothing spilled either
+        for i, x in enumerate(lines):
+            if "s_barrier" not in x:
+                continue
+            j = i - 1
+            while not re.search(r"s_waitcnt.*vmcnt\(0\)", lines[j]):
+                assert not VMEM.match(lines[j]), (name, lines[j])
+                assert not re.match(r"^\.LBB", lines[j]), (name, "no wait in the barrier's block")
+                j -= 1
+            checked += 1
+    assert checked >= 2 * 20, checked
