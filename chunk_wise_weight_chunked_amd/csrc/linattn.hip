@@ -32,9 +32,10 @@
 // than one 32x32 tile of scores a wave, and leaves two workgroups a CU; 64
 // tokens would halve the state's conversions but need 96 KB of LDS a workgroup.
 //
-// What bounds it: 131072 tokens x 20 heads of 128 in bf16 take 830 us; reading q,
-// k and v and writing o is 2.7 GB (540 us at a copy's rate).  The ends' pass
-// reads K and V a second time (250 us), the main pass runs at 4.5 to 4.7 TB/s.
+// What bounds it: 131072 tokens x 20 heads of 128 in bf16 take 838 us; reading q,
+// k and v and writing o is 2.7 GB (540 us at a copy's rate).  Traced, the ends'
+// pass takes 317 us (0.85 of K's and V's 1.34 GB, the rest has decayed to 0), the
+// sums over segments 13 us and the main pass 595 us (4.5 TB/s).
 // Back to back the clock falls to 1.7 from 2.2 GHz, which then costs more than
 // any one of the remaining waits: without loads the same passes take 600 us.
 //
