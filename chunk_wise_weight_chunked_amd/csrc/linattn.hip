@@ -187,6 +187,30 @@ struct Frag<uint16_t> {
     f[0] = join(x[0], x[1]);
     f[1] = join(x[2], x[3]);
   }
+  // 0, or NaN where a value is not finite
+  __device__ __forceinline__ static float not_finite(const Frag (&f)[2]) {
+    const bf16x2_t zero = {static_cast<__bf16>(0.0f), static_cast<__bf16>(0.0f)};
+    float acc[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t x = __builtin_bit_cast(u32x4_t, f[s].v)[e];
+        acc[s] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, x), zero, acc[s], false);
+      }
+    return acc[0] + acc[1];
+  }
+  __device__ __forceinline__ bool is_finite(int e) const {
+    const uint32_t x = __builtin_bit_cast(u32x4_t, v)[e / 2];
+    return (~(x >> 16 * (e & 1)) & 0x7f80u) != 0;
+  }
+  __device__ __forceinline__ void finite() {  // 0 for the values that are not
+    u32x4_t x = __builtin_bit_cast(u32x4_t, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (!is_finite(e)) x[e / 2] &= e & 1 ? 0xffffu : 0xffff0000u;
+    v = __builtin_bit_cast(bf16x8_t, x);
+  }
   // registers 8 half .. of a result
   __device__ __forceinline__ static Frag result(const floatx16_t& c, int half) {
     uint32_t w[4];
@@ -227,6 +251,21 @@ struct Frag<float> {
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = cols(t, 32 * i, step, lane);
   }
+  __device__ __forceinline__ static float not_finite(const Frag (&f)[2]) {
+    float acc[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) acc[s] = fmaf(f[s].v[e], 0.0f, acc[s]);
+    return acc[0] + acc[1];
+  }
+  __device__ __forceinline__ bool is_finite(int e) const {
+    return (~__float_as_uint(v[e]) & 0x7f800000u) != 0;
+  }
+  __device__ __forceinline__ void finite() {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = is_finite(e) ? v[e] : 0.0f;
+  }
   __device__ __forceinline__ static Frag result(const floatx16_t& c, int half) {
     Frag f;
 #pragma unroll
@@ -266,6 +305,14 @@ __device__ __forceinline__ void weighted(Frag<float> (&out)[1], const Frag<float
                                          const float* w, int e) {
   out[0].v[2 * e] = v.v[2 * e] * w[2 * e];
   out[0].v[2 * e + 1] = v.v[2 * e + 1] * w[2 * e + 1];
+}
+
+template <typename T>
+__device__ __forceinline__ T nan_of() {
+  if constexpr (sizeof(T) == 2)
+    return 0x7fc0;  // bf16
+  else
+    return __builtin_nanf("");
 }
 
 // 8 results in a row, to the operands' type or fp32.
@@ -567,6 +614,17 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
     Frag<T> wv[2][kTerms];  // the same weighted
     const auto weigh = [&](int pair) { weighted(wv[pair >> 2], vf[pair >> 2], w_up + 8 * (pair >> 2), pair & 3); };
     floatx16_t P, O;
+    // A masked score is 0, but 0 times an infinity or NaN is NaN: such a value of
+    // V would reach the tokens in front of its own.  The products leave it out;
+    // what it does reach is made NaN behind them.
+    bool odd = false;
+    if constexpr (kOut) {
+      odd = __builtin_amdgcn_ballot_w64(Frag<T>::not_finite(vf) != 0.0f) != 0;
+      if (__builtin_expect(odd, 0)) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) vf[s].finite();
+      }
+    }
     if constexpr (kOut) {
       // O = S^T Q^T and P^T = K Q^T.  A matrix instruction takes as long as eight
       // vector instructions: the weighting of V, the state's conversion and its
@@ -645,6 +703,31 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
                                  floatx4_t{O[8 * i + 4 * q], O[8 * i + 4 * q + 1],
                                            O[8 * i + 4 * q + 2], O[8 * i + 4 * q + 3]});
         }
+      }
+    }
+    if (__builtin_expect(odd, 0)) {
+      // recomputed here, not kept in registers through every chunk
+      uint32_t none = 0;
+      asm volatile("" : "+s"(none) : : "memory");  // and behind the stores above
+      const int l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, none));
+      const int hi = l >> 5, row = l & 31;
+      Frag<T> raw[2];
+      Frag<T>::cols2(raw, sV, 32 * wave, l);
+      int from = kC;  // the first token of the lane's value column that is not finite
+#pragma unroll
+      for (int r = 15; r >= 0; --r)
+        if (!raw[r >> 3].is_finite(r & 7)) from = 16 * (r >> 3) + 8 * hi + (r & 7);
+      from = min(from, __builtin_amdgcn_ds_bpermute((l ^ 32) * 4, from));
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[i][r] = from < kC ? __builtin_nanf("") : S[i][r];
+#pragma unroll 1
+      for (int c = 0; c < 32; ++c) {  // value column c, the lane's token
+        const int at = (32 * wave + c) * (int)sizeof(TO);
+        const int first_of_c = __builtin_amdgcn_readlane(from, perm16(c));
+        if (row >= first_of_c && hi == 0)
+          lds_store<TO>(out + out_at(row, at >> 4) + (at & 15), nan_of<TO>());
       }
     }
     wait_vmcnt<0>();  // the next chunk's tiles are here, the last one's outputs gone

@@ -122,7 +122,9 @@ ttt_status_t ttt_addnorm_backward(const ttt_addnorm_desc_t* desc, const void* dy
  *             rows behind them are not read, their outputs and gradients are 0,
  *             and the state stops at the last token.  A sequence of 0 tokens
  *             keeps its state.
- * States are fp32 [B][H][d_key][d_value], contiguous. */
+ * States are fp32 [B][H][d_key][d_value], contiguous.  An infinity or NaN reaches
+ * only the results that the formula gives it to, and may become NaN there; a
+ * token whose decay to a later one is 0 in fp32 may be left out of its result. */
 typedef struct {
   int64_t batch;
   int64_t seq_len;

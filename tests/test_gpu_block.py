@@ -323,6 +323,59 @@ def test_attention_decays():
                 assert rel(f64(got[name][:, :, h]), w[:, :, h]) <= TOL_CHUNK[dtype], (name, h)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [3, 29, 70, 600])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_attention_infinities_stay_behind_the_mask(T, bad, dtype):
+    """An infinity or NaN at token s reaches only the results that the formula gives it to: the
+    others are those of a call without it, bit for bit."""
+    H, G, dk, dv = 2, 1, 64, 72
+    g, q, k, v, _, st = attn_inputs(1, T, H, G, dk, dv, dtype, T)
+    lg = torch.tensor([-1e-3, -0.5], device="cuda")
+    dO, ds = normal(g, 1, T, H, dv, dtype=dtype), normal(g, 1, H, dk, dv)
+    names = ("q", "k", "v", "dO")
+    clean = dict(zip(names, (q, k, v, dO)))
+
+    def run(t):
+        o, S = block.linattn_forward(t["q"], t["k"], t["v"], lg, state=st)
+        d = block.linattn_backward(t["q"], t["k"], t["v"], lg, t["dO"], state=st, dstate_out=ds)
+        return {"o": o, "S": S, **{"d" + n: d[n] for n in "qkv"}, "dS": d["state"]}
+
+    want = run(clean)
+    assert all(torch.isfinite(t).all() for t in want.values())
+    before, after, own, others = (lambda s: slice(0, s)), (lambda s: slice(s + 1, T)), "own", "all"
+    # rows that a value of each input's token s does not reach
+    untouched = {
+        "q": {"o": own, "S": others, "dq": others, "dk": after, "dv": after},
+        "k": {"o": before, "dq": before, "dk": others, "dv": own, "dS": others},
+        "v": {"o": before, "dq": before, "dk": own, "dv": others, "dS": others},
+        "dO": {"o": others, "S": others, "dq": own, "dk": after, "dv": after},
+    }
+    for s in sorted({0, 1, T // 2, T - 1}):
+        for name in names:
+            t = dict(clean)
+            t[name] = clean[name].clone()
+            t[name][0, s, 0, 5] = bad
+            got = run(t)
+            say(T, dtype, bad, s, name)
+            for out, rows in untouched[name].items():
+                a, b = got[out], want[out]
+                if rows == own:
+                    keep = [i for i in range(T) if i != s]
+                    a, b = a[:, keep], b[:, keep]
+                elif rows != others:
+                    a, b = a[:, rows(s)], b[:, rows(s)]
+                assert torch.equal(a, b), (name, s, out)
+            if name == "v":  # one value of v is one column of o
+                keep = [c for c in range(dv) if c != 5]
+                assert torch.equal(got["o"][..., keep], want["o"][..., keep])
+                assert not torch.isfinite(got["o"][0, s:s + 8, 0, 5]).any()
+            if name == "k":
+                assert not torch.isfinite(got["o"][0, s:s + 8, 0]).any()
+            if name == "dO":
+                assert not torch.isfinite(got["dv"][0, max(0, s - 7):s + 1, 0, 5]).any()
+
+
 @pytest.mark.parametrize("T", [4, 70, 600])
 def test_attention_layouts(T):
     """Head-first storage, slices of one projection, a batch repeated by a stride of 0: as
