@@ -371,6 +371,9 @@ hipError_t with_types(const NormArgs& a, F&& f) {
 
 }  // namespace
 
+// A launch's threads are counted in 32 bits; calls of more rows take several.
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
+
 hipError_t launch_addnorm_forward(const NormArgs& a, const void* x, const void* res, const void* w,
                                   void* r, void* y, float* y_scale, hipStream_t s) {
   return with_types(a, [&](auto tx, auto tr) {
@@ -378,13 +381,22 @@ hipError_t launch_addnorm_forward(const NormArgs& a, const void* x, const void* 
     using TR = decltype(tr);
     return with_shape<false>(row_shape(a, false), [&](auto lpr, auto nv) {
       constexpr int L = decltype(lpr)::value, N = decltype(nv)::value;
-      const int64_t per = kBlock / L;
-      const dim3 grid((unsigned)((a.rows + per - 1) / per));
+      const int64_t per = kBlock / L, most = per * kMaxBlocks;
+      const int64_t ys = a.y_stride * (a.fp8 ? 1 : (int64_t)sizeof(TX));
+      const int64_t scales = a.grouped ? a.d / kNormScaleGroup : 1;
       const auto go = [&](auto kernel) {
-        kernel<<<grid, kBlock, 0, s>>>(static_cast<const TX*>(x), static_cast<const TR*>(res),
-                                       static_cast<const TX*>(w), static_cast<TR*>(r), y, y_scale,
-                                       a.rows, (int)a.d, a.x_stride, a.y_stride, a.eps, a.grouped);
-        return hipGetLastError();
+        for (int64_t at = 0; at < a.rows; at += most) {
+          const int64_t rows = std::min(a.rows - at, most);
+          kernel<<<dim3((unsigned)((rows + per - 1) / per)), kBlock, 0, s>>>(
+              static_cast<const TX*>(x) + at * a.x_stride,
+              res ? static_cast<const TR*>(res) + at * a.d : nullptr, static_cast<const TX*>(w),
+              r ? static_cast<TR*>(r) + at * a.d : nullptr, static_cast<char*>(y) + at * ys,
+              y_scale ? y_scale + at * scales : nullptr, rows, (int)a.d, a.x_stride, a.y_stride,
+              a.eps, a.grouped);
+          const hipError_t e = hipGetLastError();
+          if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
       };
       return a.fp8 ? go(addnorm_forward_kernel<TX, TR, true, L, N>)
                    : go(addnorm_forward_kernel<TX, TR, false, L, N>);

@@ -76,6 +76,9 @@ ttt_status_t norm_args(const ttt_addnorm_desc_t* d, ttt::NormArgs* a) {
     if (st % 8 || st > kMaxStride)
       return fail(TTT_ERR_UNSUPPORTED, "x_stride and y_stride must be multiples of 8, at most 2^40");
   }
+  for (int64_t st : {d->x_stride, d->y_stride})
+    if ((__int128)st * d->rows > ((__int128)1 << 56))
+      return fail(TTT_ERR_UNSUPPORTED, "a tensor must span less than 2^56 values");
   if (!std::isfinite(d->eps) || d->eps < 0)
     return fail(TTT_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
   if (d->out != TTT_NORM_SAME && d->out != TTT_NORM_FP8)
@@ -103,8 +106,9 @@ ttt_status_t linattn_dims(const ttt_linattn_desc_t* d) {
     return fail(TTT_ERR_INVALID_ARGUMENT, "batch, seq_len, heads and kv_heads must be >= 1");
   if (d->heads % d->kv_heads)
     return fail(TTT_ERR_INVALID_ARGUMENT, "heads must be a multiple of kv_heads");
-  if (d->heads > 65535 || d->batch > ((int64_t)1 << 24) / d->heads)
-    return fail(TTT_ERR_UNSUPPORTED, "heads must be <= 65535 and batch * heads <= 2^24");
+  // what one launch holds: its threads, up to 1024 for each head, are counted in 32 bits
+  if (d->heads > 65535 || d->batch > ((int64_t)1 << 21) / d->heads)
+    return fail(TTT_ERR_UNSUPPORTED, "heads must be <= 65535 and batch * heads <= 2^21");
   if (d->seq_len > ((int64_t)1 << 30) ||
       d->seq_len > ((int64_t)1 << 34) / (d->batch * d->heads))
     return fail(TTT_ERR_UNSUPPORTED, "seq_len must be <= 2^30 and batch * heads * seq_len <= 2^34");

@@ -33,7 +33,7 @@ extern "C" {
  * y is 0) and the stored value is y / scale rounded to nearest even, so that
  * stored * scale is y.  A NaN is stored as NaN and left out of the maximum.
  *
- *   rows      >= 1
+ *   rows      1 <= rows < 2^31
  *   d         a multiple of 8, 8 <= d <= 16384
  *   x_stride  values between rows of x (ttt_addnorm_forward) or dy (backward):
  *             a multiple of 8, >= d
@@ -100,7 +100,8 @@ ttt_status_t ttt_addnorm_backward(const ttt_addnorm_desc_t* desc, const void* dy
  * the layer's fast weight it is a sum of outer products kept in fp32 per
  * session, one per head and decayed per token.
  *
- *   batch, seq_len  B >= 1 sequences of T >= 1 tokens
+ *   batch, seq_len  B >= 1 sequences of T tokens, 1 <= T <= 2^30; B H <= 2^21,
+ *             B H T <= 2^34
  *   heads     H query heads, 1 <= H <= 65535
  *   kv_heads  G key / value heads, H a multiple of G: query head h reads
  *             key / value head h / (H / G); the state is per query head

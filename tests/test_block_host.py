@@ -70,6 +70,8 @@ BAD_NORM = [
     (dict(out=1, scale_group=64), INVALID, "scale_group"),
     (dict(scale_group=128), INVALID, "scale_group"),
     (dict(d=200, out=1, scale_group=128), UNSUPPORTED, "scale_group"),
+    (dict(rows=1 << 30, x_stride=1 << 40), UNSUPPORTED, "2^56"),
+    (dict(rows=1 << 30, y_stride=1 << 30), UNSUPPORTED, "2^56"),
 ]
 
 
@@ -148,6 +150,7 @@ BAD_ATTN = [
     (dict(kv_heads=3), INVALID, "multiple of kv_heads"),
     (dict(heads=65536, kv_heads=1), UNSUPPORTED, "65535"),
     (dict(batch=1 << 23), UNSUPPORTED, "batch * heads"),
+    (dict(batch=(1 << 19) + 1), UNSUPPORTED, "batch * heads"),
     (dict(seq_len=1 << 31), UNSUPPORTED, "seq_len"),
     (dict(seq_len=1 << 30, heads=64), UNSUPPORTED, "2^34"),
     (dict(d_key=0), INVALID, "d_key"),

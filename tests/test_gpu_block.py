@@ -117,6 +117,28 @@ def test_norm_strides_and_in_place():
     assert torch.equal(wide[:, :256], keep[:, :256]) and torch.equal(wide[:, 512:], keep[:, 512:])
 
 
+def test_norm_rows_beyond_one_launch():
+    """More rows than one launch's threads: the rows at the seams and the ends, every output."""
+    rows, d = (1 << 28) + 5, 8
+    x = torch.empty(rows, d, dtype=BF16, device="cuda").normal_()
+    res = torch.empty(rows, d, dtype=BF16, device="cuda").normal_()
+    w = normal(gen(4), d, dtype=BF16)
+    look = torch.cat([torch.arange(s - 40, s + 40) for s in (40, 1 << 27, 1 << 28)]
+                     + [torch.arange(rows - 9, rows)]).clamp(max=rows - 1).unique().cuda()
+    r64, y64 = ref.addnorm(f64(x[look]), f64(res[look]), f64(w), 1e-6)
+    y, r, scale = block.add_rmsnorm(x, res, w, out_dtype=FP8)
+    assert rel(f64(r[look]), r64) <= TOL_ROUND[BF16]
+    top = np.abs(y64).max(-1)
+    assert np.allclose(f64(scale[look]).reshape(-1), np.where(top > 0, top / 448.0, 1.0), rtol=2e-6, atol=0)
+    near = np.abs(f64(y[look].float()) * f64(scale[look]).reshape(-1, 1) - y64)
+    assert (near <= np.maximum(2.0 ** -4 * np.abs(y64), 2.0 ** -10 * top[:, None] / 448) * (1 + 1e-4)).all()
+    del y, scale, r, res
+    _, y64 = ref.addnorm(f64(x[look]), None, f64(w), 1e-6)
+    desc = block.make_addnorm_desc(rows, d, BF16)
+    block.ttt_addnorm_forward(desc, x, None, w, None, x)
+    assert rel(f64(x[look]), y64) <= TOL_ROUND[BF16]
+
+
 def test_norm_values_out_of_the_ordinary():
     x = torch.zeros(5, 256, device="cuda")
     x[1] = 3e19          # the sum of squares overflows: 1 / sqrt(inf) = 0
@@ -298,6 +320,23 @@ def test_attention_backward_against_differences():
         (fh, o, S), (fl, _, _) = f(hi), f(lo)
         size = float(dO.double().norm() * o.double().norm() + ds.double().norm() * S.double().norm())
         assert abs(float(fh - fl) / 2 - float((got[name].double() * u).sum())) <= TOL_F32 * size, name
+
+
+@pytest.mark.parametrize("T", [1, 5])
+@pytest.mark.parametrize("dv", [8, 128])
+def test_attention_most_heads(T, dv):
+    """The most heads a call may have, every sequence the same one: as a call of one sequence."""
+    B, H, dk = 1 << 17, 16, 8
+    _, q, k, v, lg, _ = attn_inputs(1, T, H, H, dk, dv, BF16, 3)
+    dO = normal(gen(6), 1, T, H, dv, dtype=BF16)
+    want, _ = block.linattn_forward(q, k, v, lg)
+    many = [t.expand(B, *t.shape[1:]) for t in (q, k, v)]
+    o, _ = block.linattn_forward(*many, lg)
+    assert (o == want).all()
+    if dv == 8:
+        d = block.linattn_backward(*many, lg, dO.expand(B, T, H, dv))
+        d1 = block.linattn_backward(q, k, v, lg, dO)
+        assert all((d[n] == d1[n]).all() for n in "qkv")
 
 
 def test_attention_decays():
