@@ -148,6 +148,8 @@ def _norm_plan(rows, d, x_stride, dtype, res_dtype, eps, fp8, scale_group):
 def _rows(t):
     """(rows, d, values between rows) of a tensor of rows; the rows may be apart."""
     d = t.shape[-1]
+    if d == 0:
+        raise ValueError("the rows have no values")
     if t.stride(-1) != 1 and d > 1:
         raise ValueError("the last dimension must be contiguous")
     if t.is_contiguous():
@@ -179,9 +181,10 @@ def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_o
 
     x [..., d] bf16 or fp32 (2-dimensional with any row stride, or contiguous), weight [d] of
     its type, res (or None) of its type or fp32.  Returns (y, r, scale).  r has res's type
-    (written to r_out if given, which may be res itself; None without a residual); y has x's type and scale is None, or with
-    out_dtype=torch.float8_e4m3fn y is 8-bit and scale holds one fp32 value for each row, or
-    for each 128 values of a row (scale_group=128): y * scale is the norm."""
+    (written to r_out if given, which may be res itself; None without a residual); y has x's
+    type and scale is None, or with out_dtype=torch.float8_e4m3fn y is 8-bit and scale holds one
+    fp32 value for each row, or for each 128 values of a row (scale_group=128): y * scale is the
+    norm."""
     if stream is not None:
         with _on(stream):
             return add_rmsnorm(x, res, weight, eps, out_dtype, scale_group, r_out)

@@ -263,7 +263,7 @@ def test_binding_refuses_tensors():
     for bad in (dict(x=x.double()), dict(weight=w[:32]), dict(weight=w.bfloat16()),
                 dict(res=x[:1]), dict(res=x.bfloat16()), dict(x=x.transpose(0, 1)),
                 dict(out_dtype=torch.bfloat16), dict(res=None, r_out=x), dict(x=x[:0], res=None),
-                dict()):
+                dict(x=x[..., :0], res=None, weight=w[:0]), dict()):
         with pytest.raises(ValueError):
             block.add_rmsnorm(**(dict(x=x, res=x, weight=w) | bad))
     with pytest.raises(ValueError):
