@@ -322,6 +322,35 @@ def test_attention_backward_against_differences():
         assert abs(float(fh - fl) / 2 - float((got[name].double() * u).sum())) <= TOL_F32 * size, name
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,T,H", [(2, 1030, 128), (2, 1024, 129), (7, 1100, 40), (16, 1030, 20),
+                                   (16, 1024, 32), (64, 1024, 16), (65, 1024, 4), (3, 2100, 60)])
+def test_attention_lengths_many_sequences(B, T, H, dtype):
+    """Batches whose workgroups are placed by the sequences' lengths: every sequence and head as
+    in a call of the sequence alone that has no lengths."""
+    say(B, T, H, dtype)
+    G, dk, dv = H // (2 if H % 2 == 0 else 1), 8, 16
+    g, q, k, v, lg, st = attn_inputs(B, T, H, G, dk, dv, dtype, B + T)
+    ln = torch.randint(0, T + 1, (B,), generator=g, dtype=torch.int32)
+    ln[0], ln[-1], ln[B // 2] = T, 0, int(ln[1])  # equal ones too
+    dO = normal(g, B, T, H, dv, dtype=dtype)
+    o, S = block.linattn_forward(q, k, v, lg, state=st, lengths=ln.cuda())
+    d = block.linattn_backward(q, k, v, lg, dO, state=st, lengths=ln.cuda())
+    for b in range(B):
+        n = int(ln[b])
+        assert (o[b, n:] == 0).all() and all((d[x][b, n:] == 0).all() for x in "qkv")
+        if n == 0:
+            assert torch.equal(S[b], st[b])
+            continue
+        one = [t[b:b + 1, :n].contiguous() for t in (q, k, v, dO)]
+        o1, S1 = block.linattn_forward(*one[:3], lg, state=st[b:b + 1])
+        d1 = block.linattn_backward(*one[:3], lg, one[3], state=st[b:b + 1])
+        pairs = [(o[b, :n], o1[0], TOL_CHUNK), (S[b], S1[0], TOL_STATE), (d["state"][b], d1["state"][0], TOL_STATE)]
+        pairs += [(d[x][b, :n], d1[x][0], TOL_CHUNK) for x in "qkv"]
+        for i, (got, want, tol) in enumerate(pairs):  # two results, each within its tolerance
+            assert rel(f64(got), f64(want)) <= 2 * tol[dtype], (b, n, i)
+
+
 @pytest.mark.parametrize("T", [1, 5])
 @pytest.mark.parametrize("dv", [8, 128])
 def test_attention_most_heads(T, dv):
