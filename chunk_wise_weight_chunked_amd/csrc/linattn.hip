@@ -32,10 +32,11 @@
 // than one 32x32 tile of scores a wave, and leaves two workgroups a CU; 64
 // tokens would halve the state's conversions but need 96 KB of LDS a workgroup.
 //
-// What bounds it: 131072 tokens x 20 heads of 128 in bf16 take 838 us; reading q,
-// k and v and writing o is 2.7 GB (540 us at a copy's rate).  Traced, the ends'
-// pass takes 317 us (0.85 of K's and V's 1.34 GB, the rest has decayed to 0), the
-// sums over segments 13 us and the main pass 595 us (4.5 TB/s).
+// What bounds it: 131072 tokens x 20 heads of 128 in bf16 take 832 us; reading q,
+// k and v and writing o is 2.7 GB (540 us at a copy's rate).  Traced (at a lower
+// clock, 970 us in all) the ends' pass takes 325 us (it reads 0.85 of K's and V's
+// 1.34 GB, the rest has decayed to 0), the sums over segments 12 and the main
+// pass 635.
 // Back to back the clock falls to 1.7 from 2.2 GHz, which then costs more than
 // any one of the remaining waits: without loads the same passes take 600 us.
 //
