@@ -88,6 +88,12 @@ __device__ __forceinline__ uint2 pack_fp8x8(const float f[8]) {
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
+// The scale that takes `top` to the largest 8-bit value; not below 2^-126, whose
+// reciprocal is still finite.
+__device__ __forceinline__ float fp8_scale(float top) {
+  return top > 0.0f ? fmaxf(top / kFp8Max, 0x1p-126f) : 1.0f;
+}
+
 template <typename TX, typename TR, bool kFp8, int LPR, int NV>
 __global__ __launch_bounds__(kBlock) void addnorm_forward_kernel(
     const TX* x, const TR* res, const TX* __restrict__ w, TR* r, void* y,
@@ -159,7 +165,7 @@ __global__ __launch_bounds__(kBlock) void addnorm_forward_kernel(
     };
     if (!grouped) {
       top = row_reduce<LPR, true>(top, red, 1);
-      const float scale = top > 0.0f ? top / kFp8Max : 1.0f;
+      const float scale = fp8_scale(top);
       if (lane == 0) y_scale[row] = scale;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -178,7 +184,7 @@ __global__ __launch_bounds__(kBlock) void addnorm_forward_kernel(
 #pragma unroll
         for (int m = 8; m >= 1; m >>= 1) t = fmaxf(t, __shfl_xor(t, m, 64));
         if (c < pieces) {
-          const float scale = t > 0.0f ? t / kFp8Max : 1.0f;
+          const float scale = fp8_scale(t);
           if ((lane & 15) == 0) y_scale[row * (d / kNormScaleGroup) + (c >> 4)] = scale;
           put(i, c, scale);
         }

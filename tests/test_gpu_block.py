@@ -103,6 +103,27 @@ def test_norm_fp8(rows, d, dtype, group):
     assert torch.equal(y[0].float(), torch.zeros(d, device="cuda"))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("group", [0, 128])
+def test_norm_fp8_smallest_values(group, dtype):
+    """Values whose scale would have no finite reciprocal: a run beside ordinary ones, a row."""
+    d = 256
+    x = torch.ones(3, d, device="cuda")
+    x[0, 128:] = torch.linspace(-1e-38, 1e-38, 128)
+    x[1, 128:] = 2.0 ** -133  # the smallest bf16
+    w = torch.ones(d, device="cuda")
+    for w in (w, w * 1e-38):
+        a, b = x.to(dtype), w.to(dtype)
+        y, _, scale = block.add_rmsnorm(a, None, b, out_dtype=FP8, scale_group=group)
+        _, y64 = ref.addnorm(f64(a), None, f64(b), 1e-6)
+        s = f64(scale)
+        y64, got = y64.reshape(3, s.shape[1], -1), f64(y.float()).reshape(3, s.shape[1], -1)
+        assert np.isfinite(got).all() and (s >= 2.0 ** -126).all()
+        # and fp32's own smallest step, on the values before the scale
+        bound = np.maximum(2.0 ** -4 * np.abs(y64), 2.0 ** -10 * s[..., None]) * (1 + 1e-4) + 2.0 ** -149
+        assert (np.abs(got * s[..., None] - y64) <= bound).all()
+
+
 def test_norm_strides_and_in_place():
     g = gen(3)
     wide = normal(g, 40, 3 * 256, dtype=BF16)
