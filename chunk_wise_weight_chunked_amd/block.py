@@ -100,12 +100,15 @@ def _current(stream, like):
     return _stream(stream)
 
 
-def _on(stream):
+def _on(stream, like):
     """A tensor-level call with stream=s allocates on s as well: its outputs and its workspace
     are that stream's, so no other stream's allocation can take their memory while s still
-    works on it."""
+    works on it.  A raw handle is a stream of the device of `like`."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        handle = int(stream)
+        # ExternalStream takes a null pointer as none given and makes a stream of its own
+        stream = (torch.cuda.ExternalStream(handle, device=like.device) if handle
+                  else torch.cuda.default_stream(like.device))
     return torch.cuda.stream(stream)
 
 
@@ -186,7 +189,7 @@ def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_o
     fp32 value for each row, or for each 128 values of a row (scale_group=128): y * scale is the
     norm."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return add_rmsnorm(x, res, weight, eps, out_dtype, scale_group, r_out)
     _norm_checks(x, res, weight, "x")
     _same_device(x, res, weight, r_out)
@@ -220,7 +223,7 @@ def add_rmsnorm_backward(dy, r, weight, eps=NORM_EPS, dr=None, stream=None):
     (dr, dx, dweight): the gradient of the sum in r's type, the same in dy's type (the same
     tensor where the types are equal), and the fp32 gradient of the weight."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, dy):
             return add_rmsnorm_backward(dy, r, weight, eps, dr)
     _norm_checks(dy, r, weight, "dy")
     _same_device(dy, r, weight, dr)
@@ -332,7 +335,7 @@ def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, 
     given.  Returns (o [B][T][H][dv], the state behind the last token); pass
     state_out=state to update a session's state in place."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, q):
             return linattn_forward(q, k, v, log_decay, scale, state, state_out, lengths, ws)
     desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
                                None, q.dtype, scale, False)
@@ -354,7 +357,7 @@ def linattn_backward(q, k, v, log_decay, dO, scale=None, state=None, dstate_out=
     Returns a dict: q, k, v (their shapes, contiguous) and state (fp32; None when no state was
     given)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, q):
             return linattn_backward(q, k, v, log_decay, dO, scale, state, dstate_out, lengths, ws)
     desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
                                dO.stride(), q.dtype, scale, True)

@@ -2,6 +2,7 @@
 every refusal with its documented status before the device is touched.  Invalid
 calls use fake (never dereferenced) device addresses.  The 64-bit forms that the
 GPU tests compare with are checked here against differences."""
+import contextlib
 import ctypes
 import os
 import re
@@ -291,6 +292,43 @@ def test_attention_reference_against_differences():
         hi, lo = list(a), list(a)
         hi[i], lo[i] = a[i] + u, a[i] - u
         assert abs((f(*hi) - f(*lo)) / 2 - (g * u).sum()) < 1e-9 * max(1, np.abs(g * u).sum())
+
+
+# ------------------------------------------------------------------ streams as arguments
+class FakeStream:
+    """Stands for torch's streams: one of the pool where no pointer, or a null one, is given."""
+
+    def __init__(self, handle=0, device=None):
+        self.cuda_stream = handle or 0xdead00
+
+
+def test_a_stream_handle_is_the_stream_entered(monkeypatch):
+    """A tensor-level call runs on the stream whose raw handle it is given, the null stream's 0
+    among them: torch takes a null pointer as none and makes a stream of its own."""
+    default = FakeStream()
+    default.cuda_stream = 0
+    entered = []
+
+    @contextlib.contextmanager
+    def stream(s):
+        entered.append(s.cuda_stream)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: default)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    for name in ("ttt_addnorm_forward", "ttt_addnorm_backward", "ttt_linattn_forward",
+                 "ttt_linattn_backward"):
+        monkeypatch.setattr(block, name, lambda *a, **k: None)
+    x, w, q, lg = torch.zeros(2, 64), torch.zeros(64), torch.zeros(1, 8, 4, 64), torch.zeros(4)
+    for s, handle in ((0, 0), (0x5000, 0x5000), (FakeStream(0x7000), 0x7000), (default, 0)):
+        for call in (lambda s: block.add_rmsnorm(x, x, w, stream=s),
+                     lambda s: block.add_rmsnorm_backward(x, x, w, stream=s),
+                     lambda s: block.linattn_forward(q, q, q, lg, stream=s),
+                     lambda s: block.linattn_backward(q, q, q, lg, q, stream=s)):
+            call(s)
+            assert entered.pop() == handle and not entered
 
 
 # ---------------------------------------------------- the waits of the compiled kernels

@@ -578,6 +578,35 @@ def test_stream_argument_owns_its_allocations():
             del junk, got
 
 
+def test_null_stream_argument():
+    """stream=0, as the default stream's handle is: behind what is pending there, and in front of
+    what follows."""
+    g, q, k, v, lg, st = attn_inputs(1, 700, 4, 4, 64, 64, BF16, 13)
+    dO = normal(g, 1, 700, 4, 64, dtype=BF16)
+    x, w = normal(g, 512, 2560, dtype=BF16), normal(g, 2560, dtype=BF16)
+    assert torch.cuda.current_stream().cuda_stream == torch.cuda.default_stream().cuda_stream == 0
+    with block._on(0, q):
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    calls = ((lambda q, x, **kw: block.linattn_forward(q, k, v, lg, state=st, **kw)),
+             (lambda q, x, **kw: tuple(block.linattn_backward(q, k, v, lg, dO, state=st, **kw).values())),
+             (lambda q, x, **kw: block.add_rmsnorm_backward(x, x, w, **kw)),
+             (lambda q, x, **kw: block.add_rmsnorm(x, x, w, **kw)[:2]))
+    busy = torch.ones(1 << 26, device="cuda")
+    for call in calls:
+        want = [t.clone() for t in call(q, x)]
+        torch.cuda.synchronize()
+        for stream in (0, torch.cuda.default_stream()):
+            q2, x2 = torch.zeros_like(q), torch.zeros_like(x)
+            torch.cuda.synchronize()
+            for _ in range(20):
+                busy.mul_(1.0)
+            q2.copy_(q)
+            x2.copy_(x)
+            got = [t.clone() for t in call(q2, x2, stream=stream)]
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_graph_replays_equal_eager():
     g, q, k, v, lg, st = attn_inputs(1, 700, 4, 2, 64, 64, BF16, 3)
     dO = normal(g, 1, 700, 4, 64, dtype=BF16)
