@@ -202,8 +202,11 @@ ttt_status_t check_workspace(const void* ws, size_t have, size_t need) {
   return TTT_OK;
 }
 
-ttt::LinOperand operand(const void* p, const int64_t st[3], int64_t rep) {
-  return {p, st[0], st[1], st[2], (int32_t)rep};
+// One token has no next one: its stride, which the limit above leaves free, must
+// not reach the chunked kernels' 32-bit offsets (of 31 rows, at a last chunk's end).
+ttt::LinOperand operand(const ttt_linattn_desc_t* d, const void* p, const int64_t st[3],
+                        int64_t rep) {
+  return {p, st[0], d->seq_len > 1 ? st[1] : 0, st[2], (int32_t)rep};
 }
 
 }  // namespace
@@ -313,9 +316,9 @@ ttt_status_t ttt_linattn_forward(const ttt_linattn_desc_t* desc, const void* q, 
           range("lengths", lengths, lengths ? desc->batch * sizeof(int32_t) : 0)))
     return st;
   ttt::LinArgs a{};
-  a.q = operand(q, desc->q_stride, 1);
-  a.k = operand(k, desc->k_stride, H / G);
-  a.v = operand(v, desc->v_stride, H / G);
+  a.q = operand(desc, q, desc->q_stride, 1);
+  a.k = operand(desc, k, desc->k_stride, H / G);
+  a.v = operand(desc, v, desc->v_stride, H / G);
   a.out = o;
   a.osb = desc->o_stride[0], a.ost = desc->o_stride[1], a.osh = desc->o_stride[2];
   a.log_decay = log_decay, a.lengths = lengths;
@@ -371,8 +374,10 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
   float* seg = static_cast<float*>(ws);
   const bool shared_heads = rep > 1;
   char* const wsb = static_cast<char*>(ws);
-  const ttt::LinOperand oq = operand(q, desc->q_stride, 1), ok_ = operand(k, desc->k_stride, rep),
-                        ov = operand(v, desc->v_stride, rep), od = operand(dO, desc->o_stride, 1);
+  const ttt::LinOperand oq = operand(desc, q, desc->q_stride, 1),
+                        ok_ = operand(desc, k, desc->k_stride, rep),
+                        ov = operand(desc, v, desc->v_stride, rep),
+                        od = operand(desc, dO, desc->o_stride, 1);
   ttt::LinArgs base{};
   base.log_decay = log_decay, base.lengths = lengths;
   base.B = B, base.T = T, base.H = H, base.dt = dt;

@@ -110,9 +110,9 @@ ttt_status_t ttt_addnorm_backward(const ttt_addnorm_desc_t* desc, const void* dy
  *   scale     finite
  *   q_stride, k_stride, v_stride, o_stride  values between sequences, tokens
  *             and heads of q, k, v and o ({batch, token, head}), multiples of 8
- *             and >= 0, token strides of q, k, v and dO at most 2^27 bytes: slices
- *             of one projection's output can be passed as they are.  A head's d
- *             values are contiguous.  A stride
+ *             and >= 0, token strides of q, k, v and dO at most 2^27 bytes where
+ *             there is more than one token: slices of one projection's output can
+ *             be passed as they are.  A head's d values are contiguous.  A stride
  *             of 0 in q, k, v or dO repeats a value; o must have no two elements
  *             at one place.  dO has the strides of o; dq, dk and dv are contiguous
  *             [B][T][H or G][d].

@@ -294,6 +294,84 @@ def test_attention_reference_against_differences():
         assert abs((f(*hi) - f(*lo)) / 2 - (g * u).sum()) < 1e-9 * max(1, np.abs(g * u).sum())
 
 
+# --------------------------------------------------- what the C ABI hands to the launches
+# block_api.cpp with launches that only take down what they were given
+LAUNCHES = r"""
+#include <cstdarg>
+#include "block.h"
+#include "api_common.h"
+extern "C" { int64_t seen[64]; int seen_count; }
+namespace ttt {
+namespace api {
+ttt_status_t fail(ttt_status_t code, const char*, ...) { return code; }
+ttt_status_t ok() { return TTT_OK; }
+ttt_status_t hip_fail(hipError_t, const char*) { return TTT_ERR_HIP; }
+Range range(const char* n, const void* p, size_t b) { return {n, (uintptr_t)p, (uintptr_t)p + b}; }
+bool overlaps(const Range& x, const Range& y) { return x.lo < y.hi && y.lo < x.hi; }
+bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
+}
+hipError_t note(const LinArgs& a) {
+  for (const LinOperand* o : {&a.q, &a.k, &a.v, &a.w}) if (o->p) seen[seen_count++] = o->st;
+  return hipSuccess;
+}
+hipError_t launch_linattn_chunked(const LinArgs& a, float*, hipStream_t) { return note(a); }
+hipError_t launch_linattn_step(const LinArgs& a, hipStream_t) { return note(a); }
+hipError_t launch_linattn_starts(const LinArgs*, int, float*, hipStream_t) { return hipSuccess; }
+hipError_t launch_linattn_sum_heads(const float*, void*, int64_t, const float*, void*, int64_t,
+                                    int64_t, int64_t, int64_t, int64_t, Dtype, hipStream_t) {
+  return hipSuccess;
+}
+bool linattn_square(int64_t dk, int64_t dv) { return (dk <= 64) == (dv <= 64); }
+size_t linattn_segment_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, Dtype) { return 0; }
+int64_t addnorm_backward_blocks(const NormArgs&) { return 1; }
+hipError_t launch_addnorm_forward(const NormArgs&, const void*, const void*, const void*, void*,
+                                  void*, float*, hipStream_t) { return hipSuccess; }
+hipError_t launch_addnorm_backward(const NormArgs&, const void*, const void*, const void*,
+                                   const void*, void*, void*, float*, float*, hipStream_t) {
+  return hipSuccess;
+}
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def api(tmp_path_factory):
+    d = tmp_path_factory.mktemp("api")
+    (d / "launches.cpp").write_text(LAUNCHES)
+    cmd = ["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-D__HIP_PLATFORM_AMD__",
+           "-I/opt/rocm/include", "-I" + hipbuild.CSRC, str(d / "launches.cpp"),
+           os.path.join(hipbuild.CSRC, "block_api.cpp"), "-o", str(d / "api.so")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    lib, own = ctypes.CDLL(str(d / "api.so")), block._load()
+    for name in ("ttt_linattn_forward", "ttt_linattn_backward"):
+        getattr(lib, name).argtypes = getattr(own, name).argtypes
+    return lib
+
+
+@pytest.mark.skipif(not os.path.exists("/opt/rocm/include/hip/hip_runtime.h"), reason="no HIP headers")
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d_value", [64, 128])
+@pytest.mark.parametrize("st", [0, 64, 1 << 27, 1 << 30, (1 << 32) // 31 // 8 * 8, 1 << 40])
+def test_one_tokens_stride_reaches_no_address(api, st, d_value, dtype):
+    """The stride between tokens of a call of one token means nothing and may be anything.  The
+    chunked kernels put a last chunk's tokens at the end of a tile of 32 and reach its rows by
+    32-bit offsets, so a stride that is passed on has to keep 31 rows below 2^32 bytes."""
+    d = attn_desc(seq_len=1, d_value=d_value, dtype=dtype, q_stride=(1 << 20, st, 64),
+                  k_stride=(1 << 20, st, 64), v_stride=(1 << 20, st, 128),
+                  o_stride=(1 << 20, st, 128))
+    seen, count = (ctypes.c_int64 * 64).in_dll(api, "seen"), ctypes.c_int.in_dll(api, "seen_count")
+    es = 2 if dtype == torch.bfloat16 else 4
+    for call, args in ((api.ttt_linattn_forward, [at(1), at(2), at(3), at(4), None, None, None, at(8)]),
+                       (api.ttt_linattn_backward, [at(1), at(2), at(3), at(4), None, None, at(7), None,
+                                                   at(8), at(9), at(10), None])):
+        count.value = 0
+        assert call(ctypes.byref(d), *args, at(20), 1 << 29, None) == 0
+        assert count.value >= 3
+        for i in range(count.value):
+            assert (31 * seen[i] + 128) * es < 1 << 32, (seen[i], es)
+
+
 # ------------------------------------------------------------------ streams as arguments
 class FakeStream:
     """Stands for torch's streams: one of the pool where no pointer, or a null one, is given."""

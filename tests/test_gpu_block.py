@@ -522,6 +522,31 @@ def test_attention_offsets_past_32_bits():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_attention_one_token_with_a_far_stride(dv, dtype):
+    """The stride between the tokens of one token means nothing, whatever it is: the same results,
+    bit for bit."""
+    B, H, G, dk = 3, 4, 2, 64
+    g, q, k, v, lg, st = attn_inputs(B, 1, H, G, dk, dv, dtype, 14)
+    dO, ds = normal(g, B, 1, H, dv, dtype=dtype), normal(g, B, H, dk, dv)
+    want = block.linattn_backward(q, k, v, lg, dO, scale=0.3, state=st, dstate_out=ds)
+    want_o, _ = block.linattn_forward(q, k, v, lg, scale=0.3, state=st)
+    new = lambda t: torch.full_like(t, 7.0)  # noqa: E731
+    for far in (0, 1 << 27, 1 << 30, 1 << 40):
+        say(dv, dtype, far)
+        desc = block.make_linattn_desc(B, 1, H, G, dk, dv, dtype, 0.3, (H * dk, far, dk),
+                                       (G * dk, far, dk), (G * dv, far, dv), (H * dv, far, dv))
+        ws = torch.empty(block.ttt_linattn_backward_workspace_size(desc) or 1, dtype=torch.uint8,
+                         device="cuda")
+        got = {"q": new(q), "k": new(k), "v": new(v), "state": new(st)}
+        block.ttt_linattn_backward(desc, q, k, v, lg, None, st, dO, ds, *got.values(), ws)
+        assert all(torch.equal(got[n], want[n]) for n in got)
+        o = new(want_o)
+        block.ttt_linattn_forward(desc, q, k, v, lg, None, st, None, o)
+        assert torch.equal(o, want_o)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_attention_prompt_then_tokens(dtype):
     """A prompt in pieces and single tokens continue one state."""
     B, T, H, G, dk, dv = 2, 300, 4, 2, 64, 64
