@@ -201,8 +201,8 @@ def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_o
     rows, d, xs = _rows(x)
     if rows == 0:
         raise ValueError("x has no rows")
-    desc = _norm_plan(rows, d, xs, x.dtype, x.dtype if res is None else res.dtype, eps, fp8,
-                      scale_group)
+    desc = _norm_plan(rows, d, xs, x.dtype, x.dtype if res is None else res.dtype, float(eps),
+                      fp8, int(scale_group))
     # contiguous outputs, whatever the rows of x are apart
     y = (torch.empty(x.shape, dtype=out_dtype, device=x.device) if fp8
          else torch.empty_like(x, memory_format=torch.contiguous_format))
@@ -232,7 +232,7 @@ def add_rmsnorm_backward(dy, r, weight, eps=NORM_EPS, dr=None, stream=None):
     rows, d, xs = _rows(dy)
     if rows == 0:
         raise ValueError("dy has no rows")
-    desc = _norm_plan(rows, d, xs, dy.dtype, r.dtype, eps, False, 0)
+    desc = _norm_plan(rows, d, xs, dy.dtype, r.dtype, float(eps), False, 0)
     out = torch.empty(r.shape, dtype=r.dtype, device=r.device)
     dx = None if r.dtype == dy.dtype else torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
     dw = torch.empty(d, dtype=torch.float32, device=dy.device)
@@ -289,6 +289,11 @@ def ttt_linattn_backward(desc, q, k, v, log_decay, lengths, state_in, dO, dstate
         _ptr(dstate_in), _ptr(ws), int(ws_bytes), _current(stream, q)))
 
 
+def _value(scale):
+    """A scale as the plans are kept by: its value, never the object given."""
+    return None if scale is None else float(scale)
+
+
 @functools.lru_cache(maxsize=256)
 def _linattn_plan(q, qs, k, ks, v, vs, os, dtype, scale, backward):
     """(descriptor, workspace bytes) of a call's shapes and strides."""
@@ -338,7 +343,7 @@ def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, 
         with _on(stream, q):
             return linattn_forward(q, k, v, log_decay, scale, state, state_out, lengths, ws)
     desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
-                               None, q.dtype, scale, False)
+                               None, q.dtype, _value(scale), False)
     _linattn_checks(q, k, v, log_decay, lengths, state, state_out)
     B, T, H, dk = q.shape
     dv = v.shape[3]
@@ -360,7 +365,7 @@ def linattn_backward(q, k, v, log_decay, dO, scale=None, state=None, dstate_out=
         with _on(stream, q):
             return linattn_backward(q, k, v, log_decay, dO, scale, state, dstate_out, lengths, ws)
     desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
-                               dO.stride(), q.dtype, scale, True)
+                               dO.stride(), q.dtype, _value(scale), True)
     _linattn_checks(q, k, v, log_decay, lengths, state, dstate_out)
     want = (*q.shape[:3], v.shape[3])
     if dO.shape != want or dO.dtype != q.dtype or dO.stride(3) != 1:

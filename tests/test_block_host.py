@@ -372,6 +372,31 @@ def test_one_tokens_stride_reaches_no_address(api, st, d_value, dtype):
             assert (31 * seen[i] + 128) * es < 1 << 32, (seen[i], es)
 
 
+# ---------------------------------------------------------- plans kept between calls
+def test_plans_take_the_values_of_scale_and_eps(monkeypatch):
+    """A scale or an eps given as a tensor counts with its value at the call: the plans that are
+    kept by shapes and values must not be found again by the tensor's identity."""
+    seen = []
+    for name in ("ttt_addnorm_forward", "ttt_addnorm_backward"):
+        monkeypatch.setattr(block, name, lambda desc, *a, **k: seen.append(desc.eps))
+    for name in ("ttt_linattn_forward", "ttt_linattn_backward"):
+        monkeypatch.setattr(block, name, lambda desc, *a, **k: seen.append(desc.scale))
+    x, w, q, lg = torch.zeros(2, 64), torch.zeros(64), torch.zeros(1, 8, 4, 64), torch.zeros(4)
+    for call in (lambda t: block.add_rmsnorm(x, x, w, eps=t),
+                 lambda t: block.add_rmsnorm_backward(x, x, w, eps=t),
+                 lambda t: block.linattn_forward(q, q, q, lg, scale=t),
+                 lambda t: block.linattn_backward(q, q, q, lg, q, scale=t)):
+        t = torch.tensor(0.5)
+        for value in (0.5, 0.25, 2.0):
+            t.fill_(value)
+            call(t)
+            assert seen.pop() == value
+        call(0.125)
+        assert seen.pop() == 0.125
+    block.linattn_forward(q, q, q, lg)
+    assert seen.pop() == 0.125  # 64^-0.5
+
+
 # ------------------------------------------------------------------ streams as arguments
 class FakeStream:
     """Stands for torch's streams: one of the pool where no pointer, or a null one, is given."""
