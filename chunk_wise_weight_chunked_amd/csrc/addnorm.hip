@@ -88,8 +88,8 @@ __device__ __forceinline__ uint2 pack_fp8x8(const float f[8]) {
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-// The scale that takes `top` to the largest 8-bit value; not below 2^-126, whose
-// reciprocal is still finite.
+// The scale that takes `top` to the largest 8-bit value; not below 2^-126, from
+// where on down a scale has fewer bits and, rounded, could take `top` past it.
 __device__ __forceinline__ float fp8_scale(float top) {
   return top > 0.0f ? fmaxf(top / kFp8Max, 0x1p-126f) : 1.0f;
 }
@@ -156,11 +156,12 @@ __global__ __launch_bounds__(kBlock) void addnorm_forward_kernel(
     }
   }
   if constexpr (kFp8) {
+    // divided, not multiplied by a rounded reciprocal, which moves values beside a
+    // tie to the next code (32768 x 2560: 164 us, 163 with the reciprocal)
     const auto put = [&](int i, int c, float scale) {
       float f[8];
-      const float inv = 1.0f / scale;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = v[i][j] * inv;
+      for (int j = 0; j < 8; ++j) f[j] = v[i][j] / scale;
       *reinterpret_cast<uint2*>(static_cast<uint8_t*>(y) + row * ys + 8 * c) = pack_fp8x8(f);
     };
     if (!grouped) {

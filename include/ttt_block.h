@@ -30,8 +30,8 @@ extern "C" {
  *
  * out = TTT_NORM_FP8 writes y in 8 bits (OCP E4M3) with fp32 scales: for each
  * row, or each run of 128 values of a row, scale = max |y| / 448 (at least
- * 2^-126, and 1 where every y is 0) and the stored value is y / scale rounded to nearest even, so that
- * stored * scale is y.  A NaN is stored as NaN and left out of the maximum.
+ * 2^-126, and 1 where every y is 0) and the stored value is y / scale, divided in
+ * fp32 and rounded to nearest even, so that stored * scale is y.  A NaN is stored as NaN and left out of the maximum.
  *
  *   rows      1 <= rows < 2^31
  *   d         a multiple of 8, 8 <= d <= 16384

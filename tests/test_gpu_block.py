@@ -124,6 +124,25 @@ def test_norm_fp8_smallest_values(group, dtype):
         assert (np.abs(got * s[..., None] - y64) <= bound).all()
 
 
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("rows,d", [(600, 128), (257, 512), (2100, 1024), (513, 2560), (40, 16384)])
+def test_norm_fp8_codes(rows, d, group):
+    """The stored codes are y / scale rounded to nearest even, y the fp32 norm: the same that the
+    call without 8 bits gives for fp32 rows, divided and rounded here."""
+    g = gen(rows)
+    x, res, w = normal(g, rows, d), normal(g, rows, d), normal(g, d)
+    y, _, _ = block.add_rmsnorm(x, res, w)
+    q, _, scale = block.add_rmsnorm(x, res, w, out_dtype=FP8, scale_group=group)
+    n = d // (group or d)
+    y = f64(y).astype(np.float32).reshape(rows, n, -1)
+    top = np.abs(y).max(-1, keepdims=True)
+    s = f64(scale).astype(np.float32).reshape(rows, n, 1)
+    assert np.array_equal(s, top / np.float32(448))
+    codes = torch.from_numpy(y / s).to(FP8).float().numpy()  # numpy's division is rounded once
+    wrong = int((f64(q.float()).reshape(codes.shape) != codes).sum())
+    assert wrong == 0, f"{wrong} of {codes.size}"
+
+
 def test_norm_strides_and_in_place():
     g = gen(3)
     wide = normal(g, 40, 3 * 256, dtype=BF16)
