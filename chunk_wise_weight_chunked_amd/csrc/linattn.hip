@@ -565,10 +565,20 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
         if (state_row(i, r) < dk && col < dv) S[i][r] = a.s_in[head_state + state_off(i, r)];
       }
   }
-  if (!kOut && g == 0) to_slot(0);
+  const float lg2 = log2_decay(lg);
+  if (!kOut && g == 0) {
+    to_slot(0);
+    // the state given decays over the tokens that are left out as well
+    if (t_lo > 0) {
+      const float f = decay_pow(lg2, t_lo);
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[i][r] *= f;
+    }
+  }
 
   // ---- decay factors
-  const float lg2 = log2_decay(lg);
   const int qrow = lane & 31;
   float w_up[16];  // update: scale_u g^(kC - late - token), token 16 (r / 8) + 8 half + r % 8
   float d_in[16];  // scores: scale_p g^(query - key), the same keys

@@ -432,6 +432,26 @@ def test_attention_decays():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dv", [64, 96])
+def test_attention_large_states_decay_to_nothing(dv, dtype):
+    """A state of 1e36 that comes in, and nothing else: with decays of exp(-1) and below it is 0 in
+    fp32 (below 2^-149) for every token from 190 on, whatever segments the tokens are in."""
+    B, T, H, G, dk = 1, 4096, 64, 1, 64
+    g, q, k, v, _, _ = attn_inputs(B, T, H, G, dk, dv, dtype, 15)
+    lg = torch.linspace(-1.0, -20.0, H, device="cuda")
+    st = torch.full((B, H, dk, dv), 1e36, device="cuda")
+    none = lambda t: torch.zeros_like(t)  # noqa: E731
+    o, S = block.linattn_forward(q, none(k), v, lg, state=st)
+    assert (o[:, 190:] == 0).all() and (S == 0).all() and (o[:, 0] != 0).any()
+    dO = torch.zeros(B, T, H, dv, dtype=dtype, device="cuda")
+    d = block.linattn_backward(q, k, v, lg, dO, state=st, dstate_out=st)
+    assert (d["k"][:, :T - 190] == 0).all() and (d["v"][:, :T - 190] == 0).all()
+    assert (d["k"][:, T - 1] != 0).any() and (d["state"] == 0).all()
+    dO = normal(g, B, T, H, dv, dtype=dtype)
+    assert (block.linattn_backward(q, none(k), v, lg, dO, state=st)["q"][:, 190:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("T", [3, 29, 70, 600])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
 def test_attention_infinities_stay_behind_the_mask(T, bad, dtype):
