@@ -93,11 +93,19 @@ def _strided(t):
     return t.data_ptr()
 
 
-def _current(stream, like):
-    """The stream given, or the current one of the tensor's device as a raw handle."""
-    if stream is None and isinstance(like, torch.Tensor) and like.is_cuda:
-        return torch._C._cuda_getCurrentRawStream(like.get_device())
-    return _stream(stream)
+def _run(fn, stream, like, *args):
+    """fn(*args, stream): the stream given, or the current one of the device of `like`.  A null
+    handle is the null stream of the device that is current, so that device is made current."""
+    if stream is None and getattr(like, "is_cuda", False):
+        where = like.get_device()
+        handle = torch._C._cuda_getCurrentRawStream(where)
+    else:
+        where = stream.device.index if isinstance(stream, torch.cuda.Stream) else None
+        handle = _stream(stream)
+    if where is None or where == torch._C._cuda_getDevice():
+        return _check(fn(*args, handle))
+    with torch.cuda.device(where):
+        return _check(fn(*args, handle))
 
 
 def _on(stream, like):
@@ -122,8 +130,8 @@ def make_addnorm_desc(rows, d, dtype, res_dtype=None, x_stride=None, y_stride=No
 
 
 def ttt_addnorm_forward(desc, x, res, w, r, y, y_scale=None, stream=None) -> None:
-    _check(_load().ttt_addnorm_forward(ctypes.byref(desc), _strided(x), _ptr(res), _ptr(w),
-                                       _ptr(r), _strided(y), _ptr(y_scale), _current(stream, x)))
+    _run(_load().ttt_addnorm_forward, stream, x, ctypes.byref(desc), _strided(x), _ptr(res),
+         _ptr(w), _ptr(r), _strided(y), _ptr(y_scale))
 
 
 def ttt_addnorm_backward_workspace_size(desc) -> int:
@@ -137,9 +145,8 @@ def ttt_addnorm_backward(desc, dy, r, w, dr_out, dr, dx, dw, ws=None, ws_bytes=N
                          stream=None) -> None:
     if ws_bytes is None:
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(_load().ttt_addnorm_backward(ctypes.byref(desc), _strided(dy), _ptr(r), _ptr(w),
-                                        _ptr(dr_out), _ptr(dr), _strided(dx), _ptr(dw), _ptr(ws),
-                                        int(ws_bytes), _current(stream, dy)))
+    _run(_load().ttt_addnorm_backward, stream, dy, ctypes.byref(desc), _strided(dy), _ptr(r),
+         _ptr(w), _ptr(dr_out), _ptr(dr), _strided(dx), _ptr(dw), _ptr(ws), int(ws_bytes))
 
 
 @functools.lru_cache(maxsize=256)
@@ -274,19 +281,18 @@ def ttt_linattn_forward(desc, q, k, v, log_decay, lengths, state_in, state_out, 
                         ws_bytes=None, stream=None) -> None:
     if ws_bytes is None:
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(_load().ttt_linattn_forward(
-        ctypes.byref(desc), _strided(q), _strided(k), _strided(v), _ptr(log_decay), _ptr(lengths),
-        _ptr(state_in), _ptr(state_out), _strided(o), _ptr(ws), int(ws_bytes), _current(stream, q)))
+    _run(_load().ttt_linattn_forward, stream, q, ctypes.byref(desc), _strided(q), _strided(k),
+         _strided(v), _ptr(log_decay), _ptr(lengths), _ptr(state_in), _ptr(state_out), _strided(o),
+         _ptr(ws), int(ws_bytes))
 
 
 def ttt_linattn_backward(desc, q, k, v, log_decay, lengths, state_in, dO, dstate_out, dq, dk, dv,
                          dstate_in, ws=None, ws_bytes=None, stream=None) -> None:
     if ws_bytes is None:
         ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(_load().ttt_linattn_backward(
-        ctypes.byref(desc), _strided(q), _strided(k), _strided(v), _ptr(log_decay), _ptr(lengths),
-        _ptr(state_in), _strided(dO), _ptr(dstate_out), _ptr(dq), _ptr(dk), _ptr(dv),
-        _ptr(dstate_in), _ptr(ws), int(ws_bytes), _current(stream, q)))
+    _run(_load().ttt_linattn_backward, stream, q, ctypes.byref(desc), _strided(q), _strided(k),
+         _strided(v), _ptr(log_decay), _ptr(lengths), _ptr(state_in), _strided(dO),
+         _ptr(dstate_out), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dstate_in), _ptr(ws), int(ws_bytes))
 
 
 def _value(scale):

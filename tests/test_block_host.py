@@ -372,6 +372,60 @@ def test_one_tokens_stride_reaches_no_address(api, st, d_value, dtype):
             assert (31 * seen[i] + 128) * es < 1 << 32, (seen[i], es)
 
 
+class FakeTensor(torch.Tensor):
+    """Stands for a tensor of another device than the current one."""
+
+    is_cuda = True
+
+    @staticmethod
+    def __new__(cls, address):
+        t = torch.Tensor._make_subclass(cls, torch.zeros(1))
+        t.address = address
+        return t
+
+    def data_ptr(self):
+        return self.address
+
+    def get_device(self):
+        return 1
+
+
+def test_null_streams_belong_to_their_device(monkeypatch):
+    """A null handle is the null stream of the device that is current: a call without a stream, or
+    with another device's default stream, makes the tensors' (the stream's) device current."""
+    entered, handles = [], []
+    device = [0]
+
+    @contextlib.contextmanager
+    def on(index):
+        device[0] = getattr(index, "index", index)
+        entered.append(device[0])
+        yield
+        device[0] = 0
+
+    monkeypatch.setattr(torch.cuda, "device", on)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: device[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: handles.append((device[0], a[-1])) or 0
+
+    monkeypatch.setattr(block, "_load", Lib)
+    t = [FakeTensor(at(i)) for i in range(13)]
+    d, n = attn_desc(), norm_desc()
+    second = FakeStream()
+    second.cuda_stream, second.device = 0, torch.device("cuda", 1)
+    for stream, want in ((None, (1, 0)), (second, (1, 0)), (0, (0, 0)), (0x5000, (0, 0x5000))):
+        block.ttt_addnorm_forward(n, *t[:5], stream=stream)
+        block.ttt_addnorm_backward(n, *t[:8], 0, stream=stream)
+        block.ttt_linattn_forward(d, *t[:9], 0, stream=stream)
+        block.ttt_linattn_backward(d, *t[:13], 0, stream=stream)
+        assert handles == [want] * 4 and entered == ([1] * 4 if want[0] else [])
+        handles.clear(), entered.clear()
+
+
 # ---------------------------------------------------------- plans kept between calls
 def test_plans_take_the_values_of_scale_and_eps(monkeypatch):
     """A scale or an eps given as a tensor counts with its value at the call: the plans that are
