@@ -320,7 +320,7 @@ def _linattn_plan(q, qs, k, ks, v, vs, os, dtype, scale, backward):
     return desc, size(desc)
 
 
-def _linattn_checks(q, k, v, log_decay, lengths, *states):
+def _linattn_checks(q, k, v, log_decay, lengths, ws, *states):
     """What the plan does not look at: types, devices, and the small and the fp32 tensors."""
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise ValueError("q, k and v must be of one type, bfloat16 or float32")
@@ -333,7 +333,7 @@ def _linattn_checks(q, k, v, log_decay, lengths, *states):
         if s is not None and (s.shape != (B, H, q.shape[3], v.shape[3])
                               or s.dtype != torch.float32):
             raise ValueError(f"states must be [{B}][{H}][{q.shape[3]}][{v.shape[3]}] float32")
-    _same_device(q, k, v, log_decay, lengths, *states)
+    _same_device(q, k, v, log_decay, lengths, ws, *states)
 
 
 def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, lengths=None,
@@ -350,7 +350,7 @@ def linattn_forward(q, k, v, log_decay, scale=None, state=None, state_out=None, 
             return linattn_forward(q, k, v, log_decay, scale, state, state_out, lengths, ws)
     desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
                                None, q.dtype, _value(scale), False)
-    _linattn_checks(q, k, v, log_decay, lengths, state, state_out)
+    _linattn_checks(q, k, v, log_decay, lengths, ws, state, state_out)
     B, T, H, dk = q.shape
     dv = v.shape[3]
     o = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
@@ -372,7 +372,7 @@ def linattn_backward(q, k, v, log_decay, dO, scale=None, state=None, dstate_out=
             return linattn_backward(q, k, v, log_decay, dO, scale, state, dstate_out, lengths, ws)
     desc, need = _linattn_plan(q.shape, q.stride(), k.shape, k.stride(), v.shape, v.stride(),
                                dO.stride(), q.dtype, _value(scale), True)
-    _linattn_checks(q, k, v, log_decay, lengths, state, dstate_out)
+    _linattn_checks(q, k, v, log_decay, lengths, ws, state, dstate_out)
     want = (*q.shape[:3], v.shape[3])
     if dO.shape != want or dO.dtype != q.dtype or dO.stride(3) != 1:
         raise ValueError(f"dO must be {want} of {q.dtype}, last dimension contiguous")

@@ -426,6 +426,19 @@ def test_null_streams_belong_to_their_device(monkeypatch):
         handles.clear(), entered.clear()
 
 
+def test_a_workspace_of_another_device_is_refused(monkeypatch):
+    looked_at = []
+    monkeypatch.setattr(block, "_same_device", lambda like, *t: looked_at.extend(t))
+    for name in ("ttt_linattn_forward", "ttt_linattn_backward"):
+        monkeypatch.setattr(block, name, lambda *a, **k: None)
+    q, lg, ws = torch.zeros(1, 8, 4, 64), torch.zeros(4), torch.zeros(256, dtype=torch.uint8)
+    block.linattn_forward(q, q, q, lg, ws=ws)
+    assert any(t is ws for t in looked_at)
+    looked_at.clear()
+    block.linattn_backward(q, q, q, lg, q, ws=ws)
+    assert any(t is ws for t in looked_at)
+
+
 # ---------------------------------------------------------- plans kept between calls
 def test_plans_take_the_values_of_scale_and_eps(monkeypatch):
     """A scale or an eps given as a tensor counts with its value at the call: the plans that are
