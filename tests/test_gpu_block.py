@@ -504,6 +504,56 @@ def test_attention_infinities_stay_behind_the_mask(T, bad, dtype):
                 assert not torch.isfinite(got["dv"][0, max(0, s - 7):s + 1, 0, 5]).any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [29, 70, 1100])
+@pytest.mark.parametrize("G,d", [(1, 64), (2, 64), (1, 128), (2, 128)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_attention_infinities_square_heads(bad, G, d, T, dtype):
+    """The same where keys and values are of one size, whose gradients of k and v come from one
+    launch, with their own heads and shared ones, in one segment and in many."""
+    H = 2
+    g, q, k, v, _, st = attn_inputs(1, T, H, G, d, d, dtype, T + G)
+    lg = torch.tensor([-1e-3, -0.5], device="cuda")
+    dO, ds = normal(g, 1, T, H, d, dtype=dtype), normal(g, 1, H, d, d)
+    clean = {"q": q, "k": k, "v": v, "dO": dO}
+
+    def run(t):
+        o, S = block.linattn_forward(t["q"], t["k"], t["v"], lg, state=st)
+        x = block.linattn_backward(t["q"], t["k"], t["v"], lg, t["dO"], state=st, dstate_out=ds)
+        return {"o": o, "S": S, **{"d" + n: x[n] for n in "qkv"}, "dS": x["state"]}
+
+    want = run(clean)
+    assert all(torch.isfinite(t).all() for t in want.values())
+    for s in (0, T // 2, T - 1):
+        own = [t for t in range(T) if t != s]
+        before, after, every = list(range(s)), list(range(s + 1, T)), list(range(T))
+        untouched = {
+            "q": {"o": own, "S": None, "dq": every, "dk": after, "dv": after},
+            "k": {"o": before, "dq": before, "dk": every, "dv": own, "dS": None},
+            "v": {"o": before, "dq": before, "dk": own, "dv": every, "dS": None},
+            "dO": {"o": every, "S": None, "dq": own, "dk": after, "dv": after},
+        }
+        for name in clean:
+            t = dict(clean)
+            t[name] = clean[name].clone()
+            t[name][0, s, 0, 5] = bad
+            got = run(t)
+            say(T, G, d, dtype, bad, s, name)
+            for out, rows in untouched[name].items():
+                a, b = (got[out], want[out]) if rows is None else (got[out][:, rows], want[out][:, rows])
+                assert torch.equal(a, b), (name, s, out)
+            near = slice(max(0, s - 7), s + 1)
+            if name == "q":
+                assert not torch.isfinite(got["dk"][0, near, 0, 5]).any()
+            if name == "dO":
+                keep = [c for c in range(d) if c != 5]
+                assert torch.equal(got["dv"][..., keep], want["dv"][..., keep])
+                assert not torch.isfinite(got["dv"][0, near, 0, 5]).any()
+            if name == "v":
+                assert not torch.isfinite(got["dk"][0, s, 0]).any()
+                assert not torch.isfinite(got["o"][0, s:s + 8, 0, 5]).any()
+
+
 @pytest.mark.parametrize("T", [4, 70, 600])
 def test_attention_layouts(T):
     """Head-first storage, slices of one projection, a batch repeated by a stride of 0: as
