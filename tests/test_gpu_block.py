@@ -554,6 +554,38 @@ def test_attention_infinities_square_heads(bad, G, d, T, dtype):
                 assert not torch.isfinite(got["o"][0, s:s + 8, 0, 5]).any()
 
 
+# What three bf16 terms a weighted value keep, the 24 bits of fp32, is lost only by the
+# fp32 sums: the weight, its product, six accumulations of a chunk and the decay, each
+# within 2^-24 (rms 2^-24 / sqrt 3), 1.6 * 2^-24 a chunk; over the n chunks that a state
+# remembers the roundings add like sqrt n.  Up to 35 chunks here: 10 * 2^-24, bound 2^-20
+# (two terms: 2^-18 a value).
+TOL_STATE_SUMS = 2.0 ** -20
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,T,H,G,d", [(1, 1100, 2, 2, 64), (2, 1100, 2, 1, 64), (1, 1100, 2, 2, 128),
+                                       (1, 1100, 2, 1, 128), (1, 777, 4, 2, 104)])
+def test_attention_gradients_of_many_segments(B, T, H, G, d, dtype, ragged):
+    """More than eight segments, whose states a launch of its own adds up, for both directions at
+    once: against the 64-bit form, and the states as exact as fp32 sums."""
+    say(B, T, H, G, d, dtype, ragged)
+    g, q, k, v, lg, st = attn_inputs(B, T, H, G, d, d, dtype, T + d)
+    lg[0] = -1e-3
+    dO, ds = normal(g, B, T, H, d, dtype=dtype), normal(g, B, H, d, d)
+    lens = [T - 61, 643][:B] if ragged else None
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, S = block.linattn_forward(q, k, v, lg, scale=0.3, state=st, lengths=ln)
+    got = block.linattn_backward(q, k, v, lg, dO, scale=0.3, state=st, dstate_out=ds, lengths=ln)
+    o64, S64 = ref.linattn(f64(q), f64(k), f64(v), f64(lg), 0.3, f64(st), lens)
+    want = ref.linattn_grads(f64(q), f64(k), f64(v), f64(lg), 0.3, f64(dO), f64(st), f64(ds), lens)
+    err = {"o": rel(f64(o), o64), **{n: rel(f64(got[n]), w) for n, w in zip("qkv", want)}}
+    states = rel(f64(S), S64), rel(f64(got["state"]), want[3])
+    say("  ", {n: "%.2e" % e for n, e in err.items()}, "states %.2e %.2e" % states)
+    assert all(e <= TOL_CHUNK[dtype] for e in err.values())
+    assert max(states) <= TOL_STATE_SUMS
+
+
 @pytest.mark.parametrize("T", [4, 70, 600])
 def test_attention_layouts(T):
     """Head-first storage, slices of one projection, a batch repeated by a stride of 0: as
