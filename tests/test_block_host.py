@@ -542,3 +542,31 @@ def test_no_load_into_lds_is_in_flight_at_a_barrier(tmp_path):
                 j -= 1
             checked += 1
     assert checked >= 2 * 20, checked
+
+
+@pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="hipcc not available")
+def test_the_librarys_own_build_waits_at_barriers(tmp_path):
+    """The same of the code that the library is built from: with the compiler and the flags of
+    build.py, whatever they become."""
+    out = tmp_path / "linattn.s"
+    flags = [f for f in hipbuild.HIPCC_FLAGS if f != "-shared"]
+    cmd = [hipbuild.hipcc(), *flags, "--cuda-device-only", "-S",
+           os.path.join(hipbuild.CSRC, "linattn.hip"), "-o", str(out)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    kernels = [k for k in re.split(r"^(?=_Z\w+:)", out.read_text(), flags=re.M)
+               if re.search(r"buffer_load\w* .*\blds$", k, re.M)]
+    barriers = 0
+    for k in kernels:
+        lines = k.split(".Lfunc_end")[0].splitlines()
+        assert not any("scratch_" in x for x in lines), lines[0]
+        waited = False  # vmcnt(0) behind the last vector memory operation of this block
+        for x in lines:
+            if VMEM.match(x) or re.match(r"^\.LBB", x):
+                waited = False
+            elif re.search(r"s_waitcnt.*vmcnt\(0\)", x):
+                waited = True
+            elif "s_barrier" in x:
+                assert waited, lines[0]
+                barriers += 1
+    assert len(kernels) >= 20 and barriers >= 2 * len(kernels), (len(kernels), barriers)
