@@ -6,7 +6,9 @@ Like ttt_mlp, this is argument marshalling only, over the same library
 (ttt_mlp.load()): the functions named as the C entry points take raw
 descriptors and buffers; add_rmsnorm, add_rmsnorm_backward, linattn_forward
 and linattn_backward allocate outputs and workspace with torch and call them, on
-the current stream or on the one given as stream=.  There is no fallback.
+the current stream of the tensors' device or on the one given as stream= (a torch
+stream, or a raw handle of a stream of that device; 0 is its null stream).  The
+inputs' memory has to last until that stream is done with it.  There is no fallback.
 """
 from __future__ import annotations
 
@@ -189,9 +191,10 @@ def add_rmsnorm(x, res, weight, eps=NORM_EPS, out_dtype=None, scale_group=0, r_o
                 stream=None):
     """r = x + res, y = r / sqrt(mean(r^2) + eps) * weight over the last dimension.
 
-    x [..., d] bf16 or fp32 (2-dimensional with any row stride, or contiguous), weight [d] of
-    its type, res (or None) of its type or fp32.  Returns (y, r, scale).  r has res's type
-    (written to r_out if given, which may be res itself; None without a residual); y has x's
+    x [..., d] bf16 or fp32 (contiguous, or 2-dimensional with rows a multiple of 8 values apart;
+    16-byte aligned), weight [d] of its type, res (or None) of its type or fp32.  Returns
+    (y, r, scale).  r has res's type (written to r_out if given, which may be res itself; None
+    without a residual); y has x's
     type and scale is None, or with out_dtype=torch.float8_e4m3fn y is 8-bit and scale holds one
     fp32 value for each row, or for each 128 values of a row (scale_group=128): y * scale is the
     norm."""

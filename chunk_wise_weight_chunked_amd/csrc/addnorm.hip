@@ -331,11 +331,14 @@ struct RowShape {
 };
 
 // 16 lanes take rows of up to 128 values; rows of up to 512 a wave.  Longer ones
-// (bf16, us with a wave a row / with a workgroup a row):
-//   forward   512 x 1024 3.3 / 3.0,  512 x 2560 4.8 / 3.9,  32768 x 1024 41 / 45,
-//             32768 x 1536 77 / 71,  32768 x 2560 129 / 121,  32768 x 4096 209 / 190
-//   backward  256 x 2560 9.0 / 7.9,  512 x 2560 9.8 / 10.9,  32768 x 1024 38 / 80,
-//             32768 x 2560 102 / 125,  4096 x 4096 38 / 25
+// (bf16, the backward without dr_out, us with a wave a row / with a workgroup a row;
+// the small ones are kernel times, a call is 8 us forward and 15 backward):
+//   forward   512 x 1024 3.3 / 3.0,  512 x 2560 4.8 / 3.9,  32768 x 1024 41 / 43,
+//             32768 x 1536 78 / 72,  32768 x 2560 129 / 120,  32768 x 4096 204 / 187
+//   backward  256 x 2560 9.0 / 7.9,  512 x 2560 9.8 / 10.9,  32768 x 1024 37 / 82,
+//             32768 x 2560 102 / 132,  4096 x 4096 38 / 25
+// and with fp32 residuals 32768 x 1024 80 / 113, 32768 x 2560 199 / 190, 4096 x 4096
+// 49 / 38, all in fp32 77 / 104, 192 / 192, 49 / 37.
 // The workgroup shortens the chain of a few rows and has fewer values in a
 // lane's registers; the wave needs no barrier and, in the backward, adds four
 // rows' sums before they leave the workgroup.
@@ -411,8 +414,12 @@ hipError_t launch_addnorm_forward(const NormArgs& a, const void* x, const void* 
   });
 }
 
-// Two workgroups a CU: the partial sums stay small (512 rows of d) and each
-// workgroup walks enough rows to hide them.
+// Two workgroups for each CU: the partial sums stay small (512 rows of d) and each
+// workgroup walks enough rows to hide them.  Rows of five fp32 pieces a lane or of
+// eight pieces need more than 256 registers, one wave a SIMD, so that their
+// workgroups run in two turns; the bytes still set their time (with dr_out and an fp32
+// residual 32768 x 2560 256 us, 16384 x 9728 488, both 5.2 TB/s; all bf16 134 and
+// 246, 5.0 and 5.2).
 int64_t addnorm_backward_blocks(const NormArgs& a) {
   const int64_t per = kBlock / row_shape(a, true).lpr;
   return std::min<int64_t>((a.rows + per - 1) / per, 512);

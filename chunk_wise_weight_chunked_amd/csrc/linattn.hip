@@ -32,11 +32,11 @@
 // than one 32x32 tile of scores a wave, and leaves two workgroups a CU; 64
 // tokens would halve the state's conversions but need 96 KB of LDS a workgroup.
 //
-// What bounds it: 131072 tokens x 20 heads of 128 in bf16 take 832 us; reading q,
-// k and v and writing o is 2.7 GB (540 us at a copy's rate).  Traced (at a lower
-// clock, 970 us in all) the ends' pass takes 325 us (it reads 0.85 of K's and V's
-// 1.34 GB, the rest has decayed to 0), the sums over segments 12 and the main
-// pass 635.
+// What bounds it: 131072 tokens x 20 heads of 128 in bf16 take 830 us (870 on
+// another host); reading q, k and v and writing o is 2.7 GB (540 us at a copy's
+// rate).  Traced (at a lower clock, 970 us in all) the ends' pass takes 325 us (it
+// reads 0.85 of K's and V's 1.34 GB, the rest has decayed to 0), the sums over
+// segments 12 and the main pass 635.
 // Back to back the clock falls to 1.7 from 2.2 GHz, which then costs more than
 // any one of the remaining waits: without loads the same passes take 600 us.
 //
@@ -47,7 +47,10 @@
 // sums make it; two terms (2^-17) where the pass's state only ever meets bf16
 // operands (the gradients of q and k).  The third term costs 3% to 4% (16
 // prompts of 8192 tokens: 636 us with two terms, 656 us with three).  fp32
-// operands use fp32 MFMAs and no rounding.
+// operands use fp32 MFMAs and no rounding; 32768 tokens x 20 heads of 128 take 944
+// us, of which the matrix instructions as issued (88 GFLOP, the scores four times)
+// are 575 at the fp32 matrix rate: tiles of 4 bytes leave one wave a SIMD, so that
+// what is not covered within the wave is waited for.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -402,9 +405,10 @@ __device__ __forceinline__ int live_tokens(const int32_t* lengths, int64_t b, in
 // (kTwo: two fit a CU) join the first; then each takes the place of one that has
 // ended.  So the shortest sequences go to the CUs that hold two, a longer one of
 // them beside a shorter, and where not all are resident the longest go first.
-// Lengths of T / 4 to T, 20 heads of 128, bf16: 16 x 8192 tokens 571 -> 499 us,
-// their gradients 1388 -> 1268, 64 x 2048 473 -> 443, 40 x 1024 153 -> 151; from
-// 1024 tokens on, as 64 x 512 with 16 heads took 95 -> 101 us.
+// Lengths of T / 4 to T, 20 heads of 128, bf16, without and with it: 16 x 8192
+// tokens 581 and 488 us, their gradients 1440 and 1261, 64 x 2048 437 and 427,
+// 40 x 1024 163 and 161; from 1024 tokens on, as 64 x 512 with 16 heads took 95
+// without and 101 with it.
 constexpr uint32_t kCUs = 256;
 constexpr int kOrderTokens = 1024, kOrderBatch = 64;
 template <bool kTwo>
@@ -807,7 +811,9 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
   }
 }
 
-// Two waves a SIMD need half the register file each; fp32 tiles leave LDS for one.
+// Two waves a SIMD need half the register file each; fp32 tiles leave LDS for one,
+// and so do the bf16 tiles of 128 keys and 64 values with fp32 outputs (56 KB, two
+// workgroups of two waves a CU), whose registers the compiler then does not limit.
 template <typename T>
 constexpr int kMinWaves = sizeof(T) == 2 ? 2 : 1;
 
@@ -973,8 +979,9 @@ int64_t padded(int64_t d) { return d <= 64 ? 64 : 128; }
 // one in fp32, whose tiles leave LDS for no more), of two chunks at least.  More
 // of them cost more in states than they gain: gradients of 32768 tokens, 20
 // heads of 128, bf16: 629 us with 2048 waves, 716 us with 4096; 4096 tokens, 16
-// heads of 64, fp32: 112 us with 1024, 148 us with 2048 (32768 tokens, 20 heads
-// of 128 the other way round, 2.46 and 2.37 ms).  At least 128 tokens a segment
+// heads of 64, fp32: 110 us with 1024, 154 us with 2048, and 50 and 60 us without
+// gradients (32768 tokens, 20 heads of 128 the other way round: 2.50 and 2.41 ms,
+// 944 and 874 us).  At least 128 tokens a segment
 // are slower for small calls (1024 tokens, 4 heads, fp32: 37 us, 29 us).
 constexpr int64_t kResidentWavesBf16 = 2048, kResidentWavesF32 = 1024, kMinSegment = 64;
 struct Split {

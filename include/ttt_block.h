@@ -31,7 +31,8 @@ extern "C" {
  * out = TTT_NORM_FP8 writes y in 8 bits (OCP E4M3) with fp32 scales: for each
  * row, or each run of 128 values of a row, scale = max |y| / 448 (at least
  * 2^-126, and 1 where every y is 0) and the stored value is y / scale, divided in
- * fp32 and rounded to nearest even, so that stored * scale is y.  A NaN is stored as NaN and left out of the maximum.
+ * fp32 and rounded to nearest even, so that stored * scale is y.  A NaN is stored
+ * as NaN and left out of the maximum; an infinity makes its scale infinite.
  *
  *   rows      1 <= rows < 2^31
  *   d         a multiple of 8, 8 <= d <= 16384
@@ -126,7 +127,8 @@ ttt_status_t ttt_addnorm_backward(const ttt_addnorm_desc_t* desc, const void* dy
  *             keeps its state.
  * States are fp32 [B][H][d_key][d_value], contiguous.  An infinity or NaN reaches
  * only the results that the formula gives it to, and may become NaN there; a
- * token whose decay to a later one is 0 in fp32 may be left out of its result. */
+ * token whose decay to a later one is 0 in fp32 may be left out of its result,
+ * an infinity or NaN in it too: whether it is depends on the sizes of the call. */
 typedef struct {
   int64_t batch;
   int64_t seq_len;
@@ -153,10 +155,13 @@ ttt_status_t ttt_linattn_backward_workspace_size(const ttt_linattn_desc_t* desc,
  *   state_out  the state behind each sequence's last token; may be state_in
  *              itself (a session's state updated in place); may be NULL
  * Calls of up to 4 tokens run in the recurrent form (state read and
- * written once, all arithmetic in fp32), longer calls in the chunked form on
- * the matrix cores: bf16 products with fp32 accumulation, in which the decayed
- * scores and the state's copy that meets q are rounded to bf16 while the state
- * itself is exact to fp32 sums; fp32 inputs use fp32 products throughout. */
+ * written once, all arithmetic in fp32 and o rounded once), longer calls in the
+ * chunked form on the matrix cores.  There bf16 operands meet in bf16 products
+ * with fp32 accumulation: the decayed scores and the state's copy that meets q are
+ * rounded to bf16, so that o is off by up to three roundings (2.0e-3 to 2.4e-3
+ * against 64 bits, one rounding is 1.7e-3) where a call of 4 tokens is off by one;
+ * the state itself is as exact as fp32 sums (2^-20; 1.4e-7 to 3.6e-7 measured).
+ * fp32 operands use fp32 products throughout and round nothing else. */
 ttt_status_t ttt_linattn_forward(const ttt_linattn_desc_t* desc, const void* q, const void* k,
                                  const void* v, const float* log_decay, const int32_t* lengths,
                                  const float* state_in, float* state_out, void* o, void* ws,
@@ -169,7 +174,11 @@ ttt_status_t ttt_linattn_forward(const ttt_linattn_desc_t* desc, const void* q, 
  *   dstate_in = scale sum_t g^(t+1) q_t dO_t^T + g^n dstate_out
  * for a sequence of n tokens; dk and dv are summed over the query heads that
  * share a key / value head (in fp32, in head order).  The decay and the scale
- * are constants of the model and get no gradient.
+ * are constants of the model and get no gradient.  Any number of tokens runs in
+ * the chunked form: with bf16 operands the scores and the copies of S and of its
+ * gradient that meet dO, v and k are rounded to bf16 as in the forward, and what
+ * is added to the S that only dq's products read carries 16 bits or more (two
+ * bf16 terms); dstate_in is as exact as the forward's state.
  *   dO         gradient of o; dstate_out [B][H][d_key][d_value] or NULL (0)
  *   state_in   the forward's, or NULL
  *   dq [B][T][H][d_key], dk [B][T][G][d_key], dv [B][T][G][d_value], dtype
