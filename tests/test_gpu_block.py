@@ -586,6 +586,32 @@ def test_attention_gradients_of_many_segments(B, T, H, G, d, dtype, ragged):
     assert max(states) <= TOL_STATE_SUMS
 
 
+# Each of some hundred segments' sums is good to 2^-22 (eight chunks, see above); adding n of
+# them up rounds the sum n times, 2^-24 / sqrt 3 rms each, of a sum that grows: sqrt(n / 2)
+# of them, 9 * 2^-24 for 512 segments, 10 with the segments' own; bound twice that.
+TOL_STATE_LONG = 2.0 ** -19.5
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attention_states_that_remember_many_segments(dtype):
+    """131072 tokens with memories of 33000 and a million: the segments' factor is applied some
+    hundred times, so that its own rounding (3e-8) must not be applied with it."""
+    T, H, d = 131072, 2, 64
+    g = gen(16)
+    q, k, v, dO = (normal(g, 1, T, H, d, dtype=dtype) for _ in range(4))
+    lg = torch.tensor([-1e-6, -3e-5], device="cuda")
+    _, S = block.linattn_forward(q, k, v, lg)
+    got = block.linattn_backward(q, k, v, lg, dO, scale=1.0, state=torch.zeros_like(S))
+    for h in range(H):
+        t = torch.arange(T, dtype=torch.float64)
+        w = torch.exp(float(lg[h]) * t)[:, None]
+        kh, vh, qh, dh = (x[0, :, h].cpu().double() for x in (k, v, q, dO))
+        err = (rel(f64(S[0, h]), (kh * w.flip(0)).t() @ vh),
+               rel(f64(got["state"][0, h]), (qh * w * np.exp(float(lg[h]))).t() @ dh))
+        say(dtype, float(lg[h]), "%.2e %.2e" % err)
+        assert max(err) <= TOL_STATE_LONG
+
+
 @pytest.mark.parametrize("T", [4, 70, 600])
 def test_attention_layouts(T):
     """Head-first storage, slices of one projection, a batch repeated by a stride of 0: as
