@@ -155,7 +155,8 @@ ttt_status_t ttt_linattn_backward_workspace_size(const ttt_linattn_desc_t* desc,
  *   state_out  the state behind each sequence's last token; may be state_in
  *              itself (a session's state updated in place); may be NULL
  * Calls of up to 4 tokens run in the recurrent form (state read and
- * written once, all arithmetic in fp32 and o rounded once), longer calls in the
+ * written once, all arithmetic in fp32 and o rounded once; the state's roundings over
+ * n calls add like sqrt n, the decay's own is not repeated), longer calls in the
  * chunked form on the matrix cores.  There bf16 operands meet in bf16 products
  * with fp32 accumulation: the decayed scores and the state's copy that meets q are
  * rounded to bf16, so that o is off by up to three roundings (2.0e-3 to 2.4e-3

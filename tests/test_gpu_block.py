@@ -612,6 +612,33 @@ def test_attention_states_that_remember_many_segments(dtype):
         assert max(err) <= TOL_STATE_LONG
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [1, 4])
+def test_attention_sessions_of_many_tokens(T, dtype):
+    """A state of size 1 carried through 4000 tokens, T at a call, that add 0.6 to it: each token
+    rounds it (the product's rest, the sum: 2 * 2^-24 / sqrt 3 rms), independently as what is added
+    differs: sqrt(4000) of them, 73 * 2^-24, bound 2^-17.  The rounding of the decay itself (up
+    to 2^-25) must not be among what is repeated: 4000 * 2^-25 is 1.2e-4."""
+    H, d, n = 4, 64, 4000
+    g = gen(18)
+    q, k, v = (normal(g, 1, n, H, d, dtype=dtype, std=s) for s in (1.0, 0.01, 1.0))
+    lg = torch.tensor([-2e-6, -7e-6, -3e-5, -3e-4], device="cuda")
+    st = normal(g, 1, H, d, d)
+    S = st.clone()
+    for t in range(0, n, T):
+        c = slice(t, t + T)
+        o, _ = block.linattn_forward(q[:, c], k[:, c], v[:, c], lg, state=S, state_out=S)
+    t = torch.arange(n, dtype=torch.float64)
+    for h in range(H):
+        w = torch.exp(float(lg[h]) * (n - 1 - t))[:, None]
+        kh, vh = (x[0, :, h].cpu().double() for x in (k, v))
+        want = st[0, h].cpu().double() * np.exp(float(lg[h]) * n) + (kh * w).t() @ vh
+        e = rel(f64(S[0, h]), want)
+        say(T, dtype, float(lg[h]), "%.2e" % e)
+        assert e <= 2.0 ** -17
+        assert rel(f64(o[0, -1, h]), q[0, -1, h].cpu().double() @ want * d ** -0.5) <= TOL_ROUND[dtype] + 2.0 ** -17
+
+
 @pytest.mark.parametrize("T", [4, 70, 600])
 def test_attention_layouts(T):
     """Head-first storage, slices of one projection, a batch repeated by a stride of 0: as
