@@ -155,15 +155,15 @@ ttt_status_t ttt_linattn_backward_workspace_size(const ttt_linattn_desc_t* desc,
  *   state_out  the state behind each sequence's last token; may be state_in
  *              itself (a session's state updated in place); may be NULL
  * Calls of up to 4 tokens run in the recurrent form (state read and
- * written once, all arithmetic in fp32 and o rounded once; the state's roundings over
- * n calls add like sqrt n, the decay's own is not repeated), longer calls in the
+ * written once, all arithmetic in fp32 and o rounded once), longer calls in the
  * chunked form on the matrix cores.  There bf16 operands meet in bf16 products
  * with fp32 accumulation: the decayed scores and the state's copy that meets q are
  * rounded to bf16, so that o is off by up to three roundings (2.0e-3 to 2.4e-3
  * against 64 bits, one rounding is 1.7e-3) where a call of 4 tokens is off by one;
  * the state itself is as exact as fp32 sums (2^-20 over some tens of chunks of 32
- * tokens, 1.4e-7 to 3.6e-7 measured; the roundings of n chunks that it remembers
- * add like sqrt n, to 1e-6 for 131072 tokens without a decay).
+ * tokens, 1.4e-7 to 3.6e-7 measured; the roundings of the n chunks, segments or
+ * calls that it remembers add like sqrt n, to 1e-6 for 131072 tokens without a decay
+ * and 2e-6 for 8192 tokens one by one; the decay's own rounding is not repeated).
  * fp32 operands use fp32 products throughout and round nothing else. */
 ttt_status_t ttt_linattn_forward(const ttt_linattn_desc_t* desc, const void* q, const void* k,
                                  const void* v, const float* log_decay, const int32_t* lengths,

@@ -639,6 +639,32 @@ def test_attention_sessions_of_many_tokens(T, dtype):
         assert rel(f64(o[0, -1, h]), q[0, -1, h].cpu().double() @ want * d ** -0.5) <= TOL_ROUND[dtype] + 2.0 ** -17
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [5, 8, 32, 33, 70])
+def test_attention_sessions_in_pieces(T, dtype):
+    """The same in calls of the chunked form: each rounds the state some eight times (six
+    accumulations and two decays a chunk), 1.6 * 2^-24 rms, sqrt(4000 / 5) of them: 46 * 2^-24,
+    bound 2^-17.4.  The rounding of a last chunk's decay, or of a call's first one, up to 2^-24
+    for each call, must not be among what is repeated: 4.8e-5 for 800 calls."""
+    H, d, n = 4, 64, 4000
+    g = gen(19)
+    q, k, v = (normal(g, 1, n, H, d, dtype=dtype, std=s) for s in (1.0, 0.01, 1.0))
+    lg = torch.tensor([-2e-6, -7e-6, -3e-5, -1e-4], device="cuda")
+    st = normal(g, 1, H, d, d)
+    S = st.clone()
+    for t in range(0, n, T):
+        c = slice(t, min(t + T, n))
+        block.linattn_forward(q[:, c], k[:, c], v[:, c], lg, state=S, state_out=S)
+    t = torch.arange(n, dtype=torch.float64)
+    for h in range(H):
+        w = torch.exp(float(lg[h]) * (n - 1 - t))[:, None]
+        kh, vh = (x[0, :, h].cpu().double() for x in (k, v))
+        want = st[0, h].cpu().double() * np.exp(float(lg[h]) * n) + (kh * w).t() @ vh
+        e = rel(f64(S[0, h]), want)
+        say(T, dtype, float(lg[h]), "%.2e" % e)
+        assert e <= 2.0 ** -17.4
+
+
 @pytest.mark.parametrize("T", [4, 70, 600])
 def test_attention_layouts(T):
     """Head-first storage, slices of one projection, a batch repeated by a stride of 0: as
