@@ -87,7 +87,8 @@ __device__ __forceinline__ float uniform(float x) {
 // rest each product is rounded for itself.  From |x| = 0.5 on little is left after
 // a few products, and the rest is left out.
 struct Decay {
-  float f, rest;
+  float f = 0.0f, rest = 0.0f;
+  Decay() = default;
   __device__ __forceinline__ explicit Decay(float x)
       : f(expf(x)), rest(fabsf(x) < 0.5f ? expm1f(x) - (f - 1.0f) : 0.0f) {}
   // s exp(x) + y
@@ -533,7 +534,7 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
   const auto state_row = [&](int i, int r) { return 32 * i + 16 * (r >> 3) + 8 * half + (r & 7); };
   const int at0 = 8 * half * rs + col * cs;
   const auto state_off = [&](int i, int r) { return at0 + (32 * i + 16 * (r >> 3) + (r & 7)) * rs; };
-  const auto from_slot = [&](int64_t j, float f) {  // S = f S + slot j
+  const auto from_slot = [&](int64_t j, const Decay& f) {  // S = f S + slot j
     const float4* p = slot + j * slot4;
     if (kPair ? pass == 1 : a.seg_trans) {
       // written by the pass with keys and values exchanged: this lane's key row
@@ -546,7 +547,7 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
           const int other = perm16(16 * (r >> 3) + 8 * half + (r & 7)) + lane_bits;
           const float x = reinterpret_cast<const float*>(
               p + ((i * NW + wave) * 4 + 2 * (w >> 4) + ((w & 7) >> 2)) * 64 + other)[w & 3];
-          S[i][r] = fmaf(f, S[i][r], x);
+          S[i][r] = f(S[i][r], x);
         }
       return;
     }
@@ -556,8 +557,8 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float4 x = p[(i * 4 + r) * 64];
-        S[i][4 * r] = fmaf(f, S[i][4 * r], x.x), S[i][4 * r + 1] = fmaf(f, S[i][4 * r + 1], x.y);
-        S[i][4 * r + 2] = fmaf(f, S[i][4 * r + 2], x.z), S[i][4 * r + 3] = fmaf(f, S[i][4 * r + 3], x.w);
+        S[i][4 * r] = f(S[i][4 * r], x.x), S[i][4 * r + 1] = f(S[i][4 * r + 1], x.y);
+        S[i][4 * r + 2] = f(S[i][4 * r + 2], x.z), S[i][4 * r + 3] = f(S[i][4 * r + 3], x.w);
       }
   };
   const auto to_slot = [&](int64_t j) {
@@ -576,9 +577,10 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
   if (kOut && slot) {
     if (t_lo < n || g == 0) {
       // few segments: their ends are added up here, otherwise by linattn_scan_kernel
-      const float f = exp2f(log2_decay(lg) * (float)seg_len);
+      const Decay f(lg * (float)seg_len);
       const int first = nseg <= kScanInPlace ? min(g, 1) : g;
-      for (int j = first; j <= g; ++j) from_slot(j, j == first ? 0.0f : f);
+      from_slot(first, Decay());
+      for (int j = first + 1; j <= g; ++j) from_slot(j, f);
     }
   } else if (g == 0 && a.s_in) {
 #pragma unroll
@@ -619,8 +621,8 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
   // g^kC is applied once per chunk, so the error of a rounded factor would grow
   // with the chunks that the state remembers: the two floats around g^kC take
   // turns so that their product stays within one rounding of the power.  In front of
-  // a sequence's last chunk, what is left of that rounding and of the last factor's
-  // goes into the product with that factor (a correction for itself would be rounded
+  // the last chunk of a sequence, or of a segment whose end is wanted, what is left of
+  // that rounding and of the last factor's goes into the product with that factor (a correction for itself would be rounded
   // off): over a session's calls it would add up in the same way.  8192 tokens, 5 or 8
   // a call, memories of 10^4 to 5 10^5: the state 2.2e-6 off at most, 4.8e-5 without;
   // calls of 5 tokens 38.8 -> 39.6 us (64 sessions), long ones within 1%.
@@ -805,8 +807,8 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
   for (int t = t_lo; t < t_hi; t += kC, buf ^= 1) {
     float step = err < 0.0f ? step_hi : step_lo;
     err += err < 0.0f ? err_hi : err_lo;
-    if (t + kC >= n) {  // the sequence's last chunk
-      const int m = n - t;
+    if (t + kC >= (kOut ? n : t_hi)) {  // the last chunk of a state that others start from
+      const int m = t_hi - t;
       if (m < kC) {
         const Decay d(lg * (float)m);
         err += d.f > 0.0f ? -d.rest / d.f : 0.0f;
@@ -814,7 +816,7 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
         step = d.f;
         f_out = a.scale_o * decay_pow(lg2, max(0, qrow - (kC - m)) + a.late);
       }
-      if (kOut && step > 0.5f && err != 0.0f) {
+      if (step > 0.5f && err != 0.0f) {
         const float rest = -step * err;
 #pragma unroll
         for (int i = 0; i < KT; ++i)

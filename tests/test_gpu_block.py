@@ -665,6 +665,31 @@ def test_attention_sessions_in_pieces(T, dtype):
         assert e <= 2.0 ** -17.4
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attention_sessions_in_calls_of_few_segments(dtype):
+    """The same in 128 calls of 512 tokens, each in eight segments: 2048 chunks of 1.6 * 2^-24 rms,
+    of a state that what is added makes four times larger: sqrt(2048 / 2) of them, 51 * 2^-24,
+    bound 2^-18.  The segments' factors, rounded by 2.7e-8 to 3e-8 for these decays, must not
+    be repeated 1024 times with their rounding: 3e-5."""
+    H, d, T, n = 4, 64, 512, 65536
+    g = gen(20)
+    q, k, v = (normal(g, 1, n, H, d, dtype=dtype, std=s) for s in (1.0, 0.015, 1.0))
+    lg = torch.tensor([-1.5e-6, -5.5e-6, -7e-6, -1.05e-5], device="cuda")
+    st = normal(g, 1, H, d, d)
+    S = st.clone()
+    for t in range(0, n, T):
+        c = slice(t, t + T)
+        block.linattn_forward(q[:, c], k[:, c], v[:, c], lg, state=S, state_out=S)
+    t = torch.arange(n, dtype=torch.float64)
+    for h in range(H):
+        w = torch.exp(float(lg[h]) * (n - 1 - t))[:, None]
+        kh, vh = (x[0, :, h].cpu().double() for x in (k, v))
+        want = st[0, h].cpu().double() * np.exp(float(lg[h]) * n) + (kh * w).t() @ vh
+        e = rel(f64(S[0, h]), want)
+        say(dtype, float(lg[h]), "%.2e" % e)
+        assert e <= 2.0 ** -18
+
+
 @pytest.mark.parametrize("T", [4, 70, 600])
 def test_attention_layouts(T):
     """Head-first storage, slices of one projection, a batch repeated by a stride of 0: as
