@@ -577,10 +577,12 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
   if (kOut && slot) {
     if (t_lo < n || g == 0) {
       // few segments: their ends are added up here, otherwise by linattn_scan_kernel
-      const Decay f(lg * (float)seg_len);
       const int first = nseg <= kScanInPlace ? min(g, 1) : g;
       from_slot(first, Decay());
-      for (int j = first + 1; j <= g; ++j) from_slot(j, f);
+      if (first < g) {
+        const Decay f(lg * (float)seg_len);
+        for (int j = first + 1; j <= g; ++j) from_slot(j, f);
+      }
     }
   } else if (g == 0 && a.s_in) {
 #pragma unroll
@@ -622,10 +624,11 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
   // with the chunks that the state remembers: the two floats around g^kC take
   // turns so that their product stays within one rounding of the power.  In front of
   // the last chunk of a sequence, or of a segment whose end is wanted, what is left of
-  // that rounding and of the last factor's goes into the product with that factor (a correction for itself would be rounded
-  // off): over a session's calls it would add up in the same way.  8192 tokens, 5 or 8
-  // a call, memories of 10^4 to 5 10^5: the state 2.2e-6 off at most, 4.8e-5 without;
-  // calls of 5 tokens 38.8 -> 39.6 us (64 sessions), long ones within 1%.
+  // that rounding and of the last factor's goes into the product with that factor (a
+  // correction for itself would be rounded off): over a session's calls it would add
+  // up in the same way.  8192 tokens, 5 or 8 a call, memories of 10^4 to 5 10^5: the
+  // state 2.2e-6 off at most, 4.8e-5 without; calls of 5 tokens 38.8 -> 39.6 us (64
+  // sessions), long ones within 1%.
   const double step64 = exp((double)lg * kC);
   const float step_lo = uniform(__double2float_rd(step64)), step_hi = uniform(__double2float_ru(step64));
   const float err_lo = uniform(step_lo > 0.0f ? (float)(step_lo / step64 - 1.0) : 0.0f);
@@ -803,11 +806,13 @@ __device__ __forceinline__ void chunked_pass(const LinArgs& a, float4* seg, int 
     wait_vmcnt<0>();  // the next chunk's tiles are here, the last one's outputs gone
     lds_barrier();
   };
+  // (from a segment's end a state goes on to the next call only if one came in)
+  const int last_of = kOut ? n : g == 0 && a.s_in ? t_hi : INT32_MAX;
   int buf = 0;
   for (int t = t_lo; t < t_hi; t += kC, buf ^= 1) {
     float step = err < 0.0f ? step_hi : step_lo;
     err += err < 0.0f ? err_hi : err_lo;
-    if (t + kC >= (kOut ? n : t_hi)) {  // the last chunk of a state that others start from
+    if (t + kC >= last_of) {  // the last chunk
       const int m = t_hi - t;
       if (m < kC) {
         const Decay d(lg * (float)m);
@@ -895,9 +900,9 @@ __global__ __launch_bounds__(64) void linattn_scan_kernel(float4* seg,
   const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x;
   if (i >= total) return;
   const int64_t head = i / slot4, e = i % slot4;
-  const Decay step(log_decay[head % H] * (float)seg_len);
   float4* p = seg + head * nseg * slot4 + e;
   float4 acc = p[slot4];
+  const Decay step(log_decay[head % H] * (float)seg_len);
   constexpr int kBatch = 8;  // loads in flight
   for (int g = 2; g < nseg; g += kBatch) {
     float4 x[kBatch];
