@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libttt_mlp.so")
 SOURCES = ["kernels.hip", "decode.hip", "backward.hip", "gemm.hip", "addnorm.hip",
-           "linattn.hip", "api.cpp", "backward_api.cpp", "block_api.cpp"]
+           "linattn.hip", "embed.hip", "gatedrec.hip", "act8.hip", "api.cpp",
+           "backward_api.cpp", "block_api.cpp", "seq_api.cpp"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

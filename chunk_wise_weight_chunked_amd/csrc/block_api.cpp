@@ -16,49 +16,6 @@ namespace {
 
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 
-bool valid_dtype(ttt_dtype_t t) { return t == TTT_F32 || t == TTT_BF16; }
-ttt::Dtype to_dtype(ttt_dtype_t t) { return t == TTT_BF16 ? ttt::Dtype::BF16 : ttt::Dtype::F32; }
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-
-// Buffers of one call: every one that is given must be 16-byte aligned, and no
-// output may overlap another buffer, except one it may be the same as.
-struct Buffers {
-  struct Item {
-    Range r;
-    const void* p;
-    bool out;
-    const void* may_be;  // an input this output may share its address with
-  };
-  Item items[16];  // more than any call has
-  int count = 0;
-  void in(const char* name, const void* p, size_t bytes) {
-    if (p) items[count++] = {range(name, p, bytes), p, false, nullptr};
-  }
-  void out(const char* name, const void* p, size_t bytes, const void* may_be = nullptr) {
-    if (p) items[count++] = {range(name, p, bytes), p, true, may_be};
-  }
-  ttt_status_t check() const {
-    for (int i = 0; i < count; ++i)
-      if (!aligned(items[i].p, 16))
-        return fail(TTT_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", items[i].r.name);
-    for (int i = 0; i < count; ++i)
-      for (int j = 0; j < count; ++j) {
-        const Item &a = items[i], &b = items[j];
-        if (i == j || !a.out || (b.out && j < i) || !overlaps(a.r, b.r)) continue;
-        if (a.may_be && a.may_be == b.p && a.p == b.p && !b.out) continue;
-        return fail(TTT_ERR_INVALID_ARGUMENT, "%s overlaps %s", a.r.name, b.r.name);
-      }
-    return TTT_OK;
-  }
-  // A small input that needs no 16-byte alignment.
-  ttt_status_t check_against(const Range& in) const {
-    for (int i = 0; i < count; ++i)
-      if (items[i].out && in.hi > in.lo && overlaps(in, items[i].r))
-        return fail(TTT_ERR_INVALID_ARGUMENT, "%s overlaps %s", items[i].r.name, in.name);
-    return TTT_OK;
-  }
-};
-
 // ------------------------------------------------ residual addition + norm
 ttt_status_t norm_args(const ttt_addnorm_desc_t* d, ttt::NormArgs* a) {
   if (!d) return fail(TTT_ERR_INVALID_ARGUMENT, "desc is NULL");
@@ -192,16 +149,6 @@ BackwardPlan backward_plan(const ttt_linattn_desc_t* d) {
   return p;
 }
 
-ttt_status_t check_workspace(const void* ws, size_t have, size_t need) {
-  if (need == 0) return TTT_OK;
-  if (!ws) return fail(TTT_ERR_INVALID_ARGUMENT, "ws is NULL (%zu bytes are needed)", need);
-  if (!aligned(ws, 256)) return fail(TTT_ERR_INVALID_ARGUMENT, "ws must be 256-byte aligned");
-  if (have < need)
-    return fail(TTT_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes is too small, %zu are needed",
-                have, need);
-  return TTT_OK;
-}
-
 // One token has no next one: its stride, which the limit above leaves free, must
 // not reach the chunked kernels' 32-bit offsets (of 31 rows, at a last chunk's end).
 ttt::LinOperand operand(const ttt_linattn_desc_t* d, const void* p, const int64_t st[3],
@@ -222,7 +169,7 @@ ttt_status_t ttt_addnorm_forward(const ttt_addnorm_desc_t* desc, const void* x, 
     return fail(TTT_ERR_INVALID_ARGUMENT, "y_scale must be given for TTT_NORM_FP8 and only then");
   const size_t es = ttt::dtype_bytes(a.dt), rs = ttt::dtype_bytes(a.res_dt);
   const size_t n = (size_t)a.rows * a.d;
-  Buffers b;
+  BufferList b;
   b.in("x", x, rows_bytes(a, a.x_stride, es));
   b.in("res", res, n * rs);
   b.in("w", w, a.d * es);
@@ -256,7 +203,7 @@ ttt_status_t ttt_addnorm_backward(const ttt_addnorm_desc_t* desc, const void* dy
   if (ttt_status_t st = check_workspace(ws, ws_bytes, need)) return st;
   const size_t es = ttt::dtype_bytes(a.dt), rs = ttt::dtype_bytes(a.res_dt);
   const size_t n = (size_t)a.rows * a.d;
-  Buffers b;
+  BufferList b;
   b.in("dy", dy, rows_bytes(a, a.x_stride, es));
   b.in("r", r, n * rs);
   b.in("w", w, a.d * es);
@@ -301,7 +248,7 @@ ttt_status_t ttt_linattn_forward(const ttt_linattn_desc_t* desc, const void* q, 
   const size_t need = forward_bytes(desc);
   if (ttt_status_t st = check_workspace(ws, ws_bytes, need)) return st;
   const int64_t H = desc->heads, G = desc->kv_heads;
-  Buffers b;
+  BufferList b;
   b.in("q", q, strided_bytes(desc, desc->q_stride, H, desc->d_key));
   b.in("k", k, strided_bytes(desc, desc->k_stride, G, desc->d_key));
   b.in("v", v, strided_bytes(desc, desc->v_stride, G, desc->d_value));
@@ -351,7 +298,7 @@ ttt_status_t ttt_linattn_backward(const ttt_linattn_desc_t* desc, const void* q,
   const int64_t K = desc->d_key, V = desc->d_value, rep = H / G;
   const ttt::Dtype dt = to_dtype(desc->dtype);
   const size_t es = ttt::dtype_bytes(dt);
-  Buffers b;
+  BufferList b;
   b.in("q", q, strided_bytes(desc, desc->q_stride, H, K));
   b.in("k", k, strided_bytes(desc, desc->k_stride, G, K));
   b.in("v", v, strided_bytes(desc, desc->v_stride, G, V));

@@ -1,0 +1,432 @@
+"""Host-side checks of the sequence operators' C ABI (no GPU needed): exports, and
+every refusal with its documented status before the device is touched.  Invalid
+calls use fake (never dereferenced) device addresses.  The 64-bit forms that the
+GPU tests compare with are checked here against differences."""
+import contextlib
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+from chunk_wise_weight_chunked_amd import seq
+from chunk_wise_weight_chunked_amd import ttt_mlp as tm
+
+import _seq_ref as ref
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
+                      "ttt_seq.h")
+A = 1 << 40  # fake addresses, 1 GiB apart
+INVALID, UNSUPPORTED = tm.TTT_ERR_INVALID_ARGUMENT, tm.TTT_ERR_UNSUPPORTED
+SMALL = tm.TTT_ERR_WORKSPACE_TOO_SMALL
+
+
+def at(i):
+    return A + (i << 30)
+
+
+def refused(call, status, word):
+    with pytest.raises(tm.TTTError) as e:
+        call()
+    assert e.value.status == status, e.value
+    assert word in str(e.value), str(e.value)
+
+
+def test_exports_every_declared_symbol():
+    lib = seq._load()
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(ttt_[a-z_0-9]+)\s*\(", text)))
+    assert set(names) == set(seq.EXPORTS)
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+# ---------------------------------------------------------------- embedding
+def embed_desc(**kw):
+    return seq.make_embed_desc(**(dict(tokens=100, vocab=50, d=64, dtype=torch.bfloat16) | kw))
+
+
+BAD_EMBED = [
+    (dict(tokens=0), INVALID, "tokens"),
+    (dict(vocab=0), INVALID, "vocab"),
+    (dict(tokens=(1 << 28) + 1), UNSUPPORTED, "tokens"),
+    (dict(vocab=(1 << 31) - 1), UNSUPPORTED, "vocab"),
+    (dict(d=0), INVALID, "d must"),
+    (dict(d=60), UNSUPPORTED, "d must"),
+    (dict(d=(1 << 20) + 8), UNSUPPORTED, "d must"),
+    (dict(tokens=1 << 28, d=2048), UNSUPPORTED, "tokens * d"),
+    (dict(vocab=1 << 30, d=2048), UNSUPPORTED, "vocab * d"),
+    (dict(scale=float("inf")), INVALID, "scale"),
+    (dict(scale=float("nan")), INVALID, "scale"),
+    (dict(dtype=7, out_dtype=7), INVALID, "dtype"),
+    (dict(dtype=torch.float32, out_dtype=torch.bfloat16), INVALID, "out_dtype"),
+    (dict(id_bytes=2), INVALID, "id_bytes"),
+    (dict(accumulate=2), INVALID, "accumulate"),
+]
+
+
+@pytest.mark.parametrize("kw,status,word", BAD_EMBED)
+def test_embed_refuses_descriptors(kw, status, word):
+    d = embed_desc(**kw)
+    refused(lambda: seq.ttt_embed_forward(d, at(1), at(2), at(3), 0), status, word)
+    refused(lambda: seq.ttt_embed_backward_workspace_size(d), status, word)
+    refused(lambda: seq.ttt_embed_backward(d, at(1), at(2), at(3), at(4), 1 << 29, 0), status, word)
+
+
+def test_embed_refuses_buffers():
+    d = embed_desc()
+    fwd = lambda *a: (lambda: seq.ttt_embed_forward(d, *a, stream=0))  # noqa: E731
+    for i in range(3):
+        bad = [at(1), at(2), at(3)]
+        bad[i] = None
+        refused(fwd(*bad), INVALID, "non-NULL")
+    refused(fwd(at(1) + 4, at(2), at(3)), INVALID, "8-byte")
+    refused(fwd(at(1), at(2) + 8, at(3)), INVALID, "16-byte")
+    refused(fwd(at(1), at(2), at(2) + 16), INVALID, "out overlaps table")
+    refused(fwd(at(3), at(2), at(3)), INVALID, "out overlaps ids")
+    narrow = embed_desc(id_bytes=4)
+    refused(lambda: seq.ttt_embed_forward(narrow, at(1) + 2, at(2), at(3), 0), INVALID, "4-byte")
+    need = seq.ttt_embed_backward_workspace_size(d)
+    bwd = lambda *a, n=need: (lambda: seq.ttt_embed_backward(d, *a, n, 0))  # noqa: E731
+    for i in range(3):
+        bad = [at(1), at(2), at(3), at(4)]
+        bad[i] = None
+        refused(bwd(*bad), INVALID, "non-NULL")
+    refused(bwd(at(1), at(2), at(3), None), INVALID, "ws is NULL")
+    refused(bwd(at(1), at(2), at(3), at(4) + 64), INVALID, "256-byte")
+    refused(bwd(at(1), at(2), at(3), at(4), n=need - 1), SMALL, "needed")
+    refused(bwd(at(1), at(2), at(2), at(4)), INVALID, "grad overlaps dout")
+    refused(bwd(at(1), at(2), at(3), at(3)), INVALID, "overlaps")
+    refused(bwd(at(4), at(2), at(3), at(4)), INVALID, "ws overlaps ids")
+
+
+# ----------------------------------------------------- gated linear recurrence
+def rec_desc(**kw):
+    return seq.make_gatedrec_desc(**(dict(batch=2, seq_len=300, d=64, dtype=torch.bfloat16) | kw))
+
+
+BAD_REC = [
+    (dict(batch=0), INVALID, "batch"),
+    (dict(seq_len=0), INVALID, "seq_len"),
+    (dict(d=0), INVALID, "d must"),
+    (dict(d=12), UNSUPPORTED, "d must"),
+    (dict(d=1 << 21), UNSUPPORTED, "d must"),
+    (dict(batch=(1 << 20) + 1, seq_len=1, d=8), UNSUPPORTED, "2^20"),
+    (dict(batch=1, seq_len=(1 << 29) + 1, d=8), UNSUPPORTED, "2^29"),
+    (dict(batch=1 << 14, seq_len=1, d=(1 << 14) + 8), UNSUPPORTED, "2^28"),
+    (dict(batch=1, seq_len=1 << 26, d=1024), UNSUPPORTED, "2^35"),
+    (dict(batch=1, seq_len=(1 << 62), d=8), UNSUPPORTED, "2^29"),
+    (dict(dtype=9), INVALID, "dtype"),
+    (dict(x_stride=(-8, 64)), INVALID, "strides"),
+    (dict(decay_stride=(64, 4)), UNSUPPORTED, "multiples of 8"),
+    (dict(input_stride=(1 << 41, 64)), UNSUPPORTED, "2^40"),
+    (dict(seq_len=1 << 20, x_stride=(0, 1 << 40)), UNSUPPORTED, "2^56"),
+    (dict(out_stride=(64, 64)), INVALID, "one place"),
+    (dict(out_stride=(300 * 64, 56)), INVALID, "one place"),
+    (dict(out_stride=(0, 64)), INVALID, "one place"),
+]
+
+
+@pytest.mark.parametrize("kw,status,word", BAD_REC)
+def test_gatedrec_refuses_descriptors(kw, status, word):
+    d = rec_desc(**kw)
+    refused(lambda: seq.ttt_gatedrec_forward(d, at(1), at(2), at(3), at(4), None, None, None, at(5),
+                                             None, at(8), 1 << 29, 0), status, word)
+    if word != "one place":
+        for fn in (seq.ttt_gatedrec_workspace_size, seq.ttt_gatedrec_backward_workspace_size,
+                   seq.ttt_gatedrec_saved_size):
+            refused(lambda: fn(d), status, word)
+
+
+def test_gatedrec_refuses_buffers():
+    d = rec_desc()
+    need = seq.ttt_gatedrec_workspace_size(d)
+    assert seq.ttt_gatedrec_saved_size(d) == 2 * 3 * 64 * 4
+    # x, decay, input, rate, lengths, state_in, state_out, h, saved
+    ok = [at(i) for i in range(1, 10)]
+    fwd = lambda a, ws=at(20), n=need: (  # noqa: E731
+        lambda: seq.ttt_gatedrec_forward(d, *a, ws, n, 0))
+    for i in (0, 1, 2, 3, 7):
+        bad = list(ok)
+        bad[i] = None
+        refused(fwd(bad), INVALID, "non-NULL")
+    for i in (0, 1, 2, 3, 5, 6, 7, 8):
+        bad = list(ok)
+        bad[i] += 8
+        refused(fwd(bad), INVALID, "16-byte")
+    bad = list(ok)
+    bad[4] += 2
+    refused(fwd(bad), INVALID, "4-byte")
+    for i, j in ((7, 0), (7, 2), (6, 3), (8, 5), (7, 4), (8, 7), (6, 7)):
+        bad = list(ok)
+        bad[i] = bad[j]
+        refused(fwd(bad), INVALID, "overlaps")
+    bad = list(ok)
+    bad[6] = bad[5] + 64  # in place is the same address or none
+    refused(fwd(bad), INVALID, "state_out overlaps state_in")
+    if need:
+        refused(fwd(ok, None, 0), INVALID, "ws is NULL")
+        refused(fwd(ok, at(20) + 16), INVALID, "256-byte")
+        refused(fwd(ok, n=need - 1), SMALL, "needed")
+        refused(fwd(ok, at(8)), INVALID, "overlaps")
+
+
+def test_gatedrec_backward_refusals():
+    d = rec_desc()
+    need = seq.ttt_gatedrec_backward_workspace_size(d)
+    # x, decay, input, rate, lengths, saved, dh, dstate_out, dx, ddecay, dinput, drate, dstate_in
+    ok = [at(i) for i in range(1, 14)]
+    bwd = lambda a, ws=at(20), n=need: (  # noqa: E731
+        lambda: seq.ttt_gatedrec_backward(d, *a, ws, n, 0))
+    for i in (0, 1, 2, 3, 5, 6, 8, 9, 10, 11):
+        bad = list(ok)
+        bad[i] = None
+        refused(bwd(bad), INVALID, "non-NULL")
+    refused(bwd(ok, None, 0), INVALID, "ws is NULL")
+    refused(bwd(ok, n=need - 1), SMALL, "needed")
+    for i, j in ((8, 0), (9, 1), (10, 2), (8, 9), (11, 3), (12, 5), (10, 6), (11, 4)):
+        bad = list(ok)
+        bad[i] = bad[j]
+        refused(bwd(bad), INVALID, "overlaps")
+
+
+# ---------------------------------------------------------- activations in 8 bits
+def act_desc(**kw):
+    return seq.make_act8_desc(**(dict(rows=10, d=64, dtype=torch.bfloat16) | kw))
+
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(rows=0), INVALID, "rows"),
+    (dict(rows=1 << 31), UNSUPPORTED, "rows"),
+    (dict(d=0), INVALID, "d must"),
+    (dict(d=36), UNSUPPORTED, "d must"),
+    (dict(rows=1 << 30, d=2048), UNSUPPORTED, "2^40"),
+    (dict(x_stride=56), INVALID, "x_stride"),
+    (dict(x_stride=68), UNSUPPORTED, "x_stride"),
+    (dict(rows=1 << 30, x_stride=1 << 40), UNSUPPORTED, "2^56"),
+    (dict(dtype=5), INVALID, "dtype"),
+])
+def test_act8_refuses_descriptors(kw, status, word):
+    d = act_desc(**kw)
+    refused(lambda: seq.ttt_act8_store(d, at(1), at(2), at(3), 0), status, word)
+    refused(lambda: seq.ttt_act8_load(d, at(1), at(2), at(3), 0), status, word)
+
+
+def test_act8_refuses_buffers():
+    d = act_desc()
+    for fn in (seq.ttt_act8_store, seq.ttt_act8_load):
+        for i in range(3):
+            bad = [at(1), at(2), at(3)]
+            bad[i] = None
+            refused(lambda: fn(d, *bad, 0), INVALID, "non-NULL")
+        refused(lambda: fn(d, at(1) + 8, at(2), at(3), 0), INVALID, "16-byte")
+    store = lambda *a: (lambda: seq.ttt_act8_store(d, *a, 0))  # noqa: E731
+    refused(store(at(1), at(1), at(3)), INVALID, "codes overlaps x")
+    refused(store(at(1), at(2), at(1) + 3), INVALID, "exps overlaps x")
+    refused(store(at(1), at(2) + 8, at(3)), INVALID, "16-byte")
+    load = lambda *a: (lambda: seq.ttt_act8_load(d, *a, 0))  # noqa: E731
+    refused(load(at(1), at(2), at(1)), INVALID, "x overlaps codes")
+    refused(load(at(1), at(2), at(3) + 8), INVALID, "16-byte")
+    refused(lambda: seq.ttt_act8_store(d, at(1), at(2), at(2) + 16, 0), INVALID, "exps overlaps codes")
+    refused(lambda: seq.ttt_act8_load(d, at(1), at(2), at(2), 0), INVALID, "x overlaps exps")
+
+
+BAD_WGRAD = [
+    (dict(rows=0), INVALID, "rows"),
+    (dict(rows=1 << 31), UNSUPPORTED, "rows"),
+    (dict(d_in=4), UNSUPPORTED, "d_in"),
+    (dict(d_out=0), INVALID, "d_out"),
+    (dict(d_out=1 << 21), UNSUPPORTED, "d_out"),
+    (dict(rows=1 << 30, d_in=2048), UNSUPPORTED, "rows * d_in"),
+    (dict(d_in=1 << 19, d_out=1 << 18), UNSUPPORTED, "2^36"),
+    (dict(dy_stride=40), INVALID, "dy_stride"),
+    (dict(dy_stride=52), UNSUPPORTED, "dy_stride"),
+    (dict(dtype=4), INVALID, "dtype"),
+    (dict(dtype=torch.float32, grad_dtype=torch.bfloat16), INVALID, "grad_dtype"),
+    (dict(accumulate=3), INVALID, "accumulate"),
+    (dict(grad_dtype=torch.bfloat16, accumulate=1), INVALID, "accumulate needs"),
+]
+
+
+def wgrad_desc(**kw):
+    return seq.make_act8_wgrad_desc(**(dict(rows=100, d_in=64, d_out=48, dtype=torch.bfloat16) | kw))
+
+
+@pytest.mark.parametrize("kw,status,word", BAD_WGRAD)
+def test_weight_grad_refuses_descriptors(kw, status, word):
+    d = wgrad_desc(**kw)
+    refused(lambda: seq.ttt_act8_weight_grad_workspace_size(d), status, word)
+    refused(lambda: seq.ttt_act8_weight_grad(d, at(1), at(2), at(3), at(4), at(5), 1 << 29, 0),
+            status, word)
+
+
+def test_weight_grad_refuses_buffers():
+    d = wgrad_desc()
+    need = seq.ttt_act8_weight_grad_workspace_size(d)
+    ok = [at(i) for i in range(1, 5)]
+    call = lambda a, ws=at(9), n=need: (  # noqa: E731
+        lambda: seq.ttt_act8_weight_grad(d, *a, ws, n, 0))
+    for i in range(4):
+        bad = list(ok)
+        bad[i] = None
+        refused(call(bad), INVALID, "non-NULL")
+    for i in (0, 2, 3):
+        bad = list(ok)
+        bad[i] += 8
+        refused(call(bad), INVALID, "16-byte")
+    for j in range(3):
+        bad = list(ok)
+        bad[3] = bad[j]
+        refused(call(bad), INVALID, "grad overlaps")
+    if need:
+        refused(call(ok, None, 0), INVALID, "ws is NULL")
+        refused(call(ok, at(9) + 128), INVALID, "256-byte")
+        refused(call(ok, n=need - 1), SMALL, "needed")
+        refused(call(ok, at(2)), INVALID, "overlaps")
+
+
+def test_sizes_need_a_place_to_go():
+    lib = seq._load()
+    for name, d in (("ttt_embed_backward_workspace_size", embed_desc()),
+                    ("ttt_gatedrec_saved_size", rec_desc()),
+                    ("ttt_gatedrec_workspace_size", rec_desc()),
+                    ("ttt_gatedrec_backward_workspace_size", rec_desc()),
+                    ("ttt_act8_weight_grad_workspace_size", wgrad_desc())):
+        assert getattr(lib, name)(ctypes.byref(d), None) == INVALID
+        n = ctypes.c_size_t(0)
+        assert getattr(lib, name)(None, ctypes.byref(n)) == INVALID
+        assert getattr(lib, name)(ctypes.byref(d), ctypes.byref(n)) == 0
+        assert tm.ttt_last_error() == ""
+
+
+# ------------------------------------------------------------------ the binding
+def test_binding_refuses_tensors():
+    ids, t = torch.zeros(3, dtype=torch.int64), torch.zeros(10, 16)
+    for bad in (dict(ids=ids.short()), dict(ids=ids.float()), dict(table=t.double()),
+                dict(table=t[0]), dict(table=t[:0]), dict(out_dtype=torch.bfloat16),
+                dict()):  # CPU tensors
+        with pytest.raises(ValueError):
+            seq.embed_forward(**(dict(ids=ids, table=t) | bad))
+    dout = torch.zeros(3, 16)
+    for bad in (dict(dout=dout[:2]), dict(dout=dout.double()), dict(ids=ids.bool()),
+                dict(grad=t[:9]), dict(grad=t.bfloat16()), dict(grad_dtype=torch.bfloat16),
+                dict(grad=t, grad_dtype=torch.float64), dict()):
+        with pytest.raises(ValueError):
+            seq.embed_backward(**(dict(dout=dout, ids=ids, vocab=10) | bad))
+    x, rate = torch.zeros(2, 5, 16), torch.zeros(16)
+    base = dict(x=x, decay_gate=x, input_gate=x, rate=rate)
+    bads = (dict(x=x[0]), dict(x=x[:, :0]), dict(x=x.double()), dict(decay_gate=x[:, :4]),
+            dict(input_gate=x.bfloat16()), dict(rate=rate[:8]), dict(rate=rate.double()),
+            dict(lengths=torch.zeros(2)), dict(lengths=torch.zeros(3, dtype=torch.int32)), dict())
+    for bad in bads + (dict(state=torch.zeros(2, 8)), dict(state_out=rate),
+                       dict(x=x.transpose(1, 2).contiguous().transpose(1, 2))):
+        with pytest.raises(ValueError):
+            seq.gatedrec_forward(**(base | bad))
+    back = dict(dh=x, saved=torch.zeros(2, 1, 16))
+    for bad in bads + (dict(dh=x[:, :3]), dict(dh=x.bfloat16()), dict(saved=None),
+                       dict(saved=torch.zeros(2, 2, 16)), dict(dstate_out=torch.zeros(16))):
+        with pytest.raises(ValueError):
+            seq.gatedrec_backward(**(base | back | bad))
+    codes, exps = torch.zeros(4, 40, dtype=torch.int8), torch.zeros(4, 2, dtype=torch.uint8)
+    for bad in (torch.zeros(4, 40).double(), torch.zeros(0, 8), torch.tensor(1.0),
+                torch.zeros(2, 3, 8).transpose(0, 1), torch.zeros(4, 40)):
+        with pytest.raises(ValueError):
+            seq.act8_store(bad)
+    for bad in (dict(codes=codes.byte()), dict(exps=exps[:3]), dict(exps=exps.char()),
+                dict(dtype=torch.float16), dict()):
+        with pytest.raises(ValueError):
+            seq.act8_load(**(dict(codes=codes, exps=exps) | bad))
+    dy = torch.zeros(4, 24)
+    for bad in (dict(dy=dy[:3]), dict(dy=dy.double()), dict(dy=dy[:, :0]), dict(exps=exps[:, :1]),
+                dict(grad_dtype=torch.bfloat16), dict(grad=torch.zeros(24, 40)),
+                dict(grad=torch.zeros(40, 24).bfloat16()), dict()):
+        with pytest.raises(ValueError):
+            seq.act8_weight_grad(**(dict(codes=codes, exps=exps, dy=dy) | bad))
+
+
+def test_calls_without_tokens():
+    e = torch.zeros(0, dtype=torch.int64)
+    assert seq.embed_forward(e, torch.zeros(10, 16)).shape == (0, 16)
+    g = seq.embed_backward(torch.zeros(0, 16), e, 10)
+    assert g.shape == (10, 16) and not g.any()
+    keep = torch.ones(10, 16)
+    assert seq.embed_backward(torch.zeros(0, 16), e, 10, grad=keep) is keep and keep.all()
+
+
+def test_a_scale_counts_with_its_value(monkeypatch):
+    seen = []
+    monkeypatch.setattr(seq, "ttt_embed_forward", lambda d, *a, **k: seen.append(d.scale))
+    monkeypatch.setattr(seq, "ttt_embed_backward", lambda d, *a, **k: seen.append(d.scale))
+    ids, t = torch.zeros(3, dtype=torch.int64), torch.zeros(10, 16)
+    s = torch.tensor(0.5)
+    for v in (0.5, 2.0):
+        s.fill_(v)
+        seq.embed_forward(ids, t, s)
+        assert seen.pop() == v
+        seq.embed_backward(torch.zeros(3, 16), ids, 10, s)
+        assert seen.pop() == v
+
+
+def test_streams_and_workspaces_given(monkeypatch):
+    """A stream given as a handle is the one that a call runs and allocates on; a workspace is
+    looked at like every other tensor."""
+    entered, looked = [], []
+    monkeypatch.setattr(seq, "_on", lambda s, like: entered.append(s) or contextlib.nullcontext())
+    monkeypatch.setattr(seq, "_same_device", lambda like, *t: looked.extend(t))
+    for name in ("ttt_embed_forward", "ttt_embed_backward", "ttt_gatedrec_forward",
+                 "ttt_gatedrec_backward", "ttt_act8_store", "ttt_act8_load",
+                 "ttt_act8_weight_grad"):
+        monkeypatch.setattr(seq, name, lambda *a, **k: None)
+    ids, t, ws = torch.zeros(3, dtype=torch.int64), torch.zeros(10, 16), torch.zeros(256)
+    x, rate = torch.zeros(2, 5, 16), torch.zeros(16)
+    codes, exps = torch.zeros(4, 40, dtype=torch.int8), torch.zeros(4, 2, dtype=torch.uint8)
+    calls = (lambda **k: seq.embed_backward(torch.zeros(3, 16), ids, 10, **k),
+             lambda **k: seq.gatedrec_forward(x, x, x, rate, **k),
+             lambda **k: seq.gatedrec_backward(x, x, x, rate, x, torch.zeros(2, 1, 16), **k),
+             lambda **k: seq.act8_weight_grad(codes, exps, torch.zeros(4, 24), **k))
+    for call in calls:
+        call(ws=ws)
+        assert any(q is ws for q in looked)
+        looked.clear()
+    for call in calls + (lambda **k: seq.embed_forward(ids, t, **k), lambda **k: seq.act8_store(t, **k),
+                         lambda **k: seq.act8_load(codes, exps, **k)):
+        call(stream=0)
+        assert entered.pop() == 0 and not entered
+
+
+# ------------------------------------------------ the 64-bit forms against differences
+def test_gatedrec_reference_against_differences():
+    rng = np.random.default_rng(3)
+    B, T, d = 2, 6, 5
+    n = rng.normal
+    x, dg, ig, dh = (n(size=(B, T, d)) for _ in range(4))
+    rate, st, ds, ln = rng.uniform(0.1, 2, size=d), n(size=(B, d)), n(size=(B, d)), [6, 4]
+    dh[1, 4:] = 0
+    grads = ref.gatedrec_grads(x, dg, ig, rate, dh, st, ds, ln)
+
+    def f(*a):
+        h, S = ref.gatedrec(*a[:4], a[4], ln)
+        return (dh * h).sum() + (ds * S).sum()
+
+    e = 1e-6
+    args = [x, dg, ig, rate, st]
+    for i, g in enumerate(grads):
+        u = n(size=args[i].shape)
+        hi, lo = list(args), list(args)
+        hi[i], lo[i] = args[i] + e * u, args[i] - e * u
+        # third derivatives times e^2 and 2^-52 / e: both far below
+        assert abs((f(*hi) - f(*lo)) / (2 * e) - (g * u).sum()) < 1e-8 * max(1, np.abs(g * u).sum())
+
+
+def test_act8_reference():
+    x = np.array([[127.0] + [0] * 31 + [127.01] + [0.5] * 7, [0.0] * 40])
+    codes, exps = ref.act8(x)
+    assert exps.tolist() == [[127, 128], [1, 1]]
+    assert codes[0, 0] == 127 and codes[0, 32] == 64 and (codes[0, 33:] == 0).all()
+    v = ref.act8_value(codes, exps)
+    assert v[0, 0] == 127 and v[0, 32] == 128 and not v[1].any()
+    x[1, 3] = np.nan
+    codes, exps = ref.act8(x)
+    assert exps[1, 0] == 255 and np.isnan(ref.act8_value(codes, exps)[1, :32]).all()
