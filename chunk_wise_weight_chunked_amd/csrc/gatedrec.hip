@@ -6,13 +6,18 @@
 // and for the gradients, from the last token, with c the part of the gradient of
 // h_t that comes from behind:
 //   l_t = dh_t + c_{t+1},  c_t = a_t l_t
-//   dx = l b i,  dinput = l u (1 - i),  y = l (a h_{t-1} - u a^2 / b^2)
+//   dx = l b i,  dinput = l u (1 - i),  y = l a (h_{t-1} - i x a / b)
 //   ddecay = y z (1 - r),  drate = -sum y r
 //
 // A channel is a chain of its own; the tokens of one are cut into tiles of
 // kRecTile, and a tile into runs that a lane holds in registers.  A run, a tile
 // or a row of tiles maps the state in front of it to that behind it by
 // h -> e^Z h + H with Z the sum of its z: two numbers a channel, that compose.
+//
+// Both directions are bound by HBM and read their inputs once: a workgroup loads a
+// tile, publishes its map, takes the state in front of it from the tiles in front (from the
+// nearest that knows its own, through the maps of those between) and writes the tile's
+// results from its registers.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -45,9 +50,14 @@ __device__ __forceinline__ bool near_one(float dec) { return __float_as_uint(dec
 __device__ __forceinline__ float decayed(float dec, float h, float u) {
   return __builtin_fmaf(dec, h, u) + (near_one(dec) ? h : 0.0f);
 }
-// 1 - a^2 = (1 - a)(1 + a)
+// 1 - a^2 = (1 - a)(1 + a), and 1 / b (0 where b is); b is their product.  The root's
+// instruction takes values below 2^-126 as 0: it is given 2^64 times its argument.
 __device__ __forceinline__ float one_minus_square(float dec) {
   return near_one(dec) ? -dec * (2.0f + dec) : (1.0f - dec) * (1.0f + dec);
+}
+__device__ __forceinline__ float inverse_root(float bb) {
+  const float inv = __builtin_amdgcn_rsqf(bb * 0x1p64f) * 0x1p32f;
+  return bb == 0.0f ? 0.0f : inv;
 }
 // z is never positive: a rate below 0 counts as NaN.
 __device__ __forceinline__ float rate_at(const float* rate, int64_t c) {
@@ -89,10 +99,6 @@ struct TileShapeOf {
   static constexpr int kRun = kRecTile / kRuns;
 };
 
-// Where a workgroup's tile is.
-struct TileAt {
-  int64_t b, j, strip;
-};
 __device__ __forceinline__ int64_t tokens_of(const RecArgs& a, int64_t b) {
   if (!a.lengths) return a.T;
   const int64_t n = a.lengths[b];
@@ -107,8 +113,8 @@ __device__ __forceinline__ void token(const uint4& vx, const uint4& vg, const ui
   for (int c = 0; c < Lane<T>::kPer; ++c) {
     z[c] = -rate[c] * sigmoid(chunk_value<T>(vg, c));
     dec[c] = decay_of(z[c]);
-    u[c] = sqrtf(one_minus_square(dec[c])) * sigmoid(chunk_value<T>(vi, c)) *
-           chunk_value<T>(vx, c);
+    const float bb = one_minus_square(dec[c]);
+    u[c] = bb * inverse_root(bb) * sigmoid(chunk_value<T>(vi, c)) * chunk_value<T>(vx, c);
   }
 }
 
@@ -158,11 +164,89 @@ __global__ __launch_bounds__(kBlock) void rec_step_kernel(RecArgs a, const float
   }
 }
 
-// The tile of a workgroup, strips of a tile next to each other.
-__device__ __forceinline__ TileAt tile_at(const RecArgs& a, int64_t tiles) {
-  const int64_t strips = (a.d + kStrip - 1) / kStrip;
-  const int64_t w = blockIdx.x;
-  return {(w / strips) / tiles, (w / strips) % tiles, w % strips};
+// ------------------------------------------------- tiles and what links them
+// A tile's word for the tiles behind it (backward: in front of it), one for each
+// channel: the decay over the tile and the state behind it from 0, or once it is known
+// the state behind it, marked by +inf, which no decay is.  Both halves come and go in
+// one 64-bit access, so a word needs no other ordering; it starts as kUnset, a NaN that
+// no decay is stored as.
+constexpr uint64_t kUnset = ~0ull;
+constexpr uint32_t kState = 0x7f800000u;
+__device__ __forceinline__ uint64_t word_of(float dec, float h) {
+  const uint32_t hi = dec != dec ? 0x7fc00000u : __float_as_uint(dec);
+  return (uint64_t)hi << 32 | __float_as_uint(h);
+}
+__device__ __forceinline__ uint64_t state_word(float h) {
+  return (uint64_t)kState << 32 | __float_as_uint(h);
+}
+__device__ __forceinline__ void put_word(uint64_t* p, uint64_t w) {
+  __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t get_word(const uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Words unset, the counter of begun tiles at 0.
+__global__ __launch_bounds__(kBlock) void rec_clear_kernel(uint4* __restrict__ words, int64_t n,
+                                                           uint32_t* __restrict__ begun) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *begun = 0;
+  const int64_t step = (int64_t)gridDim.x * kBlock;
+  for (int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x; i < n; i += step)
+    words[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
+struct Links {
+  uint64_t* words;   // [B][tiles][d], null where there is one tile
+  uint32_t* begun;
+  int64_t tiles;
+};
+
+// The workgroup's tile.  Tiles are handed out in the order in which workgroups begin,
+// those of all sequences and strips at one place before those behind it (backward: in
+// front of it): every tile that this one waits for is at work already, and the first
+// of a sequence waits for none, so that all waits end whatever the order of workgroups.
+struct TileAt {
+  int64_t b, j, strip, k;  // k: tiles that come before it in its sequence
+};
+__device__ __forceinline__ TileAt tile_at(const RecArgs& a, const Links& links, bool reverse) {
+  __shared__ uint32_t ticket;
+  uint32_t w = blockIdx.x;
+  if (links.words) {
+    if (threadIdx.x == 0)
+      ticket = __hip_atomic_fetch_add(links.begun, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    w = ticket;
+  }
+  const uint32_t strips = (uint32_t)((a.d + kStrip - 1) / kStrip), row = strips * (uint32_t)a.B;
+  TileAt at;
+  at.k = w / row;
+  at.b = w % row / strips;
+  at.strip = w % strips;
+  at.j = reverse ? links.tiles - 1 - at.k : at.k;
+  return at;
+}
+
+// The state in front of tile k of a channel (k > 0), from the words of tiles k - 1,
+// k - 2, ... at `word`, `step` words apart: from the nearest of kAhead that has its
+// state, the tiles behind that one applied in order, just as they do it themselves, so
+// that the result does not depend on which one it was.
+__device__ __forceinline__ float state_before(const uint64_t* word, int64_t step, int64_t k) {
+  constexpr int kAhead = 8;
+  for (;;) {
+    uint64_t w[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) w[i] = get_word(word + min<int64_t>(i, k - 1) * step);
+    bool found = false;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = kAhead - 1; i >= 0; --i) {
+      const uint32_t hi = (uint32_t)(w[i] >> 32);
+      const float f = __uint_as_float((uint32_t)w[i]);
+      found = hi == kState || (found && w[i] != kUnset);
+      s = hi == kState ? f : decayed(__uint_as_float(hi), s, f);
+    }
+    if (found) return s;
+  }
 }
 
 // What a lane of a tile works on.
@@ -172,7 +256,6 @@ struct LaneAt {
   int lane, run;
   int n;                 // tokens of its run that count
   int rows;              // tokens of its run inside T
-  bool live;             // channels inside d
   float rate[Lane<T>::kPer];
 };
 template <typename T>
@@ -183,12 +266,12 @@ __device__ __forceinline__ LaneAt<T> lane_at(const RecArgs& a, const TileAt& at)
   l.b = at.b, l.j = at.j;
   l.c0 = at.strip * kStrip + l.lane * S::kPer;
   l.t0 = at.j * kRecTile + l.run * S::kRun;
-  l.live = l.c0 < a.d;
+  const bool live = l.c0 < a.d;
   const int64_t n = tokens_of(a, at.b);
-  l.n = l.live ? (int)min<int64_t>(max<int64_t>(n - l.t0, 0), S::kRun) : 0;
-  l.rows = l.live ? (int)min<int64_t>(max<int64_t>(a.T - l.t0, 0), S::kRun) : 0;
+  l.n = live ? (int)min<int64_t>(max<int64_t>(n - l.t0, 0), S::kRun) : 0;
+  l.rows = live ? (int)min<int64_t>(max<int64_t>(a.T - l.t0, 0), S::kRun) : 0;
 #pragma unroll
-  for (int c = 0; c < S::kPer; ++c) l.rate[c] = l.live ? rate_at(a.rate, l.c0 + c) : 0.0f;
+  for (int c = 0; c < S::kPer; ++c) l.rate[c] = live ? rate_at(a.rate, l.c0 + c) : 0.0f;
   return l;
 }
 template <typename T>
@@ -196,27 +279,114 @@ __device__ __forceinline__ const T* row_of(const RecOperand& o, const LaneAt<T>&
   return static_cast<const T*>(o.p) + l.b * o.sb + l.t0 * o.st + l.c0;
 }
 
-// z sums and states (from 0) of a workgroup's runs, by run and channel.
+// The runs of a tile in LDS, by run and channel: decays over a run and states behind
+// it from 0, sums of z.  A wave folds kRuns / kParts of them for 64 channels.
+constexpr int kParts = kBlock / 64;
 template <typename T>
-struct RunSums {
-  float z[TileShapeOf<T>::kRuns][kStrip], h[TileShapeOf<T>::kRuns][kStrip];
+struct alignas(16) Runs {
+  static constexpr int kRuns = TileShapeOf<T>::kRuns, kEach = kRuns / kParts;
+  float z[kRuns][kStrip], dec[kRuns][kStrip], h[kRuns][kStrip];
+  float part_z[kParts][kStrip], part_h[kParts][kStrip];
 };
 
-// A run's decays and u; its sum of z and its state from 0.
+// A lane's run into LDS.
 template <typename T>
-__device__ __forceinline__ void load_run(const RecArgs& a, const LaneAt<T>& l,
-                                         float dec[][Lane<T>::kPer], float u[][Lane<T>::kPer],
-                                         float* Z, float* H) {
+__device__ __forceinline__ void put_run(Runs<T>& rs, const LaneAt<T>& l, const float* Z,
+                                        const float* H) {
+#pragma unroll
+  for (int c = 0; c < Lane<T>::kPer; ++c) {
+    const int k = l.lane * Lane<T>::kPer + c;
+    rs.z[l.run][k] = Z[c], rs.dec[l.run][k] = decay_of(Z[c]), rs.h[l.run][k] = H[c];
+  }
+}
+
+// From the runs in LDS to the state in front of each run, which takes the place of its
+// h: the waves fold their runs, the first wave folds the waves' and links the tile with
+// the ones before it, the waves go through their runs once more.  first: the state of
+// the channel in front of the first tile; done(channel, state in front of the tile,
+// state behind it) in the first wave.
+template <typename T, bool kReverse, class First, class Done>
+__device__ __forceinline__ void link_tile(Runs<T>& rs, const RecArgs& a, const Links& links,
+                                          const TileAt& at, First&& first, Done&& done) {
+  using R = Runs<T>;
+  const int ch = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const auto run = [&](int i) { return kReverse ? R::kRuns - 1 - i : i; };
+  __syncthreads();
+  float z = -0.0f, h = 0.0f;
+#pragma unroll
+  for (int i = 0; i < R::kEach; ++i) {
+    const int r = run(wave * R::kEach + i);
+    h = decayed(rs.dec[r][ch], h, rs.h[r][ch]);
+    z += rs.z[r][ch];
+  }
+  rs.part_z[wave][ch] = z, rs.part_h[wave][ch] = h;
+  __syncthreads();
+  const int64_t c = at.strip * kStrip + ch;
+  if (wave == 0 && c < a.d) {
+    float dec[kParts], z = -0.0f, ph = 0.0f;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const float zp = rs.part_z[p][ch];
+      dec[p] = decay_of(zp);
+      ph = decayed(dec[p], ph, rs.part_h[p][ch]);
+      z += zp;
+    }
+    const float whole = decay_of(z);
+    float s;
+    if (links.words) {
+      uint64_t* const word = links.words + (at.b * links.tiles + at.k) * a.d + c;
+      if (at.k == 0) {
+        s = first(c);
+      } else {
+        if (at.k + 1 < links.tiles) put_word(word, word_of(whole, ph));
+        s = state_before(word - a.d, -a.d, at.k);
+      }
+      if (at.k + 1 < links.tiles) put_word(word, state_word(decayed(whole, s, ph)));
+    } else {
+      s = first(c);
+    }
+    const float before = s;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const float next = decayed(dec[p], s, rs.part_h[p][ch]);
+      rs.part_h[p][ch] = s;  // the state in front of the part
+      s = next;
+    }
+    done(c, before, decayed(whole, before, ph));
+  }
+  __syncthreads();
+  float s = rs.part_h[wave][ch];
+#pragma unroll
+  for (int i = 0; i < R::kEach; ++i) {
+    const int r = run(wave * R::kEach + i);
+    const float next = decayed(rs.dec[r][ch], s, rs.h[r][ch]);
+    rs.h[r][ch] = s;
+    s = next;
+  }
+  __syncthreads();
+}
+
+// A tile's outputs.
+template <typename T>
+__global__ __launch_bounds__(kBlock) void rec_forward_kernel(RecArgs a, Links links,
+                                                             const float* s_in, float* s_out,
+                                                             T* __restrict__ h, int64_t hsb,
+                                                             int64_t hst,
+                                                             float* __restrict__ saved) {
   using S = TileShapeOf<T>;
+  __shared__ Runs<T> rs;
+  const TileAt at = tile_at(a, links, false);
+  const LaneAt<T> l = lane_at<T>(a, at);
   uint4 vx[S::kRun], vg[S::kRun], vi[S::kRun];
   const T *x = row_of<T>(a.x, l), *g = row_of<T>(a.decay, l), *in = row_of<T>(a.input, l);
 #pragma unroll
   for (int t = 0; t < S::kRun; ++t)
     if (t < l.n) {
-      vx[t] = get16(x + t * a.x.st);
       vg[t] = get16(g + t * a.decay.st);
       vi[t] = get16(in + t * a.input.st);
+      vx[t] = get16(x + t * a.x.st);
     }
+  float dec[S::kRun][S::kPer], u[S::kRun][S::kPer], Z[S::kPer], H[S::kPer];
 #pragma unroll
   for (int c = 0; c < S::kPer; ++c) Z[c] = -0.0f, H[c] = 0.0f;
 #pragma unroll
@@ -234,83 +404,13 @@ __device__ __forceinline__ void load_run(const RecArgs& a, const LaneAt<T>& l,
       H[c] = decayed(dec[t][c], H[c], u[t][c]);
     }
   }
-}
-
-// Each tile's sum of z and state from 0: sums [B][tiles][d] of (Z, H).
-template <typename T>
-__global__ __launch_bounds__(kBlock) void rec_sums_kernel(RecArgs a, int64_t tiles,
-                                                          float2* __restrict__ sums) {
-  using S = TileShapeOf<T>;
-  __shared__ RunSums<T> rs;
-  const TileAt at = tile_at(a, tiles);
-  const LaneAt<T> l = lane_at<T>(a, at);
-  float dec[S::kRun][S::kPer], u[S::kRun][S::kPer], Z[S::kPer], H[S::kPer];
-  load_run<T>(a, l, dec, u, Z, H);
-#pragma unroll
-  for (int c = 0; c < S::kPer; ++c) {
-    rs.z[l.run][l.lane * S::kPer + c] = Z[c];
-    rs.h[l.run][l.lane * S::kPer + c] = H[c];
-  }
-  __syncthreads();
-  const int64_t ch = at.strip * kStrip + threadIdx.x;
-  if (threadIdx.x >= kStrip || ch >= a.d) return;
-  float z = -0.0f, h = 0.0f;
-  for (int r = 0; r < S::kRuns; ++r) {
-    h = decayed(decay_of(rs.z[r][threadIdx.x]), h, rs.h[r][threadIdx.x]);
-    z += rs.z[r][threadIdx.x];
-  }
-  sums[(at.b * tiles + at.j) * a.d + ch] = make_float2(z, h);
-}
-
-// The state in front of every tile, and behind the last (backward: the gradient
-// that comes from behind every tile, and in front of the first).
-__global__ __launch_bounds__(kBlock) void rec_scan_kernel(const float2* __restrict__ sums,
-                                                          const float* s_in, float* s_out,
-                                                          float* __restrict__ starts, int64_t B,
-                                                          int64_t tiles, int64_t d, bool reverse) {
-  const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-  if (i >= B * d) return;
-  const int64_t b = i / d, ch = i % d;
-  float s = s_in ? s_in[i] : 0.0f;
-  for (int64_t k = 0; k < tiles; ++k) {
-    const int64_t j = reverse ? tiles - 1 - k : k;
-    const int64_t o = (b * tiles + j) * d + ch;
-    starts[o] = s;
-    const float2 f = sums[o];
-    s = decayed(decay_of(f.x), s, f.y);
-  }
-  if (s_out) s_out[i] = s;
-}
-
-// The outputs of a tile from the state in front of it.
-template <typename T>
-__global__ __launch_bounds__(kBlock) void rec_apply_kernel(RecArgs a, int64_t tiles,
-                                                           const float* __restrict__ starts,
-                                                           T* __restrict__ h, int64_t hsb,
-                                                           int64_t hst) {
-  using S = TileShapeOf<T>;
-  __shared__ RunSums<T> rs;
-  const TileAt at = tile_at(a, tiles);
-  const LaneAt<T> l = lane_at<T>(a, at);
-  float dec[S::kRun][S::kPer], u[S::kRun][S::kPer], Z[S::kPer], H[S::kPer];
-  load_run<T>(a, l, dec, u, Z, H);
-#pragma unroll
-  for (int c = 0; c < S::kPer; ++c) {
-    rs.z[l.run][l.lane * S::kPer + c] = Z[c];
-    rs.h[l.run][l.lane * S::kPer + c] = H[c];
-  }
-  __syncthreads();
-  const int64_t ch = at.strip * kStrip + threadIdx.x;
-  if (threadIdx.x < kStrip && ch < a.d) {
-    float s = starts[(at.b * tiles + at.j) * a.d + ch];
-    for (int r = 0; r < S::kRuns; ++r) {
-      const float next = decayed(decay_of(rs.z[r][threadIdx.x]), s, rs.h[r][threadIdx.x]);
-      rs.h[r][threadIdx.x] = s;  // the state in front of the run
-      s = next;
-    }
-  }
-  __syncthreads();
-  if (l.rows == 0) return;
+  put_run<T>(rs, l, Z, H);
+  link_tile<T, false>(
+      rs, a, links, at, [&](int64_t c) { return s_in ? s_in[at.b * a.d + c] : 0.0f; },
+      [&](int64_t c, float before, float behind) {
+        if (saved) saved[(at.b * links.tiles + at.j) * a.d + c] = before;
+        if (s_out && at.k + 1 == links.tiles) s_out[at.b * a.d + c] = behind;
+      });
   float s[S::kPer];
 #pragma unroll
   for (int c = 0; c < S::kPer; ++c) s[c] = rs.h[l.run][l.lane * S::kPer + c];
@@ -328,132 +428,112 @@ __global__ __launch_bounds__(kBlock) void rec_apply_kernel(RecArgs a, int64_t ti
   }
 }
 
-// Each tile's sum of z and gradient from behind, from 0, in front of it.
+// The gradients of a tile, from the saved state in front of it; the tile's sums of
+// drate in `part` [B][tiles][d].
 template <typename T>
-__global__ __launch_bounds__(kBlock) void rec_back_sums_kernel(RecArgs a, int64_t tiles,
-                                                               float2* __restrict__ sums) {
+__global__ __launch_bounds__(kBlock) void rec_backward_kernel(RecArgs a, Links links,
+                                                              const float* __restrict__ saved,
+                                                              const float* ds_out, float* ds_in,
+                                                              T* __restrict__ dx,
+                                                              T* __restrict__ dg,
+                                                              T* __restrict__ di,
+                                                              float* __restrict__ part) {
   using S = TileShapeOf<T>;
-  __shared__ RunSums<T> rs;
-  const TileAt at = tile_at(a, tiles);
+  __shared__ Runs<T> rs;
+  __shared__ __attribute__((aligned(16))) float hs[S::kRuns][kStrip];
+  const TileAt at = tile_at(a, links, true);
   const LaneAt<T> l = lane_at<T>(a, at);
-  const T *g = row_of<T>(a.decay, l), *dh = row_of<T>(a.dh, l);
-  float Z[S::kPer], C[S::kPer];
+  uint4 vx[S::kRun], vg[S::kRun], vi[S::kRun], vd[S::kRun];
+  {
+    const T *x = row_of<T>(a.x, l), *g = row_of<T>(a.decay, l), *in = row_of<T>(a.input, l),
+            *dh = row_of<T>(a.dh, l);
 #pragma unroll
-  for (int c = 0; c < S::kPer; ++c) Z[c] = -0.0f, C[c] = 0.0f;
+    for (int t = 0; t < S::kRun; ++t) {
+      vx[t] = vg[t] = vi[t] = vd[t] = make_uint4(0, 0, 0, 0);
+      if (t < l.n) {
+        vg[t] = get16(g + t * a.decay.st);
+        vd[t] = get16(dh + t * a.dh.st);
+        vi[t] = get16(in + t * a.input.st);
+        vx[t] = get16(x + t * a.x.st);
+      }
+    }
+  }
+  // a token's decay, r, i and b i
+  float dec[S::kRun][S::kPer], r[S::kRun][S::kPer], i[S::kRun][S::kPer], bi[S::kRun][S::kPer];
+  float Z[S::kPer], H[S::kPer], C[S::kPer];
 #pragma unroll
-  for (int t = S::kRun - 1; t >= 0; --t) {
-    if (t >= l.n) continue;
-    const uint4 vg = get16(g + t * a.decay.st), vd = get16(dh + t * a.dh.st);
+  for (int c = 0; c < S::kPer; ++c) Z[c] = -0.0f, H[c] = C[c] = 0.0f;
+#pragma unroll
+  for (int t = 0; t < S::kRun; ++t)
 #pragma unroll
     for (int c = 0; c < S::kPer; ++c) {
-      const float z = -l.rate[c] * sigmoid(chunk_value<T>(vg, c));
+      r[t][c] = sigmoid(chunk_value<T>(vg[t], c));
+      i[t][c] = sigmoid(chunk_value<T>(vi[t], c));
+      const float z = t < l.n ? -l.rate[c] * r[t][c] : -0.0f;
+      dec[t][c] = decay_of(z);
+      const float bb = one_minus_square(dec[t][c]);
+      bi[t][c] = bb * inverse_root(bb) * i[t][c];
       Z[c] += z;
-      C[c] = decayed(decay_of(z), C[c] + chunk_value<T>(vd, c), 0.0f);
+      H[c] = decayed(dec[t][c], H[c], bi[t][c] * chunk_value<T>(vx[t], c));
     }
-  }
 #pragma unroll
-  for (int c = 0; c < S::kPer; ++c) {
-    rs.z[l.run][l.lane * S::kPer + c] = Z[c];
-    rs.h[l.run][l.lane * S::kPer + c] = C[c];
-  }
-  __syncthreads();
-  const int64_t ch = at.strip * kStrip + threadIdx.x;
-  if (threadIdx.x >= kStrip || ch >= a.d) return;
-  float z = -0.0f, h = 0.0f;
-  for (int r = S::kRuns - 1; r >= 0; --r) {
-    h = decayed(decay_of(rs.z[r][threadIdx.x]), h, rs.h[r][threadIdx.x]);
-    z += rs.z[r][threadIdx.x];
-  }
-  sums[(at.b * tiles + at.j) * a.d + ch] = make_float2(z, h);
-}
-
-// The gradients of a tile, from the saved state in front of it and the gradient
-// that comes from behind it; the tile's sums of drate in `part` [B][tiles][d].
-template <typename T>
-__global__ __launch_bounds__(kBlock) void rec_back_kernel(RecArgs a, int64_t tiles,
-                                                          const float* __restrict__ saved,
-                                                          const float* __restrict__ behind,
-                                                          T* __restrict__ dx, T* __restrict__ dg,
-                                                          T* __restrict__ di,
-                                                          float* __restrict__ part) {
-  using S = TileShapeOf<T>;
-  __shared__ RunSums<T> rs;
-  __shared__ float back[S::kRuns][kStrip];
-  const TileAt at = tile_at(a, tiles);
-  const LaneAt<T> l = lane_at<T>(a, at);
-  float dec[S::kRun][S::kPer], u[S::kRun][S::kPer], Z[S::kPer], H[S::kPer];
-  load_run<T>(a, l, dec, u, Z, H);
-  const T *x = row_of<T>(a.x, l), *g = row_of<T>(a.decay, l), *in = row_of<T>(a.input, l),
-          *dh = row_of<T>(a.dh, l);
-  float C[S::kPer];
-#pragma unroll
-  for (int c = 0; c < S::kPer; ++c) C[c] = 0.0f;
-#pragma unroll
-  for (int t = S::kRun - 1; t >= 0; --t) {
-    if (t >= l.n) continue;
-    const uint4 vd = get16(dh + t * a.dh.st);
+  for (int t = S::kRun - 1; t >= 0; --t)
 #pragma unroll
     for (int c = 0; c < S::kPer; ++c)
-      C[c] = decayed(dec[t][c], C[c] + chunk_value<T>(vd, c), 0.0f);
-  }
+      C[c] = decayed(dec[t][c], C[c] + chunk_value<T>(vd[t], c), 0.0f);
+  put_run<T>(rs, l, Z, C);
 #pragma unroll
-  for (int c = 0; c < S::kPer; ++c) {
-    const int k = l.lane * S::kPer + c;
-    rs.z[l.run][k] = Z[c], rs.h[l.run][k] = H[c], back[l.run][k] = C[c];
-  }
-  __syncthreads();
+  for (int c = 0; c < S::kPer; ++c) hs[l.run][l.lane * S::kPer + c] = H[c];
+  link_tile<T, true>(
+      rs, a, links, at, [&](int64_t c) { return ds_out ? ds_out[at.b * a.d + c] : 0.0f; },
+      [&](int64_t c, float, float behind) {
+        if (ds_in && at.k + 1 == links.tiles) ds_in[at.b * a.d + c] = behind;
+      });
+  // the states in front of the runs, from the one in front of the tile
   const int64_t ch = at.strip * kStrip + threadIdx.x;
-  const int64_t o = (at.b * tiles + at.j) * a.d + ch;
+  const int64_t o = (at.b * links.tiles + at.j) * a.d + ch;
   if (threadIdx.x < kStrip && ch < a.d) {
-    float s = saved[o], c = behind[o];
-    for (int r = 0; r < S::kRuns; ++r) {
-      const float next = decayed(decay_of(rs.z[r][threadIdx.x]), s, rs.h[r][threadIdx.x]);
-      rs.h[r][threadIdx.x] = s;
+    float s = saved[o];
+#pragma unroll 8
+    for (int k = 0; k < S::kRuns; ++k) {
+      const float next = decayed(rs.dec[k][threadIdx.x], s, hs[k][threadIdx.x]);
+      hs[k][threadIdx.x] = s;
       s = next;
     }
-    for (int r = S::kRuns - 1; r >= 0; --r) {
-      const float next = decayed(decay_of(rs.z[r][threadIdx.x]), c, back[r][threadIdx.x]);
-      back[r][threadIdx.x] = c;
-      c = next;
-    }
   }
   __syncthreads();
-  float s[S::kRun][S::kPer], c[S::kPer], dr[S::kPer];  // s: the state in front of a token
+  const int64_t row = (l.b * a.T + l.t0) * a.d + l.c0;
+  float dr[S::kPer], c[S::kPer], s[S::kRun][S::kPer];  // s: the state in front of a token
 #pragma unroll
   for (int k = 0; k < S::kPer; ++k) {
-    float f = rs.h[l.run][l.lane * S::kPer + k];
-    c[k] = back[l.run][l.lane * S::kPer + k];
+    float f = hs[l.run][l.lane * S::kPer + k];
+    c[k] = rs.h[l.run][l.lane * S::kPer + k];
     dr[k] = 0.0f;
 #pragma unroll
     for (int t = 0; t < S::kRun; ++t) {
       s[t][k] = f;
-      f = decayed(dec[t][k], f, u[t][k]);
+      f = decayed(dec[t][k], f, bi[t][k] * chunk_value<T>(vx[t], k));
     }
   }
-  const int64_t row = (l.b * a.T + l.t0) * a.d + l.c0;
 #pragma unroll
   for (int t = S::kRun - 1; t >= 0; --t) {
-    if (t >= l.rows) continue;
     float fx[S::kPer], fg[S::kPer], fi[S::kPer];
-    if (t < l.n) {
-      const uint4 vx = get16(x + t * a.x.st), vg = get16(g + t * a.decay.st),
-                  vi = get16(in + t * a.input.st), vd = get16(dh + t * a.dh.st);
 #pragma unroll
-      for (int k = 0; k < S::kPer; ++k) {
-        const float r = sigmoid(chunk_value<T>(vg, k)), i = sigmoid(chunk_value<T>(vi, k));
-        const float lam = chunk_value<T>(vd, k) + c[k];
-        const float bb = one_minus_square(dec[t][k]), bi = sqrtf(bb) * i;
-        // y = l (a h - u a^2 / b^2)
-        const float al = decayed(dec[t][k], lam, 0.0f);
-        const float ua = bb > 0.0f ? decayed(dec[t][k], u[t][k], 0.0f) / bb : 0.0f;
-        const float y = al * (s[t][k] - ua);
-        fx[k] = lam * bi;
-        fi[k] = fx[k] * chunk_value<T>(vx, k) * (1.0f - i);
-        fg[k] = -y * l.rate[k] * r * (1.0f - r);
-        dr[k] -= y * r;
-        c[k] = al;
-      }
-    } else {
+    for (int k = 0; k < S::kPer; ++k) {
+      const float xv = chunk_value<T>(vx[t], k), lam = chunk_value<T>(vd[t], k) + c[k];
+      // y = l a (h - i x a / b)
+      const float al = decayed(dec[t][k], lam, 0.0f);
+      const float ix = i[t][k] * xv * inverse_root(one_minus_square(dec[t][k]));
+      const float y = al * (s[t][k] - decayed(dec[t][k], ix, 0.0f));
+      fx[k] = lam * bi[t][k];
+      fi[k] = fx[k] * xv * (1.0f - i[t][k]);
+      const float yr = y * r[t][k];
+      fg[k] = -yr * l.rate[k] * (1.0f - r[t][k]);
+      dr[k] -= t < l.n ? yr : 0.0f;
+      c[k] = al;
+    }
+    if (t >= l.rows) continue;
+    if (t >= l.n) {
 #pragma unroll
       for (int k = 0; k < S::kPer; ++k) fx[k] = fg[k] = fi[k] = 0.0f;
     }
@@ -461,13 +541,13 @@ __global__ __launch_bounds__(kBlock) void rec_back_kernel(RecArgs a, int64_t til
     Lane<T>::put(dg + row + t * a.d, fg);
     Lane<T>::put(di + row + t * a.d, fi);
   }
-  __syncthreads();  // rs.z is read no more
 #pragma unroll
   for (int k = 0; k < S::kPer; ++k) rs.z[l.run][l.lane * S::kPer + k] = dr[k];
   __syncthreads();
   if (threadIdx.x < kStrip && ch < a.d) {
     float f = 0.0f;
-    for (int r = 0; r < S::kRuns; ++r) f += rs.z[r][threadIdx.x];
+#pragma unroll 8
+    for (int k = 0; k < S::kRuns; ++k) f += rs.z[k][threadIdx.x];
     part[o] = f;
   }
 }
@@ -509,12 +589,31 @@ hipError_t with_type(Dtype dt, F&& f) {
 
 }  // namespace
 
-// The tiles' sums, and the states in front of the tiles where they are not saved.
-size_t gatedrec_forward_bytes(const RecArgs& a) {
-  if (a.T <= kRecStepTokens) return 0;
-  const size_t n = (size_t)(a.B * tiles_of(a) * a.d);
-  return align256(n * sizeof(float2)) + n * sizeof(float);
+// The words that link the tiles, and behind them the counter.
+size_t link_bytes(const RecArgs& a) {
+  return tiles_of(a) > 1 ? align256((size_t)(a.B * tiles_of(a) * a.d) * sizeof(uint64_t)) + 256 : 0;
 }
+
+namespace {
+// The workspace's links, cleared.
+hipError_t clear_links(const RecArgs& a, void* ws, Links* links, hipStream_t s) {
+  links->tiles = tiles_of(a);
+  links->words = nullptr, links->begun = nullptr;
+  if (links->tiles == 1) return hipSuccess;
+  const size_t bytes = link_bytes(a) - 256;
+  links->words = static_cast<uint64_t*>(ws);
+  links->begun = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + bytes);
+  const int64_t n = (int64_t)(bytes / 16);
+  rec_clear_kernel<<<dim3((unsigned)std::min<int64_t>((n + kBlock - 1) / kBlock, 2048)), kBlock, 0,
+                     s>>>(static_cast<uint4*>(ws), n, links->begun);
+  return hipGetLastError();
+}
+dim3 tile_grid(const RecArgs& a) {
+  return dim3((unsigned)(a.B * tiles_of(a) * ((a.d + kStrip - 1) / kStrip)));
+}
+}  // namespace
+
+size_t gatedrec_forward_bytes(const RecArgs& a) { return link_bytes(a); }
 
 hipError_t launch_gatedrec_forward(const RecArgs& a, const float* s_in, float* s_out, void* h,
                                    int64_t hsb, int64_t hst, float* saved, void* ws,
@@ -528,23 +627,18 @@ hipError_t launch_gatedrec_forward(const RecArgs& a, const float* s_in, float* s
           a, s_in, s_out, out, hsb, hst, saved);
       return hipGetLastError();
     }
-    const int64_t tiles = tiles_of(a), n = a.B * tiles * a.d;
-    float2* sums = static_cast<float2*>(ws);
-    float* starts = saved ? saved
-                          : reinterpret_cast<float*>(static_cast<char*>(ws) +
-                                                     align256(n * sizeof(float2)));
-    const dim3 grid((unsigned)(a.B * tiles * ((a.d + kStrip - 1) / kStrip)));
-    rec_sums_kernel<T><<<grid, kBlock, 0, s>>>(a, tiles, sums);
-    rec_scan_kernel<<<dim3((unsigned)((a.B * a.d + kBlock - 1) / kBlock)), kBlock, 0, s>>>(
-        sums, s_in, s_out, starts, a.B, tiles, a.d, false);
-    rec_apply_kernel<T><<<grid, kBlock, 0, s>>>(a, tiles, starts, out, hsb, hst);
+    Links links;
+    const hipError_t e = clear_links(a, ws, &links, s);
+    if (e != hipSuccess) return e;
+    rec_forward_kernel<T><<<tile_grid(a), kBlock, 0, s>>>(a, links, s_in, s_out, out, hsb, hst,
+                                                          saved);
     return hipGetLastError();
   });
 }
 
+// The links, and the tiles' sums of drate.
 size_t gatedrec_backward_bytes(const RecArgs& a) {
-  const size_t n = (size_t)(a.B * tiles_of(a) * a.d);
-  return align256(n * sizeof(float2)) + 2 * align256(n * sizeof(float));
+  return link_bytes(a) + (size_t)(a.B * tiles_of(a) * a.d) * sizeof(float);
 }
 
 hipError_t launch_gatedrec_backward(const RecArgs& a, const float* saved, const float* ds_out,
@@ -552,21 +646,15 @@ hipError_t launch_gatedrec_backward(const RecArgs& a, const float* saved, const 
                                     float* ds_in, void* ws, hipStream_t s) {
   return with_type(a.dt, [&](auto t) {
     using T = decltype(t);
-    const int64_t tiles = tiles_of(a), n = a.B * tiles * a.d;
-    char* const base = static_cast<char*>(ws);
-    float2* sums = reinterpret_cast<float2*>(base);
-    float* behind = reinterpret_cast<float*>(base + align256(n * sizeof(float2)));
-    float* part = reinterpret_cast<float*>(base + align256(n * sizeof(float2)) +
-                                           align256(n * sizeof(float)));
-    const dim3 grid((unsigned)(a.B * tiles * ((a.d + kStrip - 1) / kStrip)));
-    rec_back_sums_kernel<T><<<grid, kBlock, 0, s>>>(a, tiles, sums);
-    rec_scan_kernel<<<dim3((unsigned)((a.B * a.d + kBlock - 1) / kBlock)), kBlock, 0, s>>>(
-        sums, ds_out, ds_in, behind, a.B, tiles, a.d, true);
-    rec_back_kernel<T><<<grid, kBlock, 0, s>>>(a, tiles, saved, behind, static_cast<T*>(dx),
-                                               static_cast<T*>(ddecay), static_cast<T*>(dinput),
-                                               part);
-    rec_rate_kernel<<<dim3((unsigned)((a.d + 63) / 64)), kBlock, 0, s>>>(part, drate, a.B * tiles,
-                                                                         a.d);
+    Links links;
+    const hipError_t e = clear_links(a, ws, &links, s);
+    if (e != hipSuccess) return e;
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + link_bytes(a));
+    rec_backward_kernel<T><<<tile_grid(a), kBlock, 0, s>>>(
+        a, links, saved, ds_out, ds_in, static_cast<T*>(dx), static_cast<T*>(ddecay),
+        static_cast<T*>(dinput), part);
+    rec_rate_kernel<<<dim3((unsigned)((a.d + 63) / 64)), kBlock, 0, s>>>(part, drate,
+                                                                         a.B * links.tiles, a.d);
     return hipGetLastError();
   });
 }
