@@ -30,42 +30,60 @@ namespace ttt {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int kForward = 256;   // threads of a tile
+constexpr int kBackward = 256;
 constexpr int kStrip = 64;  // channels of a tile
 
-// A decay as one float: e^z itself (sign bit clear) or, where z > -1/4, e^z - 1
-// (sign bit set, -0 for z = 0).  The second keeps what a decay near 1 loses by its
-// rounding, which would be repeated for as long as the channel remembers.
-// e^z - 1 = z (1 + z/2 (1 + z/3 (...))) to the sixth power: what is left out is
-// below z^6 / 5040 = 5e-8 of it.
+// Exponents are base 2 throughout: z is log2 a = -rate log2(e) r.
+//
+// A decay over a run of tokens as one float: 2^z itself (sign bit clear) or, where
+// z > -1/2, 2^z - 1 (sign bit set, -0 for z = 0).  The second keeps what a decay near 1
+// loses by its rounding, which would be repeated for as long as the channel remembers.
+// The polynomial is 2^z - 1 to 3.3e-8 of it (Chebyshev nodes in [-1/2, 0]).
 __device__ __forceinline__ float decay_of(float z) {
-  float p = 1.0f + z * (1.0f / 6.0f);
-  p = 1.0f + z * (1.0f / 5.0f) * p;
-  p = 1.0f + z * (1.0f / 4.0f) * p;
-  p = 1.0f + z * (1.0f / 3.0f) * p;
-  p = 1.0f + z * (1.0f / 2.0f) * p;
-  return z > -0.25f ? __builtin_copysignf(z * p, -1.0f) : __expf(z);
+  float p = __builtin_fmaf(z, 0x1.2ee444p-10f, 0x1.38ae68p-7f);
+  p = __builtin_fmaf(z, p, 0x1.c6947ap-5f);
+  p = __builtin_fmaf(z, p, 0x1.ebfb70p-3f);
+  p = __builtin_fmaf(z, p, 0x1.62e430p-1f);
+  const float near = z * p, far = __builtin_amdgcn_exp2f(z);
+  return z > -0.5f ? near : far;  // a z of -0 gives -0
 }
 __device__ __forceinline__ bool near_one(float dec) { return __float_as_uint(dec) >> 31; }
 // a h + u
 __device__ __forceinline__ float decayed(float dec, float h, float u) {
   return __builtin_fmaf(dec, h, u) + (near_one(dec) ? h : 0.0f);
 }
-// 1 - a^2 = (1 - a)(1 + a), and 1 / b (0 where b is); b is their product.  The root's
-// instruction takes values below 2^-126 as 0: it is given 2^64 times its argument.
-__device__ __forceinline__ float one_minus_square(float dec) {
-  return near_one(dec) ? -dec * (2.0f + dec) : (1.0f - dec) * (1.0f + dec);
+
+// 2^64 (1 - a^2) from a and its z: near a = 1 by the same polynomial of 2 z.  The roots'
+// instructions take values below 2^-126 as 0, which 2^64 times the smallest is not: b
+// comes as 2^32 b, its inverse as 2^-32 / b.
+__device__ __forceinline__ float root_arg(float z, float a) {
+  float p = __builtin_fmaf(z, -0x1.2ee444p+59f, -0x1.38ae68p+61f);
+  p = __builtin_fmaf(z, p, -0x1.c6947ap+62f);
+  p = __builtin_fmaf(z, p, -0x1.ebfb70p+63f);
+  p = __builtin_fmaf(z, p, -0x1.62e430p+64f);
+  const float near = z * p, far = __builtin_fmaf(-a, a, 1.0f) * 0x1p64f;
+  return z > -0.25f ? near : far;
 }
-__device__ __forceinline__ float inverse_root(float bb) {
-  const float inv = __builtin_amdgcn_rsqf(bb * 0x1p64f) * 0x1p32f;
-  return bb == 0.0f ? 0.0f : inv;
-}
-// z is never positive: a rate below 0 counts as NaN.
-__device__ __forceinline__ float rate_at(const float* rate, int64_t c) {
+
+constexpr float kLog2e = 0x1.715476p+0f;
+// -log2(e) rate; z is never positive: a rate below 0 counts as NaN.  2^100 is as good as
+// any above it, and 0 times it is 0.
+__device__ __forceinline__ float log_rate(const float* rate, int64_t c) {
   const float r = rate[c];
-  return r >= 0.0f ? r : __builtin_nanf("");
+  return r >= 0.0f ? -kLog2e * fminf(r, 0x1p100f) : __builtin_nanf("");
 }
 __device__ __forceinline__ float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + __expf(-x));
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
+}
+// 2^-32 of it, beside 2^32 b
+__device__ __forceinline__ float sigmoid_scaled(float x) {
+  return __builtin_amdgcn_rcpf(
+      __builtin_fmaf(__builtin_amdgcn_exp2f(-kLog2e * x), 0x1p32f, 0x1p32f));
+}
+// b i from z, a and the input gate
+__device__ __forceinline__ float gated(float z, float a, float gate) {
+  return __builtin_amdgcn_sqrtf(root_arg(z, a)) * sigmoid_scaled(gate);
 }
 
 // kPer values of a lane: 16 bytes.
@@ -74,6 +92,7 @@ struct Lane;
 template <>
 struct Lane<uint16_t> {
   static constexpr int kPer = 8;
+  __device__ __forceinline__ static uint32_t word(const float f[2]) { return pack_bf16x2(f[0], f[1]); }
   __device__ __forceinline__ static void put(uint16_t* p, const float f[8]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                               pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
@@ -82,40 +101,37 @@ struct Lane<uint16_t> {
 template <>
 struct Lane<float> {
   static constexpr int kPer = 4;
+  __device__ __forceinline__ static uint32_t word(const float f[1]) { return __float_as_uint(f[0]); }
   __device__ __forceinline__ static void put(float* p, const float f[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   }
 };
+// A decay gate of -infinity in every channel: a token that neither decays nor enters.
+template <typename T>
+__device__ __forceinline__ uint4 no_token() {
+  constexpr uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  return make_uint4(w, w, w, w);
+}
 template <typename T>
 __device__ __forceinline__ uint4 get16(const T* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// Lane layout of a tile: kLanes lanes across the strip's channels, kRuns runs of
-// kRun tokens.
-template <typename T>
-struct TileShapeOf {
+// Lane layout of a tile on kThreads: kLanes lanes across the strip's channels, kRuns
+// runs of kRun tokens.
+template <typename T_, int kThreads_>
+struct TileLayout {
+  using T = T_;
+  static constexpr int kThreads = kThreads_;
   static constexpr int kPer = Lane<T>::kPer;
   static constexpr int kLanes = kStrip / kPer;
-  static constexpr int kRuns = kBlock / kLanes;
+  static constexpr int kRuns = kThreads / kLanes;
   static constexpr int kRun = kRecTile / kRuns;
+  static constexpr int kParts = kThreads / 64;  // waves, each folds kRuns / kParts runs
 };
 
 __device__ __forceinline__ int64_t tokens_of(const RecArgs& a, int64_t b) {
   if (!a.lengths) return a.T;
   const int64_t n = a.lengths[b];
   return n < 0 ? 0 : n > a.T ? a.T : n;
-}
-
-// z as its decay and u of one token's channels.
-template <typename T>
-__device__ __forceinline__ void token(const uint4& vx, const uint4& vg, const uint4& vi,
-                                      const float* rate, float* z, float* dec, float* u) {
-#pragma unroll
-  for (int c = 0; c < Lane<T>::kPer; ++c) {
-    z[c] = -rate[c] * sigmoid(chunk_value<T>(vg, c));
-    dec[c] = decay_of(z[c]);
-    const float bb = one_minus_square(dec[c]);
-    u[c] = bb * inverse_root(bb) * sigmoid(chunk_value<T>(vi, c)) * chunk_value<T>(vx, c);
-  }
 }
 
 // The recurrent form: a lane walks the tokens of its channels.
@@ -133,7 +149,7 @@ __global__ __launch_bounds__(kBlock) void rec_step_kernel(RecArgs a, const float
   float s[kPer], rate[kPer];
 #pragma unroll
   for (int c = 0; c < kPer; ++c) {
-    rate[c] = rate_at(a.rate, c0 + c);
+    rate[c] = log_rate(a.rate, c0 + c);
     s[c] = s_in ? s_in[b * a.d + c0 + c] : 0.0f;
   }
   if (saved) {
@@ -147,11 +163,14 @@ __global__ __launch_bounds__(kBlock) void rec_step_kernel(RecArgs a, const float
   for (int64_t t = 0; t < a.T; ++t) {
     float f[kPer];
     if (t < n) {
-      float z[kPer], dec[kPer], u[kPer];
-      token<T>(get16(x + t * a.x.st), get16(g + t * a.decay.st), get16(in + t * a.input.st), rate,
-               z, dec, u);
+      const uint4 vx = get16(x + t * a.x.st), vg = get16(g + t * a.decay.st),
+                  vi = get16(in + t * a.input.st);
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) f[c] = s[c] = decayed(dec[c], s[c], u[c]);
+      for (int c = 0; c < kPer; ++c) {
+        const float z = rate[c] * sigmoid(chunk_value<T>(vg, c));
+        const float u = gated(z, __builtin_amdgcn_exp2f(z), chunk_value<T>(vi, c));
+        f[c] = s[c] = decayed(decay_of(z), s[c], u * chunk_value<T>(vx, c));
+      }
     } else {
 #pragma unroll
       for (int c = 0; c < kPer; ++c) f[c] = 0.0f;
@@ -250,18 +269,17 @@ __device__ __forceinline__ float state_before(const uint64_t* word, int64_t step
 }
 
 // What a lane of a tile works on.
-template <typename T>
+template <class S>
 struct LaneAt {
   int64_t b, j, c0, t0;  // t0: its run's first token
   int lane, run;
   int n;                 // tokens of its run that count
   int rows;              // tokens of its run inside T
-  float rate[Lane<T>::kPer];
+  float rate[S::kPer];  // as log_rate gives it
 };
-template <typename T>
-__device__ __forceinline__ LaneAt<T> lane_at(const RecArgs& a, const TileAt& at) {
-  using S = TileShapeOf<T>;
-  LaneAt<T> l;
+template <class S>
+__device__ __forceinline__ LaneAt<S> lane_at(const RecArgs& a, const TileAt& at) {
+  LaneAt<S> l;
   l.lane = threadIdx.x % S::kLanes, l.run = threadIdx.x / S::kLanes;
   l.b = at.b, l.j = at.j;
   l.c0 = at.strip * kStrip + l.lane * S::kPer;
@@ -271,31 +289,30 @@ __device__ __forceinline__ LaneAt<T> lane_at(const RecArgs& a, const TileAt& at)
   l.n = live ? (int)min<int64_t>(max<int64_t>(n - l.t0, 0), S::kRun) : 0;
   l.rows = live ? (int)min<int64_t>(max<int64_t>(a.T - l.t0, 0), S::kRun) : 0;
 #pragma unroll
-  for (int c = 0; c < S::kPer; ++c) l.rate[c] = live ? rate_at(a.rate, l.c0 + c) : 0.0f;
+  for (int c = 0; c < S::kPer; ++c) l.rate[c] = live ? log_rate(a.rate, l.c0 + c) : -0.0f;
   return l;
 }
-template <typename T>
-__device__ __forceinline__ const T* row_of(const RecOperand& o, const LaneAt<T>& l) {
-  return static_cast<const T*>(o.p) + l.b * o.sb + l.t0 * o.st + l.c0;
+template <class S>
+__device__ __forceinline__ const typename S::T* row_of(const RecOperand& o, const LaneAt<S>& l) {
+  return static_cast<const typename S::T*>(o.p) + l.b * o.sb + l.t0 * o.st + l.c0;
 }
 
 // The runs of a tile in LDS, by run and channel: decays over a run and states behind
-// it from 0, sums of z.  A wave folds kRuns / kParts of them for 64 channels.
-constexpr int kParts = kBlock / 64;
-template <typename T>
+// it from 0, sums of z.  A wave folds kEach of them for 64 channels.
+template <class S>
 struct alignas(16) Runs {
-  static constexpr int kRuns = TileShapeOf<T>::kRuns, kEach = kRuns / kParts;
-  float z[kRuns][kStrip], dec[kRuns][kStrip], h[kRuns][kStrip];
-  float part_z[kParts][kStrip], part_h[kParts][kStrip];
+  static constexpr int kEach = S::kRuns / S::kParts;
+  float z[S::kRuns][kStrip], dec[S::kRuns][kStrip], h[S::kRuns][kStrip];
+  float part_z[S::kParts][kStrip], part_h[S::kParts][kStrip];
 };
 
 // A lane's run into LDS.
-template <typename T>
-__device__ __forceinline__ void put_run(Runs<T>& rs, const LaneAt<T>& l, const float* Z,
+template <class S>
+__device__ __forceinline__ void put_run(Runs<S>& rs, const LaneAt<S>& l, const float* Z,
                                         const float* H) {
 #pragma unroll
-  for (int c = 0; c < Lane<T>::kPer; ++c) {
-    const int k = l.lane * Lane<T>::kPer + c;
+  for (int c = 0; c < S::kPer; ++c) {
+    const int k = l.lane * S::kPer + c;
     rs.z[l.run][k] = Z[c], rs.dec[l.run][k] = decay_of(Z[c]), rs.h[l.run][k] = H[c];
   }
 }
@@ -304,18 +321,19 @@ __device__ __forceinline__ void put_run(Runs<T>& rs, const LaneAt<T>& l, const f
 // h: the waves fold their runs, the first wave folds the waves' and links the tile with
 // the ones before it, the waves go through their runs once more.  first: the state of
 // the channel in front of the first tile; done(channel, state in front of the tile,
-// state behind it) in the first wave.
-template <typename T, bool kReverse, class First, class Done>
-__device__ __forceinline__ void link_tile(Runs<T>& rs, const RecArgs& a, const Links& links,
-                                          const TileAt& at, First&& first, Done&& done) {
-  using R = Runs<T>;
+// state behind it) in the first wave; beside(channel) in the second one meanwhile.
+template <bool kReverse, class S, class First, class Done, class Beside>
+__device__ __forceinline__ void link_tile(Runs<S>& rs, const RecArgs& a, const Links& links,
+                                          const TileAt& at, First&& first, Done&& done,
+                                          Beside&& beside) {
+  constexpr int kParts = S::kParts, kEach = Runs<S>::kEach;
   const int ch = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const auto run = [&](int i) { return kReverse ? R::kRuns - 1 - i : i; };
+  const auto run = [&](int i) { return kReverse ? S::kRuns - 1 - i : i; };
   __syncthreads();
   float z = -0.0f, h = 0.0f;
 #pragma unroll
-  for (int i = 0; i < R::kEach; ++i) {
-    const int r = run(wave * R::kEach + i);
+  for (int i = 0; i < kEach; ++i) {
+    const int r = run(wave * kEach + i);
     h = decayed(rs.dec[r][ch], h, rs.h[r][ch]);
     z += rs.z[r][ch];
   }
@@ -354,11 +372,12 @@ __device__ __forceinline__ void link_tile(Runs<T>& rs, const RecArgs& a, const L
     }
     done(c, before, decayed(whole, before, ph));
   }
+  if (wave == 1 && c < a.d) beside(c);
   __syncthreads();
   float s = rs.part_h[wave][ch];
 #pragma unroll
-  for (int i = 0; i < R::kEach; ++i) {
-    const int r = run(wave * R::kEach + i);
+  for (int i = 0; i < kEach; ++i) {
+    const int r = run(wave * kEach + i);
     const float next = decayed(rs.dec[r][ch], s, rs.h[r][ch]);
     rs.h[r][ch] = s;
     s = next;
@@ -368,49 +387,47 @@ __device__ __forceinline__ void link_tile(Runs<T>& rs, const RecArgs& a, const L
 
 // A tile's outputs.
 template <typename T>
-__global__ __launch_bounds__(kBlock) void rec_forward_kernel(RecArgs a, Links links,
-                                                             const float* s_in, float* s_out,
-                                                             T* __restrict__ h, int64_t hsb,
-                                                             int64_t hst,
-                                                             float* __restrict__ saved) {
-  using S = TileShapeOf<T>;
-  __shared__ Runs<T> rs;
+__global__ __launch_bounds__(kForward) __attribute__((amdgpu_waves_per_eu(4))) void
+rec_forward_kernel(RecArgs a, Links links, const float* s_in, float* s_out, T* __restrict__ h,
+                   int64_t hsb, int64_t hst, float* __restrict__ saved) {
+  using S = TileLayout<T, kForward>;
+  __shared__ Runs<S> rs;
   const TileAt at = tile_at(a, links, false);
-  const LaneAt<T> l = lane_at<T>(a, at);
+  const LaneAt<S> l = lane_at<S>(a, at);
   uint4 vx[S::kRun], vg[S::kRun], vi[S::kRun];
-  const T *x = row_of<T>(a.x, l), *g = row_of<T>(a.decay, l), *in = row_of<T>(a.input, l);
+  const T *x = row_of(a.x, l), *g = row_of(a.decay, l), *in = row_of(a.input, l);
 #pragma unroll
-  for (int t = 0; t < S::kRun; ++t)
+  for (int t = 0; t < S::kRun; ++t) {
+    vg[t] = no_token<T>();
+    vx[t] = vi[t] = make_uint4(0, 0, 0, 0);
     if (t < l.n) {
       vg[t] = get16(g + t * a.decay.st);
       vi[t] = get16(in + t * a.input.st);
       vx[t] = get16(x + t * a.x.st);
     }
+  }
+  // Inside a run of a few tokens a itself will do; from run to run the sum of z counts.
   float dec[S::kRun][S::kPer], u[S::kRun][S::kPer], Z[S::kPer], H[S::kPer];
 #pragma unroll
   for (int c = 0; c < S::kPer; ++c) Z[c] = -0.0f, H[c] = 0.0f;
 #pragma unroll
-  for (int t = 0; t < S::kRun; ++t) {
-    float z[S::kPer];
-    if (t < l.n) {
-      token<T>(vx[t], vg[t], vi[t], l.rate, z, dec[t], u[t]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < S::kPer; ++c) z[c] = -0.0f, dec[t][c] = -0.0f, u[t][c] = 0.0f;
-    }
+  for (int t = 0; t < S::kRun; ++t)
 #pragma unroll
     for (int c = 0; c < S::kPer; ++c) {
-      Z[c] += z[c];
-      H[c] = decayed(dec[t][c], H[c], u[t][c]);
+      const float z = l.rate[c] * sigmoid(chunk_value<T>(vg[t], c));
+      dec[t][c] = __builtin_amdgcn_exp2f(z);
+      u[t][c] = gated(z, dec[t][c], chunk_value<T>(vi[t], c)) * chunk_value<T>(vx[t], c);
+      Z[c] += z;
+      H[c] = __builtin_fmaf(dec[t][c], H[c], u[t][c]);
     }
-  }
-  put_run<T>(rs, l, Z, H);
-  link_tile<T, false>(
+  put_run(rs, l, Z, H);
+  link_tile<false>(
       rs, a, links, at, [&](int64_t c) { return s_in ? s_in[at.b * a.d + c] : 0.0f; },
       [&](int64_t c, float before, float behind) {
         if (saved) saved[(at.b * links.tiles + at.j) * a.d + c] = before;
         if (s_out && at.k + 1 == links.tiles) s_out[at.b * a.d + c] = behind;
-      });
+      },
+      [](int64_t) {});
   float s[S::kPer];
 #pragma unroll
   for (int c = 0; c < S::kPer; ++c) s[c] = rs.h[l.run][l.lane * S::kPer + c];
@@ -421,7 +438,7 @@ __global__ __launch_bounds__(kBlock) void rec_forward_kernel(RecArgs a, Links li
     float f[S::kPer];
 #pragma unroll
     for (int c = 0; c < S::kPer; ++c) {
-      s[c] = decayed(dec[t][c], s[c], u[t][c]);
+      s[c] = __builtin_fmaf(dec[t][c], s[c], u[t][c]);
       f[c] = t < l.n ? s[c] : 0.0f;
     }
     Lane<T>::put(out + t * hst, f);
@@ -429,126 +446,149 @@ __global__ __launch_bounds__(kBlock) void rec_forward_kernel(RecArgs a, Links li
 }
 
 // The gradients of a tile, from the saved state in front of it; the tile's sums of
-// drate in `part` [B][tiles][d].
+// drate in `part` [B][tiles][d].  A lane holds its tokens' x and dh as loaded, and their
+// r and b i; it goes through its channels one after the other at the end, so that
+// the states and results of few are in registers beside them.
 template <typename T>
-__global__ __launch_bounds__(kBlock) void rec_backward_kernel(RecArgs a, Links links,
-                                                              const float* __restrict__ saved,
-                                                              const float* ds_out, float* ds_in,
-                                                              T* __restrict__ dx,
-                                                              T* __restrict__ dg,
-                                                              T* __restrict__ di,
-                                                              float* __restrict__ part) {
-  using S = TileShapeOf<T>;
-  __shared__ Runs<T> rs;
+__global__ __launch_bounds__(kBackward) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 3 : 2))) void
+rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, const float* ds_out,
+                    float* ds_in, T* __restrict__ dx, T* __restrict__ dg, T* __restrict__ di,
+                    float* __restrict__ part) {
+  using S = TileLayout<T, kBackward>;
+  __shared__ Runs<S> rs;
   __shared__ __attribute__((aligned(16))) float hs[S::kRuns][kStrip];
   const TileAt at = tile_at(a, links, true);
-  const LaneAt<T> l = lane_at<T>(a, at);
-  uint4 vx[S::kRun], vg[S::kRun], vi[S::kRun], vd[S::kRun];
+  const LaneAt<S> l = lane_at<S>(a, at);
+  uint4 vx[S::kRun], vd[S::kRun];
+  float r[S::kRun][S::kPer], bi[S::kRun][S::kPer];
   {
-    const T *x = row_of<T>(a.x, l), *g = row_of<T>(a.decay, l), *in = row_of<T>(a.input, l),
-            *dh = row_of<T>(a.dh, l);
+    uint4 vg[S::kRun], vi[S::kRun];
+    const T *x = row_of(a.x, l), *g = row_of(a.decay, l), *in = row_of(a.input, l),
+            *dh = row_of(a.dh, l);
 #pragma unroll
     for (int t = 0; t < S::kRun; ++t) {
-      vx[t] = vg[t] = vi[t] = vd[t] = make_uint4(0, 0, 0, 0);
+      vg[t] = no_token<T>();
+      vx[t] = vi[t] = vd[t] = make_uint4(0, 0, 0, 0);
       if (t < l.n) {
         vg[t] = get16(g + t * a.decay.st);
-        vd[t] = get16(dh + t * a.dh.st);
         vi[t] = get16(in + t * a.input.st);
         vx[t] = get16(x + t * a.x.st);
+        vd[t] = get16(dh + t * a.dh.st);
       }
     }
-  }
-  // a token's decay, r, i and b i
-  float dec[S::kRun][S::kPer], r[S::kRun][S::kPer], i[S::kRun][S::kPer], bi[S::kRun][S::kPer];
-  float Z[S::kPer], H[S::kPer], C[S::kPer];
+    // C: what comes from behind the run, from 0: the sum of its dh, each through the decays
+    // up to its token (A)
+    float Z[S::kPer], H[S::kPer], C[S::kPer], A[S::kPer];
 #pragma unroll
-  for (int c = 0; c < S::kPer; ++c) Z[c] = -0.0f, H[c] = C[c] = 0.0f;
+    for (int c = 0; c < S::kPer; ++c) Z[c] = -0.0f, H[c] = C[c] = 0.0f, A[c] = 1.0f;
 #pragma unroll
-  for (int t = 0; t < S::kRun; ++t)
+    for (int t = 0; t < S::kRun; ++t) {
+      __builtin_amdgcn_sched_barrier(0);  // registers: one token at a time
 #pragma unroll
-    for (int c = 0; c < S::kPer; ++c) {
-      r[t][c] = sigmoid(chunk_value<T>(vg[t], c));
-      i[t][c] = sigmoid(chunk_value<T>(vi[t], c));
-      const float z = t < l.n ? -l.rate[c] * r[t][c] : -0.0f;
-      dec[t][c] = decay_of(z);
-      const float bb = one_minus_square(dec[t][c]);
-      bi[t][c] = bb * inverse_root(bb) * i[t][c];
-      Z[c] += z;
-      H[c] = decayed(dec[t][c], H[c], bi[t][c] * chunk_value<T>(vx[t], c));
+      for (int c = 0; c < S::kPer; ++c) {
+        r[t][c] = sigmoid(chunk_value<T>(vg[t], c));
+        const float z = l.rate[c] * r[t][c], dec = __builtin_amdgcn_exp2f(z);
+        bi[t][c] = gated(z, dec, chunk_value<T>(vi[t], c));
+        Z[c] += z;
+        H[c] = __builtin_fmaf(dec, H[c], bi[t][c] * chunk_value<T>(vx[t], c));
+        A[c] *= dec;
+        C[c] = __builtin_fmaf(A[c], chunk_value<T>(vd[t], c), C[c]);
+      }
     }
+    put_run(rs, l, Z, C);
 #pragma unroll
-  for (int t = S::kRun - 1; t >= 0; --t)
-#pragma unroll
-    for (int c = 0; c < S::kPer; ++c)
-      C[c] = decayed(dec[t][c], C[c] + chunk_value<T>(vd[t], c), 0.0f);
-  put_run<T>(rs, l, Z, C);
-#pragma unroll
-  for (int c = 0; c < S::kPer; ++c) hs[l.run][l.lane * S::kPer + c] = H[c];
-  link_tile<T, true>(
+    for (int c = 0; c < S::kPer; ++c) hs[l.run][l.lane * S::kPer + c] = H[c];
+  }
+  const auto tile_row = [&](int64_t c) { return (at.b * links.tiles + at.j) * a.d + c; };
+  link_tile<true>(
       rs, a, links, at, [&](int64_t c) { return ds_out ? ds_out[at.b * a.d + c] : 0.0f; },
       [&](int64_t c, float, float behind) {
         if (ds_in && at.k + 1 == links.tiles) ds_in[at.b * a.d + c] = behind;
-      });
-  // the states in front of the runs, from the one in front of the tile
-  const int64_t ch = at.strip * kStrip + threadIdx.x;
-  const int64_t o = (at.b * links.tiles + at.j) * a.d + ch;
-  if (threadIdx.x < kStrip && ch < a.d) {
-    float s = saved[o];
+      },
+      // the states in front of the runs, from the one in front of the tile
+      [&](int64_t c) {
+        const int ch = threadIdx.x & 63;
+        float s = saved[tile_row(c)];
 #pragma unroll 8
-    for (int k = 0; k < S::kRuns; ++k) {
-      const float next = decayed(rs.dec[k][threadIdx.x], s, hs[k][threadIdx.x]);
-      hs[k][threadIdx.x] = s;
-      s = next;
-    }
-  }
-  __syncthreads();
-  const int64_t row = (l.b * a.T + l.t0) * a.d + l.c0;
-  float dr[S::kPer], c[S::kPer], s[S::kRun][S::kPer];  // s: the state in front of a token
+        for (int k = 0; k < S::kRuns; ++k) {
+          const float next = decayed(rs.dec[k][ch], s, hs[k][ch]);
+          hs[k][ch] = s;
+          s = next;
+        }
+      });
+  // what is worked out again below must not be kept in registers from above
 #pragma unroll
-  for (int k = 0; k < S::kPer; ++k) {
-    float f = hs[l.run][l.lane * S::kPer + k];
-    c[k] = rs.h[l.run][l.lane * S::kPer + k];
-    dr[k] = 0.0f;
+  for (int t = 0; t < S::kRun; ++t) {
+    asm("" : "+v"(vx[t].x), "+v"(vx[t].y), "+v"(vx[t].z), "+v"(vx[t].w));
+    asm("" : "+v"(vd[t].x), "+v"(vd[t].y), "+v"(vd[t].z), "+v"(vd[t].w));
+#pragma unroll
+    for (int c = 0; c < S::kPer; ++c) asm("" : "+v"(r[t][c]));
+  }
+  uint32_t ox[S::kRun][4], og[S::kRun][4], oi[S::kRun][4];  // results as stored
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    __builtin_amdgcn_sched_barrier(0);  // and one word of channels
+    constexpr int kIn = S::kPer / 4;  // channels of a 32-bit word
+    float fx[S::kRun][kIn], fg[S::kRun][kIn], fi[S::kRun][kIn];
+#pragma unroll
+    for (int q = 0; q < kIn; ++q) {
+      const int k = w * kIn + q, at_k = l.lane * S::kPer + k;
+      // decays, and the states in front of the tokens
+      float dec[S::kRun], s[S::kRun], f = hs[l.run][at_k];
+#pragma unroll
+      for (int t = 0; t < S::kRun; ++t) {
+        s[t] = f;
+        dec[t] = __builtin_amdgcn_exp2f(l.rate[k] * r[t][k]);
+        f = __builtin_fmaf(dec[t], f, bi[t][k] * chunk_value<T>(vx[t], k));
+      }
+      float c = rs.h[l.run][at_k], dr = 0.0f;
+#pragma unroll
+      for (int t = S::kRun - 1; t >= 0; --t) {
+        const float x = chunk_value<T>(vx[t], k), lam = chunk_value<T>(vd[t], k) + c;
+        // y = l a (h - i x a / b), with i = (b i) / b; where b is 0 so is what they stand
+        // beside (2^62: above all others, and finite)
+        const float al = dec[t] * lam;
+        const float inv = fminf(__builtin_amdgcn_rsqf(root_arg(l.rate[k] * r[t][k], dec[t])),
+                                0x1p62f) * 0x1p32f;
+        const float i = bi[t][k] * inv;
+        const float y = al * __builtin_fmaf(-dec[t], i * x * inv, s[t]);
+        const float yr = t < l.n ? y * r[t][k] : 0.0f;
+        fx[t][q] = lam * bi[t][k];
+        fi[t][q] = fx[t][q] * x * (1.0f - i);
+        fg[t][q] = yr * (l.rate[k] * (1.0f / kLog2e)) * (1.0f - r[t][k]);
+        if (t >= l.n) fx[t][q] = fi[t][q] = fg[t][q] = 0.0f;
+        dr -= yr;
+        c = al;
+      }
+      rs.z[l.run][at_k] = dr;  // read last in front of link_tile's second barrier
+    }
 #pragma unroll
     for (int t = 0; t < S::kRun; ++t) {
-      s[t][k] = f;
-      f = decayed(dec[t][k], f, bi[t][k] * chunk_value<T>(vx[t], k));
+      ox[t][w] = Lane<T>::word(fx[t]);
+      og[t][w] = Lane<T>::word(fg[t]);
+      oi[t][w] = Lane<T>::word(fi[t]);
+      // here, not in front of the stores, up to where all they come from would be kept
+      asm volatile("" : "+v"(ox[t][w]), "+v"(og[t][w]), "+v"(oi[t][w]));
     }
   }
+  const int64_t row = (l.b * a.T + l.t0) * a.d + l.c0;
+  const auto put = [&](T* p, const uint32_t* o) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+  };
 #pragma unroll
-  for (int t = S::kRun - 1; t >= 0; --t) {
-    float fx[S::kPer], fg[S::kPer], fi[S::kPer];
-#pragma unroll
-    for (int k = 0; k < S::kPer; ++k) {
-      const float xv = chunk_value<T>(vx[t], k), lam = chunk_value<T>(vd[t], k) + c[k];
-      // y = l a (h - i x a / b)
-      const float al = decayed(dec[t][k], lam, 0.0f);
-      const float ix = i[t][k] * xv * inverse_root(one_minus_square(dec[t][k]));
-      const float y = al * (s[t][k] - decayed(dec[t][k], ix, 0.0f));
-      fx[k] = lam * bi[t][k];
-      fi[k] = fx[k] * xv * (1.0f - i[t][k]);
-      const float yr = y * r[t][k];
-      fg[k] = -yr * l.rate[k] * (1.0f - r[t][k]);
-      dr[k] -= t < l.n ? yr : 0.0f;
-      c[k] = al;
-    }
-    if (t >= l.rows) continue;
-    if (t >= l.n) {
-#pragma unroll
-      for (int k = 0; k < S::kPer; ++k) fx[k] = fg[k] = fi[k] = 0.0f;
-    }
-    Lane<T>::put(dx + row + t * a.d, fx);
-    Lane<T>::put(dg + row + t * a.d, fg);
-    Lane<T>::put(di + row + t * a.d, fi);
+  for (int t = 0; t < S::kRun; ++t) {
+    if (t >= l.rows) break;
+    put(dx + row + t * a.d, ox[t]);
+    put(dg + row + t * a.d, og[t]);
+    put(di + row + t * a.d, oi[t]);
   }
-#pragma unroll
-  for (int k = 0; k < S::kPer; ++k) rs.z[l.run][l.lane * S::kPer + k] = dr[k];
   __syncthreads();
+  const int64_t ch = at.strip * kStrip + threadIdx.x;
   if (threadIdx.x < kStrip && ch < a.d) {
     float f = 0.0f;
 #pragma unroll 8
     for (int k = 0; k < S::kRuns; ++k) f += rs.z[k][threadIdx.x];
-    part[o] = f;
+    part[tile_row(ch)] = f;
   }
 }
 
@@ -630,7 +670,7 @@ hipError_t launch_gatedrec_forward(const RecArgs& a, const float* s_in, float* s
     Links links;
     const hipError_t e = clear_links(a, ws, &links, s);
     if (e != hipSuccess) return e;
-    rec_forward_kernel<T><<<tile_grid(a), kBlock, 0, s>>>(a, links, s_in, s_out, out, hsb, hst,
+    rec_forward_kernel<T><<<tile_grid(a), kForward, 0, s>>>(a, links, s_in, s_out, out, hsb, hst,
                                                           saved);
     return hipGetLastError();
   });
@@ -650,7 +690,7 @@ hipError_t launch_gatedrec_backward(const RecArgs& a, const float* saved, const 
     const hipError_t e = clear_links(a, ws, &links, s);
     if (e != hipSuccess) return e;
     float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + link_bytes(a));
-    rec_backward_kernel<T><<<tile_grid(a), kBlock, 0, s>>>(
+    rec_backward_kernel<T><<<tile_grid(a), kBackward, 0, s>>>(
         a, links, saved, ds_out, ds_in, static_cast<T*>(dx), static_cast<T*>(ddecay),
         static_cast<T*>(dinput), part);
     rec_rate_kernel<<<dim3((unsigned)((a.d + 63) / 64)), kBlock, 0, s>>>(part, drate,
