@@ -98,57 +98,110 @@ __global__ __launch_bounds__(kBlock) void act8_load_kernel(const int8_t* __restr
   }
 }
 
-// An fp32 dy as three bf16 terms whose sum it is: the leading 8 bits of what is left,
-// three times.  parts [3][rows][n]; an infinity or NaN goes into the first alone.
-__global__ __launch_bounds__(kBlock) void act8_split_kernel(const float* __restrict__ dy,
-                                                            int64_t dys, uint16_t* __restrict__ parts,
-                                                            int64_t rows, int64_t n) {
-  const int64_t pieces = n >> 3, total = rows * pieces;
-  const int64_t step = (int64_t)gridDim.x * kBlock;
-  for (int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x; i < total; i += step) {
-    const int64_t row = i / pieces, c = i % pieces;
-    Piece<float> p;
-    p.load(dy + row * dys + 8 * c);
-    float f[8];
-    p.get(f);
+// ------------------------------------------------------------ weight gradient
+// Operands for the matrix product come token-major in blocks of 64 tokens, [block][column]
+// [64 tokens] bf16 (128-byte rows: a k-tile of the mainloop), zeros behind the last token.
+constexpr int kTokens = kRowBytes / 2;
+
+// A lane takes 4 columns of 8 tokens: load(first token, first column, tokens that are
+// there), then out(place of a column's 8 tokens, column).  The 8 lanes that share columns
+// are neighbours, so that they write whole 128-byte rows; a workgroup has 128 columns.
+template <class Load, class Out>
+__device__ __forceinline__ void to_blocks(int64_t rows, int64_t n, Load&& load, Out&& out) {
+  const int64_t block = blockIdx.x, c0 = blockIdx.y * (int64_t)128 + 4 * (threadIdx.x >> 3);
+  const int oct = threadIdx.x & 7;
+  if (c0 >= n) return;
+  const int64_t t0 = block * kTokens + 8 * oct;
+  load(t0, c0, (int)max<int64_t>(0, min<int64_t>(8, rows - t0)));
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = __float_as_uint(f[2 * j]), hi = __float_as_uint(f[2 * j + 1]);
-        // a NaN whose upper bits are an infinity's stays one
-        const uint32_t a = abs_bits(f[2 * j]) > 0x7f800000u ? 0x7fc00000u : lo & 0xffff0000u;
-        const uint32_t b = abs_bits(f[2 * j + 1]) > 0x7f800000u ? 0x7fc00000u : hi & 0xffff0000u;
-        w[j] = (a >> 16) | b;
-        f[2 * j] = abs_bits(f[2 * j]) >= 0x7f800000u ? 0.0f : f[2 * j] - __uint_as_float(a);
-        f[2 * j + 1] =
-            abs_bits(f[2 * j + 1]) >= 0x7f800000u ? 0.0f : f[2 * j + 1] - __uint_as_float(b);
-      }
-      *reinterpret_cast<uint4*>(parts + (k * rows + row) * n + 8 * c) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
+  for (int c = 0; c < 4; ++c) out((block * n + c0 + c) * kTokens + 8 * oct, c);
 }
 
-// ------------------------------------------------------------ weight gradient
+__global__ __launch_bounds__(kBlock) void act8_blocks_kernel(const int8_t* __restrict__ codes,
+                                                             const uint8_t* __restrict__ exps,
+                                                             uint16_t* __restrict__ x, int64_t rows,
+                                                             int64_t d) {
+  float v[8][4];
+  to_blocks(
+      rows, d,
+      [&](int64_t t0, int64_t c0, int live) {
+        const int64_t groups = (d + kAct8Group - 1) / kAct8Group;
+        uint32_t w[8], e[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          w[t] = e[t] = 0;
+          if (t < live) {
+            w[t] = *reinterpret_cast<const uint32_t*>(codes + (t0 + t) * d + c0);
+            e[t] = exps[(t0 + t) * groups + c0 / kAct8Group];
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            v[t][c] = (float)((int32_t)(w[t] << (24 - 8 * c)) >> 24) * __uint_as_float(e[t] << 23);
+      },
+      [&](int64_t at, int c) {
+        *reinterpret_cast<uint4*>(x + at) =
+            make_uint4(pack_bf16x2(v[0][c], v[1][c]), pack_bf16x2(v[2][c], v[3][c]),
+                       pack_bf16x2(v[4][c], v[5][c]), pack_bf16x2(v[6][c], v[7][c]));
+      });
+}
+
+// An fp32 dy as three bf16 terms whose sum it is: the leading 8 bits of what is left,
+// three times; an infinity or NaN goes into the first alone.  Terms `part` values apart.
+__global__ __launch_bounds__(kBlock) void act8_terms_kernel(const float* __restrict__ dy,
+                                                            int64_t dys, uint16_t* __restrict__ out,
+                                                            int64_t part, int64_t rows, int64_t n) {
+  float v[8][4];
+  to_blocks(
+      rows, n,
+      [&](int64_t t0, int64_t c0, int live) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          float4 f = make_float4(0, 0, 0, 0);
+          if (t < live) f = *reinterpret_cast<const float4*>(dy + (t0 + t) * dys + c0);
+          v[t][0] = f.x, v[t][1] = f.y, v[t][2] = f.z, v[t][3] = f.w;
+        }
+      },
+      [&](int64_t at, int c) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          uint32_t top[8];
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const uint32_t u = __float_as_uint(v[t][c]), m = u & 0x7fffffffu;
+            // a NaN whose upper bits are an infinity's stays one
+            top[t] = m > 0x7f800000u ? 0x7fc00000u : u & 0xffff0000u;
+            v[t][c] = m >= 0x7f800000u ? 0.0f : v[t][c] - __uint_as_float(top[t]);
+          }
+          *reinterpret_cast<uint4*>(out + k * part + at) =
+              make_uint4(top[0] >> 16 | top[1], top[2] >> 16 | top[3], top[4] >> 16 | top[5],
+                         top[6] >> 16 | top[7]);
+        }
+      });
+}
+
 using WTile = TileShape<256, 256, 2, 4>;
-constexpr int kTokens = kRowBytes / 2;  // tokens of a k-tile
 constexpr int kEpiCols = 64;
 constexpr int kEpiStride = kEpiCols + 8;  // floats per staged row
 
-// A tokens-by-columns operand whose k-tiles are walked `parts` times (x8), or
-// once over parts one after the other (dy's terms).
+// k-tiles [k0, k0 + n) of an operand, kParts times: of x again and again, of dy's terms
+// one after the other (part_stride bytes between them).
+template <class Base, int kParts>
 struct PartLoader {
-  using Base = KMajorLoader<uint16_t, WTile::kWaves>;
   static constexpr int kPer = Base::kPer;
   Base l;
-  int64_t per_part, part_stride;  // k-tiles of a part, bytes between parts
-  const char* base;
+  int64_t n, part_stride;
   __device__ __forceinline__ rsrc_t rsrc(int64_t kt, bool live = true) const {
-    const int64_t part = kt / per_part, k = kt - part * per_part;
-    return make_rsrc(base + part * part_stride + k * l.kt_stride,
-                     live ? l.valid_bytes - k * l.kt_stride : 0);
+    if constexpr (kParts == 1) {
+      return l.rsrc(kt, live);
+    } else {
+      const int64_t part = kt / n;
+      Base at = l;
+      at.base += part * part_stride;
+      return at.rsrc(kt - part * n, live);
+    }
   }
   __device__ __forceinline__ void issue_one(rsrc_t r, lds_char* stage, int q) const {
     l.issue_one(r, stage, q);
@@ -159,50 +212,177 @@ struct PartLoader {
     for (int q = 0; q < kPer; ++q) l.issue_one(r, stage, q);
   }
 };
-// Columns from n0 of token rows [0, rows), ld values apart, n values each.
-__device__ __forceinline__ PartLoader part_loader(const uint16_t* p, int64_t ld, int64_t rows,
-                                                  int64_t n, int64_t n0, int64_t part_stride) {
-  PartLoader l;
-  l.base = reinterpret_cast<const char*>(p + n0);
-  l.l.init(l.base, kRowBytes, ld * 2, kTokens * ld * 2, ((rows - 1) * ld + n - n0) * 2);
-  l.per_part = (rows + kTokens - 1) / kTokens;
-  l.part_stride = part_stride;
+using BlockLoader = DirectLoader<256, WTile::kWaves>;
+using RowLoader = KMajorLoader<uint16_t, WTile::kWaves>;
+// 256 columns from n0 of an operand of N columns in blocks.
+__device__ __forceinline__ BlockLoader block_loader(const uint16_t* p, int64_t N, int64_t n0,
+                                                    int64_t k0) {
+  BlockLoader l;
+  l.init(p + (k0 * N + n0) * kTokens, kRowBytes, N * kRowBytes, (N - n0) * kRowBytes, 0);
+  return l;
+}
+// The same of rows [rows][ld] of N columns.
+__device__ __forceinline__ RowLoader row_loader(const uint16_t* p, int64_t ld, int64_t rows,
+                                                int64_t N, int64_t n0, int64_t k0) {
+  RowLoader l;
+  l.init(p + k0 * kTokens * ld + n0, kRowBytes, ld * 2, kTokens * ld * 2,
+         ((rows - k0 * kTokens - 1) * ld + N - n0) * 2);
   return l;
 }
 
+// A k-tile's products with x's fragments read as rows and dy's transposed from token rows
+// (kRows), or both as rows.  Reads for the next 16 tokens are spread between the matrix
+// instructions, hook(q) follows instruction q.  The transposing reads are inline assembly,
+// each block with its wait: the compiler lets the builtin wait for every direct-to-LDS load
+// in flight, also those into the other stage (2560 x 7680 at 32K tokens: 1438 us with it, 1118 without).
+template <bool kRows>
+struct GradMma {
+  using S = WTile;
+  using Plain = Mma16<S, false, false>;
+  static constexpr int kSteps = Plain::kSteps;
+  // A lane's addresses in a stage's first 16 token rows: [columns 32 apart][tokens 4 apart]
+  // (see read_a_tr in gemm_core.h: a step of 16 tokens adds 16 rows, and only that).
+  uint32_t at[2][2];
+  __device__ __forceinline__ void init(const LanePos& p) {
+    if constexpr (kRows) {
+      const int g = p.lane >> 4, j = p.lane & 15;
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int m = p.wave_n0 + 32 * f + 16 * (g & 1) + 4 * (j & 3);
+          const int R = (m >> 6) * 64 + 8 * (g >> 1) + (j >> 2) + 4 * h;
+          at[f][h] = (uint32_t)R * kRowBytes +
+                     (uint32_t)((((m & 63) >> 3) ^ lds_swz_tr(R)) << 4) + (uint32_t)((m & 7) * 2);
+        }
+    }
+  }
+  __device__ __forceinline__ void read_rows(bf16x8_t (&b)[2], const lds_char* sB, int s) const {
+    const uint32_t base = (uint32_t)(uintptr_t)sB + (uint32_t)(16 * s * kRowBytes);
+    u32x2_t x[4];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4\n\t"
+        "ds_read_b64_tr_b16 %1, %5\n\t"
+        "ds_read_b64_tr_b16 %2, %6\n\t"
+        "ds_read_b64_tr_b16 %3, %7\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+        : "v"(base + at[0][0]), "v"(base + at[0][1]), "v"(base + at[1][0]), "v"(base + at[1][1])
+        : "memory");
+    b[0] = __builtin_bit_cast(bf16x8_t, u32x4_t{x[0][0], x[0][1], x[1][0], x[1][1]});
+    b[1] = __builtin_bit_cast(bf16x8_t, u32x4_t{x[2][0], x[2][1], x[3][0], x[3][1]});
+  }
+  template <class Hook>
+  __device__ __forceinline__ void ktile(Accum<S>& acc, const lds_char* sA, const lds_char* sB,
+                                        const LanePos& p, Hook&& hook) const {
+    if constexpr (!kRows) {
+      Plain::ktile_spread(acc, sA, sB, p, hook);
+    } else {
+      static_assert(S::MB == 4 && S::NB == 2, "the reads below");
+      bf16x8_t a[2][4], b[2][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[0][i] = Plain::read_a(sA, p, i, 0);
+      read_rows(b[0], sB, 0);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          const int i = m >> 1, j = m & 1;
+          acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[s & 1][i], b[s & 1][j],
+                                                                acc.v[i][j], 0, 0, 0);
+          if (s + 1 < kSteps) {
+            if (m < 4) a[(s + 1) & 1][m] = Plain::read_a(sA, p, m, s + 1);
+            if (m == 5) read_rows(b[(s + 1) & 1], sB, s + 1);
+          }
+          hook(8 * s + m);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+  }
+};
+
+// The mainloop of gemm_core.h on these fragments: k-tile kt + 1's loads one after each of
+// kt's first matrix instructions.
+template <class Mma, class LA, class LB>
+__device__ __forceinline__ void grad_mainloop(Accum<WTile>& acc, LA& la, LB& lb, int64_t nk,
+                                              lds_char* smem, const LanePos& p) {
+  using S = WTile;
+  constexpr int kLoads = LA::kPer + LB::kPer;
+  static_assert(kLoads <= Mma::kSteps * S::MB * S::NB, "the loads fit the k-tile's MFMAs");
+  Mma mma;
+  mma.init(p);
+  la.issue(0, smem);
+  lb.issue(0, smem + S::BM * kRowBytes);
+  wait_vmcnt<0>();
+  __syncthreads();
+  for (int64_t kt = 0; kt < nk; ++kt) {
+    const lds_char* cur = smem + (kt & 1) * S::kStageBytes;
+    lds_char* nxt = smem + ((kt + 1) & 1) * S::kStageBytes;
+    const bool more = kt + 1 < nk;
+    const rsrc_t ra = la.rsrc(kt + 1, more), rb = lb.rsrc(kt + 1, more);
+    mma.ktile(acc, cur, cur + S::BM * kRowBytes, p, [&](int q) {
+      if (q < LA::kPer)
+        la.issue_one(ra, nxt, q);
+      else if (q < kLoads)
+        lb.issue_one(rb, nxt + S::BM * kRowBytes, q - LA::kPer);
+    });
+    wait_vmcnt<0>();
+    __syncthreads();
+  }
+}
+
+// Tiles of the gradient; the first `whole` by one workgroup each, the others by
+// `slices` workgroups, `slice` k-tiles each, that leave their sums in `part`
+// [tile][slice][256][256].
 struct GradArgs {
-  const uint16_t* x;   // [rows][M], decoded
-  const uint16_t* dy;  // [parts][rows][N], rows dys apart
-  int64_t rows, M, N, dys;
-  int64_t slice;       // tokens of a slice, a multiple of kTokens
-  int64_t dy_part;     // values between dy's parts
-  int32_t parts;
-  int32_t slices;
-  void* out;           // slices > 1: fp32 [slices][M][N]; otherwise the gradient
+  const uint16_t* x;   // blocks of [M]
+  const uint16_t* dy;  // rows dys apart (bf16), or terms in blocks of [N]
+  int64_t rows, M, N, dys, ktiles;
+  int64_t dy_part;     // values between dy's terms
+  int64_t slice;
+  int32_t whole, slices;
+  float* part;
+  void* out;
   bool accumulate;
 };
 
-template <typename TO>
+template <typename TO, bool kTerms>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 act8_grad_kernel(GradArgs g) {
   using S = WTile;
   static_assert(S::kLdsBytes >= S::BM * kEpiStride * 4, "epilogue stage fits the pipeline's LDS");
+  constexpr int kParts = kTerms ? 3 : 1;
   __shared__ __attribute__((aligned(16))) char smem_raw[S::kLdsBytes];
   lds_char* smem = (lds_char*)smem_raw;
   const int tiles_m = (int)((g.M + S::BM - 1) / S::BM), tiles_n = (int)((g.N + S::BN - 1) / S::BN);
-  const int L = xcd_remap(blockIdx.x, (int)gridDim.x);
-  const int64_t slice = L / (tiles_m * tiles_n);
-  const TileCoord tc = grouped_tile(L % (tiles_m * tiles_n), tiles_m, tiles_n, 8);
+  int tile, slice = -1;
+  int64_t k0 = 0, n = g.ktiles;
+  if ((int)blockIdx.x < g.whole) {
+    tile = xcd_remap(blockIdx.x, g.whole);
+  } else {
+    const int rest = tiles_m * tiles_n - g.whole;
+    const int u = xcd_remap(blockIdx.x - g.whole, rest * g.slices);
+    slice = u / rest, tile = g.whole + u % rest;
+    k0 = slice * g.slice, n = min(g.slice, g.ktiles - k0);
+  }
+  const TileCoord tc = grouped_tile(tile, tiles_m, tiles_n, 8);
   const int64_t m0 = (int64_t)tc.m * S::BM, n0 = (int64_t)tc.n * S::BN;
-  const int64_t k0 = slice * g.slice, rows = min(g.slice, g.rows - k0);
   Accum<S> acc;
   acc.zero();
   const LanePos p = lane_pos<S>();
-  PartLoader la = part_loader(g.x + k0 * g.M, g.M, rows, g.M, m0, 0);
-  PartLoader lb = part_loader(g.dy + k0 * g.dys, g.dys, rows, g.N, n0, g.dy_part * 2);
-  mainloop<uint16_t, S, true, true, true, 1>(acc, la, lb, la.per_part * g.parts, smem, p,
-                                             [](int64_t) {});
-  TO* const out = static_cast<TO*>(g.out) + slice * g.M * g.N;
+  PartLoader<BlockLoader, kParts> la{block_loader(g.x, g.M, m0, k0), n, 0};
+  if constexpr (kTerms) {
+    PartLoader<BlockLoader, kParts> lb{block_loader(g.dy, g.N, n0, k0), n, g.dy_part * 2};
+    grad_mainloop<GradMma<false>>(acc, la, lb, n * kParts, smem, p);
+  } else {
+    PartLoader<RowLoader, kParts> lb{row_loader(g.dy, g.dys, g.rows, g.N, n0, k0), n, 0};
+    grad_mainloop<GradMma<true>>(acc, la, lb, n, smem, p);
+  }
+  float* const part =
+      slice < 0 ? nullptr
+                : g.part + ((int64_t)(tile - g.whole) * g.slices + slice) * (S::BM * S::BN);
   for (int q = 0; q < S::BN / kEpiCols; ++q) {
     __syncthreads();  // the mainloop's (or the previous pass's) reads of LDS are done
 #pragma unroll
@@ -224,7 +404,11 @@ act8_grad_kernel(GradArgs g) {
       const floatx4_t lo = lds_load<floatx4_t>(smem + ((uint32_t)t * kEpiStride + c) * 4);
       const floatx4_t hi = lds_load<floatx4_t>(smem + ((uint32_t)t * kEpiStride + c + 4) * 4);
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      TO* const to = out + (m0 + t) * g.N + cb + c;
+      if (part) {
+        Piece<float>::store(part + t * S::BN + kEpiCols * q + c, v);
+        continue;
+      }
+      TO* const to = static_cast<TO*>(g.out) + (m0 + t) * g.N + cb + c;
       if (g.accumulate) {
         Piece<TO> old;
         old.load(to);
@@ -238,35 +422,40 @@ act8_grad_kernel(GradArgs g) {
   }
 }
 
-// grad (+)= the slices' products, in order.
+// The tiles that came in slices, added in order: 8 rows of a tile a workgroup.
 template <typename TO>
-__global__ __launch_bounds__(kBlock) void act8_sum_kernel(const float* __restrict__ part,
-                                                          int slices, TO* __restrict__ grad,
-                                                          int64_t n, bool accumulate) {
-  const int64_t step = (int64_t)gridDim.x * kBlock * 8;
-  for (int64_t i = ((int64_t)blockIdx.x * kBlock + threadIdx.x) * 8; i < n; i += step) {
-    float f[8];
-    Piece<float> p;
-    p.load(part + i);
-    p.get(f);
-    for (int s = 1; s < slices; ++s) {
-      Piece<float> q;
-      q.load(part + s * n + i);
-      float v[8];
-      q.get(v);
+__global__ __launch_bounds__(kBlock) void act8_sum_kernel(GradArgs g) {
+  using S = WTile;
+  constexpr int kEach = S::BM * S::BN / (8 * kBlock);  // workgroups of a tile
+  const int tiles_m = (int)((g.M + S::BM - 1) / S::BM), tiles_n = (int)((g.N + S::BN - 1) / S::BN);
+  const int tile = blockIdx.x / kEach;
+  const TileCoord tc = grouped_tile(g.whole + tile, tiles_m, tiles_n, 8);
+  const int at = (blockIdx.x % kEach) * (8 * kBlock) + 8 * threadIdx.x;
+  const int64_t row = (int64_t)tc.m * S::BM + at / S::BN, col = (int64_t)tc.n * S::BN + at % S::BN;
+  if (row >= g.M || col >= g.N) return;
+  const float* p = g.part + (int64_t)tile * g.slices * (S::BM * S::BN) + at;
+  float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += v[j];
-    }
-    if (accumulate) {
-      Piece<TO> old;
-      old.load(grad + i);
-      float v[8];
-      old.get(v);
+  for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < g.slices; ++s) {
+    Piece<float> q;
+    q.load(p + (int64_t)s * (S::BM * S::BN));
+    float v[8];
+    q.get(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += v[j];
-    }
-    Piece<TO>::store(grad + i, f);
+    for (int j = 0; j < 8; ++j) f[j] += v[j];
   }
+  TO* const to = static_cast<TO*>(g.out) + row * g.N + col;
+  if (g.accumulate) {
+    Piece<TO> old;
+    old.load(to);
+    float v[8];
+    old.get(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] += v[j];
+  }
+  Piece<TO>::store(to, f);
 }
 
 template <typename F>
@@ -294,33 +483,50 @@ hipError_t in_launches(int64_t rows, int64_t per, F&& f) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Token slices: a workgroup owns a CU, so tiles x slices should fill whole rounds
-// of 256 CUs, at some 1.7 us for 64 tokens of a tile; a slice more costs a write
-// and a read of the fp32 gradient (8 bytes at 4 TB/s) and 10 us.
-int slices_of(const Act8Grad& g) {
-  const int64_t tiles = ((g.d_in + 255) / 256) * ((g.d_out + 255) / 256);
-  const int64_t ktiles = (g.rows + kTokens - 1) / kTokens * (g.dt == Dtype::F32 ? 3 : 1);
-  int best = 1;
+int64_t ktiles_of(const Act8Grad& g) { return (g.rows + kTokens - 1) / kTokens; }
+int64_t grad_tiles(const Act8Grad& g) {
+  return ((g.d_in + 255) / 256) * ((g.d_out + 255) / 256);
+}
+
+// A workgroup owns a CU: tiles that fill whole rounds of 256 CUs are one workgroup's
+// each, in step with one another along the tokens (they share their operands in L2); what
+// is left over is cut along the tokens, so that the last round is short.  Some 1.6 us for
+// 64 tokens of a tile and 10 around it; a slice more costs a write and a read of its
+// 256 KB of sums.
+struct Slices {
+  int whole, slices;
+  int64_t slice;  // k-tiles of a slice
+};
+Slices slices_of(const Act8Grad& g) {
+  constexpr int kCus = 256;
+  const int64_t tiles = grad_tiles(g), n = ktiles_of(g);
+  const double us = g.dt == Dtype::F32 ? 3 * 1.6 : 1.6;
+  const int rest = (int)(tiles % kCus);
+  Slices best{(int)(tiles - rest), 1, n};
   double least = 0;
-  for (int s = 1; s <= 32 && (s == 1 || g.rows >= (int64_t)s * 4 * kTokens); ++s) {
-    const double rounds = (double)((tiles * s + 255) / 256);
-    const double us = rounds * ((double)((ktiles + s - 1) / s) * 1.7 + 10.0) +
-                      (s > 1 ? s * (double)(g.d_in * g.d_out) * 8e-6 / 4.0 + 10.0 : 0.0);
-    if (s == 1 || us < least) best = s, least = us;
+  for (int64_t s = 1; s <= 64 && (s == 1 || n >= 2 * s); ++s) {
+    const int64_t slice = (n + s - 1) / s, used = (n + slice - 1) / slice;
+    const double rounds = (double)((rest * used + kCus - 1) / kCus);
+    const double t = rounds * ((double)slice * us + 10.0) +
+                     (used > 1 ? (double)(rest * used) * 0.5e6 / 4e6 + 5.0 : 0.0);
+    if (s == 1 || t < least) best.slices = (int)used, best.slice = slice, least = t;
   }
+  if (best.slices == 1) best.whole = (int)tiles;
   return best;
 }
 
+// Workspace: x and dy's terms in blocks, the slices' sums.
 struct GradPlan {
   size_t dy, part, bytes;
-  int slices;
+  Slices s;
 };
 GradPlan grad_plan(const Act8Grad& g) {
   GradPlan p;
-  p.slices = slices_of(g);
-  p.dy = align256((size_t)(g.rows * g.d_in) * 2);
-  p.part = p.dy + (g.dt == Dtype::F32 ? align256((size_t)(3 * g.rows * g.d_out) * 2) : 0);
-  p.bytes = p.part + (p.slices > 1 ? (size_t)p.slices * g.d_in * g.d_out * sizeof(float) : 0);
+  p.s = slices_of(g);
+  const size_t tokens = (size_t)ktiles_of(g) * kTokens;
+  p.dy = align256(tokens * g.d_in * 2);
+  p.part = p.dy + (g.dt == Dtype::F32 ? align256(3 * tokens * g.d_out * 2) : 0);
+  p.bytes = p.part + (size_t)(grad_tiles(g) - p.s.whole) * p.s.slices * (256 * 256 * sizeof(float));
   return p;
 }
 
@@ -358,45 +564,50 @@ hipError_t launch_act8_weight_grad(const Act8Grad& g, const int8_t* codes, const
                                    const void* dy, void* grad, void* ws, hipStream_t s) {
   const GradPlan p = grad_plan(g);
   char* const base = static_cast<char*>(ws);
-  uint16_t* const x = reinterpret_cast<uint16_t*>(base);
-  float* const part = reinterpret_cast<float*>(base + p.part);
-  hipError_t e = launch_act8_load(Dtype::BF16, codes, exps, g.rows, g.d_in, g.d_in, x, s);
-  if (e != hipSuccess) return e;
+  const int64_t n = ktiles_of(g);
   GradArgs a{};
-  a.x = x, a.rows = g.rows, a.M = g.d_in, a.N = g.d_out;
-  a.slice = (g.rows + p.slices - 1) / p.slices;
-  a.slice = (a.slice + kTokens - 1) / kTokens * kTokens;
-  a.slices = (int32_t)((g.rows + a.slice - 1) / a.slice);
+  a.x = reinterpret_cast<uint16_t*>(base), a.rows = g.rows, a.M = g.d_in, a.N = g.d_out;
+  a.ktiles = n, a.slice = p.s.slice, a.whole = p.s.whole, a.slices = p.s.slices;
+  a.part = reinterpret_cast<float*>(base + p.part);
+  a.out = grad, a.accumulate = g.accumulate;
+  uint16_t* const x = reinterpret_cast<uint16_t*>(base);
+  const int64_t groups = (g.d_in + kAct8Group - 1) / kAct8Group;
+  const auto columns = [](int64_t n) { return (unsigned)((n + 127) / 128); };
+  hipError_t e = in_launches(n, 1, [&](int64_t at, int64_t, dim3 grid) {
+    grid.y = columns(g.d_in);
+    const int64_t t = at * kTokens;
+    act8_blocks_kernel<<<grid, kBlock, 0, s>>>(codes + t * g.d_in, exps + t * groups,
+                                               x + t * g.d_in, g.rows - t, g.d_in);
+  });
+  if (e != hipSuccess) return e;
   if (g.dt == Dtype::F32) {
     uint16_t* const terms = reinterpret_cast<uint16_t*>(base + p.dy);
-    const int64_t n = g.rows * (g.d_out / 8);
-    act8_split_kernel<<<dim3((unsigned)std::min<int64_t>((n + kBlock - 1) / kBlock, 8192)), kBlock,
-                        0, s>>>(static_cast<const float*>(dy), g.dys, terms, g.rows, g.d_out);
-    e = hipGetLastError();
+    a.dy = terms, a.dy_part = n * kTokens * g.d_out;
+    e = in_launches(n, 1, [&](int64_t at, int64_t, dim3 grid) {
+      grid.y = columns(g.d_out);
+      const int64_t t = at * kTokens;
+      act8_terms_kernel<<<grid, kBlock, 0, s>>>(static_cast<const float*>(dy) + t * g.dys, g.dys,
+                                                terms + t * g.d_out, a.dy_part, g.rows - t,
+                                                g.d_out);
+    });
     if (e != hipSuccess) return e;
-    a.dy = terms, a.dys = g.d_out, a.parts = 3, a.dy_part = g.rows * g.d_out;
   } else {
-    a.dy = static_cast<const uint16_t*>(dy), a.dys = g.dys, a.parts = 1, a.dy_part = 0;
+    a.dy = static_cast<const uint16_t*>(dy), a.dys = g.dys;
   }
-  const int64_t tiles = ((g.d_in + 255) / 256) * ((g.d_out + 255) / 256);
-  const dim3 grid((unsigned)(tiles * a.slices));
-  const bool direct = a.slices == 1;
-  a.out = direct ? grad : part;
-  a.accumulate = direct && g.accumulate;
-  if (direct && g.grad_dt == Dtype::BF16)
-    act8_grad_kernel<uint16_t><<<grid, 512, 0, s>>>(a);
+  const int64_t rest = grad_tiles(g) - a.whole;
+  const dim3 grid((unsigned)(a.whole + rest * a.slices)), sums((unsigned)(rest * 32));
+  if (g.dt == Dtype::F32)
+    act8_grad_kernel<float, true><<<grid, 512, 0, s>>>(a);
+  else if (g.grad_dt == Dtype::F32)
+    act8_grad_kernel<float, false><<<grid, 512, 0, s>>>(a);
   else
-    act8_grad_kernel<float><<<grid, 512, 0, s>>>(a);
+    act8_grad_kernel<uint16_t, false><<<grid, 512, 0, s>>>(a);
   e = hipGetLastError();
-  if (e != hipSuccess || direct) return e;
-  const int64_t n = g.d_in * g.d_out;
-  const dim3 sg((unsigned)std::min<int64_t>((n / 8 + kBlock - 1) / kBlock, 16384));
-  if (g.grad_dt == Dtype::BF16)
-    act8_sum_kernel<uint16_t><<<sg, kBlock, 0, s>>>(part, a.slices, static_cast<uint16_t*>(grad), n,
-                                                    g.accumulate);
+  if (e != hipSuccess || rest == 0) return e;
+  if (g.grad_dt == Dtype::F32)
+    act8_sum_kernel<float><<<sums, kBlock, 0, s>>>(a);
   else
-    act8_sum_kernel<float><<<sg, kBlock, 0, s>>>(part, a.slices, static_cast<float*>(grad), n,
-                                                 g.accumulate);
+    act8_sum_kernel<uint16_t><<<sums, kBlock, 0, s>>>(a);
   return hipGetLastError();
 }
 
