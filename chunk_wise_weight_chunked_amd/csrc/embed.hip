@@ -5,7 +5,7 @@
 //
 // The lookup copies rows: bound by HBM.  The gradient sorts the tokens by id
 // (least significant digit first, stable, so that equal ids keep the order of
-// their places), cuts the sorted tokens into pieces of kPiece and lets a wave sum
+// their places), cuts the sorted tokens into pieces of 8 or 32 and lets a wave sum
 // a piece's rows in registers: an id whose tokens lie in one piece gets its row
 // written at once, the sums of ids that reach over pieces go to the workspace and
 // are added in order by a last launch.  No atomic sums: the result does not
@@ -22,11 +22,9 @@ namespace ttt {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kPiece = 32;       // sorted tokens that a wave sums
+constexpr int kPiece = 32;       // sorted tokens that a wave sums, at most
 constexpr int kWaveCols = 512;   // columns of a wave: 8 a lane
-constexpr int kSortBlock = 1024;
-constexpr int kSortTile = 4096;  // tokens that a workgroup of the sort orders
-constexpr int kSortRounds = kSortTile / kSortBlock;
+constexpr int kSortBlock = 1024;  // tokens that a workgroup of the sort orders, one a lane
 constexpr int kSortWaves = kSortBlock / 64;
 constexpr int kMaxBins = 512;
 
@@ -73,21 +71,37 @@ struct SortIn {
   }
 };
 
+// A share of a gradient's zeros, written by the workgroups of a launch of the sort that
+// come behind its own: the sort leaves most of the chip idle, and the zeros need no more
+// than the memory's bandwidth.
+struct Zeros {
+  uint4* p;       // null: none
+  int64_t n;
+  int32_t own;    // the launch's own workgroups
+  template <int kThreads>
+  __device__ __forceinline__ bool fill() const {
+    if ((int)blockIdx.x < own) return false;
+    const int64_t step = (int64_t)(gridDim.x - own) * kThreads;
+    for (int64_t i = (int64_t)(blockIdx.x - own) * kThreads + threadIdx.x; i < n; i += step)
+      p[i] = make_uint4(0, 0, 0, 0);
+    return true;
+  }
+};
+
 // hist[bin][tile]: tokens of a tile with this digit.
 __global__ __launch_bounds__(kSortBlock) void embed_hist_kernel(SortIn in, int shift, int bins,
                                                                 int64_t tiles,
-                                                                uint32_t* __restrict__ hist) {
+                                                                uint32_t* __restrict__ hist,
+                                                                Zeros zeros) {
   __shared__ uint32_t count[kMaxBins];
-  for (int b = threadIdx.x; b < bins; b += kSortBlock) count[b] = 0;
+  if (zeros.fill<kSortBlock>()) return;
+  const int b = threadIdx.x;
+  if (b < bins) count[b] = 0;
   __syncthreads();
-  const int64_t n0 = (int64_t)blockIdx.x * kSortTile;
-#pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
-    const int64_t n = n0 + r * kSortBlock + threadIdx.x;
-    if (n < in.N) atomicAdd(&count[(in.key(n) >> shift) & (bins - 1)], 1u);
-  }
+  const int64_t n = (int64_t)blockIdx.x * kSortBlock + threadIdx.x;
+  if (n < in.N) atomicAdd(&count[(in.key(n) >> shift) & (bins - 1)], 1u);
   __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += kSortBlock) hist[b * tiles + blockIdx.x] = count[b];
+  if (b < bins) hist[b * tiles + blockIdx.x] = count[b];
 }
 
 // Exclusive sums of v over the workgroup's threads (kThreads a multiple of 64),
@@ -119,8 +133,10 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* wave_s
 // hist[bin][tile] -> tokens of this digit in the tiles in front; total[bin].
 __global__ __launch_bounds__(kBlock) void embed_scan_kernel(uint32_t* __restrict__ hist,
                                                             int64_t tiles,
-                                                            uint32_t* __restrict__ total) {
+                                                            uint32_t* __restrict__ total,
+                                                            Zeros zeros) {
   __shared__ uint32_t wave_sum[kBlock / 64];
+  if (zeros.fill<kBlock>()) return;
   uint32_t run = 0;
   uint32_t* const h = hist + blockIdx.x * tiles;
   for (int64_t t0 = 0; t0 < tiles; t0 += kBlock) {
@@ -134,51 +150,39 @@ __global__ __launch_bounds__(kBlock) void embed_scan_kernel(uint32_t* __restrict
   if (threadIdx.x == 0) total[blockIdx.x] = run;
 }
 
-// The tile's tokens to their places.  Wave w takes the tokens 256 w .. of the
-// tile in rounds of 64; a token's rank among those of its digit is the count of
-// the wave's earlier rounds and of the lower lanes of its own with that digit,
-// found by a ballot for each bit.
+// The tile's tokens to their places.  A token's rank among those of its digit is the
+// count of the lower lanes of its wave with that digit, found by a ballot for each bit,
+// and of the waves and tiles in front.
 __global__ __launch_bounds__(kSortBlock) void embed_scatter_kernel(
     SortIn in, int shift, int bits, int64_t tiles, const uint32_t* __restrict__ hist,
     const uint32_t* __restrict__ total, uint32_t* __restrict__ keys_out,
-    uint32_t* __restrict__ pos_out) {
+    uint32_t* __restrict__ pos_out, Zeros zeros) {
   __shared__ uint32_t count[kSortWaves][kMaxBins];
   __shared__ uint32_t wave_sum[kSortWaves];
+  if (zeros.fill<kSortBlock>()) return;
   const int bins = 1 << bits;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int i = threadIdx.x; i < kSortWaves * bins; i += kSortBlock) count[i / bins][i % bins] = 0;
-  __syncthreads();
-  const int64_t n0 = (int64_t)blockIdx.x * kSortTile + wave * (64 * kSortRounds) + lane;
-  uint32_t key[kSortRounds], rank[kSortRounds];
-#pragma unroll
-  for (int r = 0; r < kSortRounds; ++r)
-    key[r] = n0 + 64 * r < in.N ? in.key(n0 + 64 * r) : 0;
-#pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
-    const bool live = n0 + 64 * r < in.N;
-    const uint32_t digit = (key[r] >> shift) & (bins - 1);
-    uint64_t same = __ballot(live);
-    for (int b = 0; b < bits; ++b) {
-      const bool one = (digit >> b) & 1;
-      const uint64_t with = __ballot(one);
-      same &= one ? with : ~with;
-    }
-    const uint32_t lower = __popcll(same & ((1ull << lane) - 1));
-    uint32_t before = 0;
-    if (live) before = count[wave][digit];
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (live && lower == 0) count[wave][digit] = before + (uint32_t)__popcll(same);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    rank[r] = before + lower;
-  }
-  __syncthreads();
-  // places: digits in front, tiles in front, waves in front
-  const bool has = threadIdx.x < (unsigned)bins;
+  const int64_t n = (int64_t)blockIdx.x * kSortBlock + threadIdx.x;
+  const bool live = n < in.N, has = threadIdx.x < (unsigned)bins;
+  const uint32_t key = live ? in.key(n) : 0;
+  const uint32_t place = live && in.pos ? in.pos[n] : (uint32_t)n;
   const uint32_t mine = has ? total[threadIdx.x] : 0;
+  const uint32_t tile = has ? hist[threadIdx.x * tiles + blockIdx.x] : 0;
+  for (int i = lane; i < bins; i += 64) count[wave][i] = 0;
+  const uint32_t digit = (key >> shift) & (bins - 1);
+  uint64_t same = __ballot(live);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (digit >> b) & 1;
+    const uint64_t with = __ballot(one);
+    same &= one ? with : ~with;
+  }
+  const uint32_t rank = __popcll(same & ((1ull << lane) - 1));
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if (live && rank == 0) count[wave][digit] = (uint32_t)__popcll(same);
+  __syncthreads();
   uint32_t all;
-  uint32_t at = block_exclusive<kSortBlock>(mine, wave_sum, &all);
+  uint32_t at = block_exclusive<kSortBlock>(mine, wave_sum, &all) + tile;
   if (has) {
-    at += hist[threadIdx.x * tiles + blockIdx.x];
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
       const uint32_t c = count[w][threadIdx.x];
@@ -187,90 +191,199 @@ __global__ __launch_bounds__(kSortBlock) void embed_scatter_kernel(
     }
   }
   __syncthreads();
+  if (!live) return;
+  const uint32_t to = count[wave][digit] + rank;
+  keys_out[to] = key;
+  pos_out[to] = place;
+}
+
+// All passes for up to kSmall tokens in one workgroup: tokens in LDS, wave w has the
+// tokens w 64 rounds .. of each pass in rounds of 64, and counts a digit's tokens of its
+// earlier rounds as well.  (A gradient of d = 1024 added to, one workgroup / the launches
+// above: 1000 tokens 15 / 21 us, 4100 26 / 39, 8000 39 / 40.)
+constexpr int kSmallRounds = 8;
+constexpr int kSmall = kSmallRounds * kSortBlock;
+__global__ __launch_bounds__(kSortBlock) void embed_sort_kernel(SortIn in, int passes, int bits,
+                                                                uint32_t* __restrict__ keys_out,
+                                                                uint32_t* __restrict__ pos_out,
+                                                                Zeros zeros) {
+  __shared__ uint32_t count[kSortWaves][kMaxBins];
+  __shared__ uint32_t wave_sum[kSortWaves];
+  __shared__ uint2 token[kSmall];  // key, place
+  if (zeros.fill<kSortBlock>()) return;
+  const int bins = 1 << bits, N = (int)in.N;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int rounds = (N + kSortBlock - 1) / kSortBlock;
+  const int n0 = wave * 64 * rounds + lane;
+  uint2 own[kSmallRounds];
 #pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
-    const int64_t n = n0 + 64 * r;
-    if (n >= in.N) continue;
-    const uint32_t to = count[wave][(key[r] >> shift) & (bins - 1)] + rank[r];
-    keys_out[to] = key[r];
-    pos_out[to] = in.pos ? in.pos[n] : (uint32_t)n;
+  for (int r = 0; r < kSmallRounds; ++r) {
+    const int n = n0 + 64 * r;
+    own[r] = make_uint2(r < rounds && n < N ? in.key(n) : 0, (uint32_t)n);
+  }
+  for (int p = 0; p < passes; ++p) {
+    const int shift = p * bits;
+    for (int i = lane; i < bins; i += 64) count[wave][i] = 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    uint32_t rank[kSmallRounds];
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+      if (r >= rounds) break;
+      const bool live = n0 + 64 * r < N;
+      const uint32_t digit = (own[r].x >> shift) & (bins - 1);
+      uint64_t same = __ballot(live);
+      for (int b = 0; b < bits; ++b) {
+        const bool one = (digit >> b) & 1;
+        const uint64_t with = __ballot(one);
+        same &= one ? with : ~with;
+      }
+      const uint32_t lower = __popcll(same & ((1ull << lane) - 1));
+      const uint32_t before = live ? count[wave][digit] : 0;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (live && lower == 0) count[wave][digit] = before + (uint32_t)__popcll(same);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      rank[r] = before + lower;
+    }
+    __syncthreads();
+    uint32_t mine = 0, all;
+    const bool has = threadIdx.x < (unsigned)bins;
+    if (has) {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) mine += count[w][threadIdx.x];
+    }
+    uint32_t at = block_exclusive<kSortBlock>(mine, wave_sum, &all);
+    if (has) {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        const uint32_t c = count[w][threadIdx.x];
+        count[w][threadIdx.x] = at;
+        at += c;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r)
+      if (r < rounds && n0 + 64 * r < N)
+        token[count[wave][(own[r].x >> shift) & (bins - 1)] + rank[r]] = own[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r)
+      if (r < rounds && n0 + 64 * r < N) own[r] = token[n0 + 64 * r];
+    __syncthreads();  // counts and tokens are written again
+  }
+#pragma unroll
+  for (int r = 0; r < kSmallRounds; ++r) {
+    const int n = n0 + 64 * r;
+    if (r < rounds && n < N) keys_out[n] = own[r].x, pos_out[n] = own[r].y;
   }
 }
 
 // ------------------------------------------------------------------- the sums
-__global__ __launch_bounds__(kBlock) void embed_zero_kernel(uint4* __restrict__ p, int64_t n) {
-  const int64_t step = (int64_t)gridDim.x * kBlock;
-  for (int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x; i < n; i += step)
-    p[i] = make_uint4(0, 0, 0, 0);
-}
-
-template <typename TO>
-__device__ __forceinline__ void put_row(TO* row, const float sum[8], float scale, bool accumulate) {
-  float f[8], old[8];
-  if (accumulate) {
-    Piece<TO> p;
-    p.load(row);
-    p.get(old);
-  }
+// A gradient's row from its sum and, where it is added to, what is there.
+template <typename TO, bool kAdd>
+__device__ __forceinline__ void put_row(TO* row, const float sum[8], float scale,
+                                        const Piece<TO>& there) {
+  float f[8];
+  there.get(f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = accumulate ? old[j] + scale * sum[j] : scale * sum[j];
+  for (int j = 0; j < 8; ++j) f[j] = kAdd ? f[j] + scale * sum[j] : scale * sum[j];
   Piece<TO>::store(row, f);
 }
 
-// A wave sums kWaveCols columns of a piece of the sorted tokens.  part[2 p] has
+// Zeros for rows without tokens: a wave takes kZeroRows rows from v0 on and looks each up
+// in the sorted tokens' ids.
+constexpr int kZeroRows = 16;
+template <typename TO>
+__device__ __forceinline__ void zero_rows(const uint32_t* __restrict__ keys, TO* __restrict__ grad,
+                                          int64_t N, int64_t V, int64_t d, int64_t v0) {
+  const int lane = threadIdx.x & 63;
+  const int64_t v = v0 + lane;
+  int64_t lo = 0, hi = N;  // the first token whose id is not below v
+  while (lane < kZeroRows && lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if ((int64_t)keys[mid] < v) lo = mid + 1; else hi = mid;
+  }
+  uint64_t none = __ballot(lane < kZeroRows && v < V && (lo == N || (int64_t)keys[lo] != v));
+  const int64_t n = d * (int64_t)sizeof(TO) / 16;
+  while (none) {
+    uint4* const row = reinterpret_cast<uint4*>(grad + (v0 + __builtin_ctzll(none)) * d);
+    none &= none - 1;
+    for (int64_t i = lane; i < n; i += 64) row[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// A wave sums kWaveCols columns of a piece of the sorted tokens; behind those waves come
+// the ones that write the zeros of rows [zero0, zero1).  part[2 p] has
 // the sum of piece p's first tokens where their id began in front of it or goes
 // on behind it without another in the piece, part[2 p + 1] that of its last
 // tokens where their id goes on behind it.
-template <typename T, typename TO>
+template <typename T, typename TO, bool kAdd>
 __global__ __launch_bounds__(kBlock) void embed_sum_kernel(
     const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos,
     const T* __restrict__ dout, TO* __restrict__ grad, float* __restrict__ part, int64_t N,
-    int64_t V, int64_t d, float scale, bool accumulate, int64_t units, int col_parts) {
+    int64_t V, int64_t d, float scale, int piece, int64_t units, int col_parts, int64_t zero0,
+    int64_t zero1) {
   const int lane = threadIdx.x & 63;
-  const int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
-  if (unit >= units) return;
+  const int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) +
+                       __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // wave-uniform
+  if (unit >= units) {
+    const int64_t v0 = zero0 + (unit - units) * kZeroRows;
+    if (v0 < zero1) zero_rows(keys, grad, N, zero1, d, v0);
+    return;
+  }
   const int64_t p = unit / col_parts;
   const int64_t col = (unit % col_parts) * kWaveCols + 8 * lane;
-  const int64_t n0 = p * kPiece;
-  const int n = (int)min<int64_t>(kPiece, N - n0);
+  const int64_t n0 = p * piece;
+  const int n = (int)min<int64_t>(piece, N - n0);
   // lane l: token l of the piece; ids in front of it and behind it (none: V + 1)
   const uint32_t none = (uint32_t)V + 1;
   const uint32_t key = lane < n ? keys[n0 + lane] : none;
-  const uint32_t at = lane < n ? pos[n0 + lane] : 0;
+  const uint32_t at = pos[n0 + min(lane, n - 1)];
   const uint32_t front = n0 > 0 ? keys[n0 - 1] : none;
   const uint32_t behind = n0 + n < N ? keys[n0 + n] : none;
   const bool mine = col < d;
+  const T* const from = dout + (mine ? col : 0);
   float sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
   int first = 0;  // of the current id
-  constexpr int kAhead = 8;
-  for (int t0 = 0; t0 < n; t0 += kAhead) {
+  // Rows are loaded ahead, and with kAdd the gradient's row of each token's id beside them
+  // (again and again for an id of many tokens, from L2): a call of 31984 tokens of 1024
+  // values takes 72.5 us, 75.3 where a wave waits for it at the end of each id.
+  constexpr int kAhead = kAdd ? 4 : 8;
+  struct Ahead {
     Piece<T> row[kAhead];
+    Piece<TO> there[kAhead];
+  } ahead[2];
+  // what is read for nothing (behind the last token, of no id) is never put anywhere
+  const auto load = [&](Ahead& a, int t0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      row[i].zero();
-      const int t = t0 + i;
-      const uint32_t where = __builtin_amdgcn_readlane(at, t);
-      const uint32_t id = __builtin_amdgcn_readlane(key, t);
-      if (t < n && mine && id < (uint32_t)V) row[i].load(dout + (int64_t)where * d + col);
+      a.row[i].load(from + (int64_t)(uint32_t)__builtin_amdgcn_readlane(at, t0 + i) * d);
+      a.there[i].zero();
+      if constexpr (kAdd) {
+        const uint32_t id = __builtin_amdgcn_readlane(key, t0 + i);
+        a.there[i].load(grad + (int64_t)(id < (uint32_t)V ? id : 0) * d + (mine ? col : 0));
+      }
+      __builtin_amdgcn_sched_barrier(0);  // in the order in which they are used
     }
+  };
+  const auto add = [&](const Ahead& a, int t0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int t = t0 + i;
-      if (t >= n) break;
       float f[8];
-      row[i].get(f);
+      a.row[i].get(f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += f[j];
       const uint32_t id = __builtin_amdgcn_readlane(key, t);
       const uint32_t next = t + 1 < n ? __builtin_amdgcn_readlane(key, t + 1) : behind;
-      if (t + 1 < n && next == id) continue;
+      if (t >= n || (t + 1 < n && next == id)) continue;
       // the id's last token of the piece
       if (id < (uint32_t)V && mine) {
-        const bool whole = (first > 0 || front != id) && (t + 1 < n || next != id);
+        const bool whole = (first > 0 || front != id) && next != id;
         if (whole)
-          put_row<TO>(grad + (int64_t)id * d + col, sum, scale, accumulate);
+          put_row<TO, kAdd>(grad + (int64_t)id * d + col, sum, scale, a.there[i]);
         else
           Piece<float>::store(part + (2 * p + (first > 0 ? 1 : 0)) * d + col, sum);
       }
@@ -278,36 +391,52 @@ __global__ __launch_bounds__(kBlock) void embed_sum_kernel(
       for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
       first = t + 1;
     }
+  };
+  load(ahead[0], 0);
+  for (int t0 = 0; t0 < n; t0 += 2 * kAhead) {
+    if (t0 + kAhead < n) load(ahead[1], t0 + kAhead);
+    add(ahead[0], t0);
+    if (t0 + 2 * kAhead < n) load(ahead[0], t0 + 2 * kAhead);
+    add(ahead[1], t0 + kAhead);
   }
 }
 
 // The rows of ids that reach over pieces: the workgroups of the piece in which
 // one begins add its pieces' sums, 4 waves every fourth and then each other's,
 // 256 columns each.
-template <typename TO>
+template <typename TO, bool kAdd>
 __global__ __launch_bounds__(kBlock) void embed_join_kernel(
     const uint32_t* __restrict__ keys, const float* __restrict__ part, TO* __restrict__ grad,
-    int64_t N, int64_t V, int64_t d, float scale, bool accumulate) {
+    int64_t N, int64_t V, int64_t d, float scale, int piece, unsigned pieces, int64_t zero0) {
   __shared__ float s[4][256];
-  const int64_t p = blockIdx.x, n0 = p * kPiece;
-  const int64_t last = min<int64_t>(n0 + kPiece, N) - 1;
+  if (blockIdx.x >= pieces) {  // the last rows' zeros
+    const int64_t v0 = zero0 + kZeroRows * (((int64_t)(blockIdx.x - pieces) * gridDim.y +
+                                             blockIdx.y) * (kBlock / 64) + (threadIdx.x >> 6));
+    if (v0 < V) zero_rows(keys, grad, N, V, d, v0);
+    return;
+  }
+  const int64_t p = blockIdx.x, n0 = p * piece;
+  const int64_t last = min<int64_t>(n0 + piece, N) - 1;
   if (last + 1 >= N) return;
   const uint32_t id = keys[last];
   if (id >= (uint32_t)V || keys[last + 1] != id) return;
   const bool inside = keys[n0] != id;  // begins behind the piece's first token
   if (!inside && n0 > 0 && keys[n0 - 1] == id) return;  // began in an earlier piece
-  // the first token behind the id's
-  int64_t lo = last + 1, hi = N;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (keys[mid] <= id) lo = mid + 1; else hi = mid;
-  }
-  const int64_t end = (lo - 1) / kPiece;  // its last piece
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  int64_t end = p;  // the id's last piece: those behind p begin with it
+  for (;;) {
+    const int64_t n = (end + 1 + lane) * piece;
+    const uint64_t other = __ballot(n >= N || keys[n] != id);
+    if (other) {
+      end += __builtin_ctzll(other);
+      break;
+    }
+    end += 64;
+  }
   const int64_t col = (int64_t)blockIdx.y * 256 + 4 * lane;
   float4 a = make_float4(0, 0, 0, 0);
   if (col < d) {
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t q = p + wave; q <= end; q += 4) {
       const int64_t slot = 2 * q + (q == p && inside ? 1 : 0);
       const float4 v = *reinterpret_cast<const float4*>(part + slot * d + col);
@@ -324,7 +453,10 @@ __global__ __launch_bounds__(kBlock) void embed_join_kernel(
     const int x = 8 * threadIdx.x + j;
     sum[j] = (s[0][x] + s[1][x]) + (s[2][x] + s[3][x]);
   }
-  put_row<TO>(grad + (int64_t)id * d + c, sum, scale, accumulate);
+  Piece<TO> there;
+  there.zero();
+  if constexpr (kAdd) there.load(grad + (int64_t)id * d + c);
+  put_row<TO, kAdd>(grad + (int64_t)id * d + c, sum, scale, there);
 }
 
 // ---------------------------------------------------------------- host side
@@ -338,11 +470,14 @@ SortPlan sort_plan(const EmbedArgs& a) {
   SortPlan p;
   p.passes = (bits + 8) / 9;
   p.bits = (bits + p.passes - 1) / p.passes;
-  p.tiles = (a.N + kSortTile - 1) / kSortTile;
+  p.tiles = (a.N + kSortBlock - 1) / kSortBlock;
   return p;
 }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-int64_t pieces_of(const EmbedArgs& a) { return (a.N + kPiece - 1) / kPiece; }
+// Tokens of a piece: few tokens make more waves of shorter chains (64 tokens 13 us with
+// pieces of 8, 20 with 32; 4000 23 and 30), many tokens fewer sums that the join adds.
+int piece_of(const EmbedArgs& a) { return a.N <= kSmall ? 8 : kPiece; }
+int64_t pieces_of(const EmbedArgs& a) { return (a.N + piece_of(a) - 1) / piece_of(a); }
 
 // Workspace: two sets of keys and places, the digits' counts, the partial sums.
 struct GradPlan {
@@ -407,38 +542,67 @@ hipError_t launch_embed_backward(const EmbedArgs& a, const void* ids, const void
   const auto u32 = [&](size_t off) { return reinterpret_cast<uint32_t*>(base + off); };
   uint32_t *hist = u32(p.hist), *total = u32(p.total);
   const int bins = 1 << sp.bits;
+  // The first rows are zeroed whole beside the sort, as many as its launches have time for
+  // (some 4 us each, 16 MB); the launches behind it leave out those that have tokens.
+  const int64_t row = a.d * (int64_t)dtype_bytes(a.out_dt) / 16;
+  const int64_t share = std::min<int64_t>(((int64_t)1 << 20) / row,
+                                          a.V / (3 * sp.passes + 4));  // rows a launch
+  int64_t zeroed = a.accumulate ? a.V : 0;
+  const auto zeros = [&](int64_t own, int threads, unsigned* grid) {
+    const int64_t rows = std::min(share, a.V - zeroed);
+    Zeros z{static_cast<uint4*>(grad) + zeroed * row, rows * row, (int32_t)own};
+    zeroed += rows;
+    *grid = (unsigned)(own + std::min<int64_t>((z.n + threads - 1) / threads, (1 << 20) / threads));
+    return z;
+  };
+  unsigned grid;
   int cur = 0;
-  for (int i = 0; i < sp.passes; ++i) {
-    const int shift = i * sp.bits;
-    SortIn in{i ? nullptr : ids, u32(p.keys[cur ^ 1]), i ? u32(p.pos[cur ^ 1]) : nullptr,
-              a.wide_ids, a.N, a.V};
-    embed_hist_kernel<<<dim3((unsigned)sp.tiles), kSortBlock, 0, s>>>(in, shift, bins, sp.tiles,
-                                                                      hist);
-    embed_scan_kernel<<<dim3((unsigned)bins), kBlock, 0, s>>>(hist, sp.tiles, total);
-    embed_scatter_kernel<<<dim3((unsigned)sp.tiles), kSortBlock, 0, s>>>(
-        in, shift, sp.bits, sp.tiles, hist, total, u32(p.keys[cur]), u32(p.pos[cur]));
-    cur ^= 1;
+  if (a.N <= kSmall) {
+    const SortIn in{ids, nullptr, nullptr, a.wide_ids, a.N, a.V};
+    const Zeros z = zeros(1, kSortBlock, &grid);
+    embed_sort_kernel<<<dim3(grid), kSortBlock, 0, s>>>(in, sp.passes, sp.bits, u32(p.keys[0]),
+                                                        u32(p.pos[0]), z);
+    cur = 1;
+  } else {
+    for (int i = 0; i < sp.passes; ++i) {
+      const int shift = i * sp.bits;
+      const SortIn in{i ? nullptr : ids, u32(p.keys[cur ^ 1]), i ? u32(p.pos[cur ^ 1]) : nullptr,
+                      a.wide_ids, a.N, a.V};
+      Zeros z = zeros(sp.tiles, kSortBlock, &grid);
+      embed_hist_kernel<<<dim3(grid), kSortBlock, 0, s>>>(in, shift, bins, sp.tiles, hist, z);
+      z = zeros(bins, kBlock, &grid);
+      embed_scan_kernel<<<dim3(grid), kBlock, 0, s>>>(hist, sp.tiles, total, z);
+      z = zeros(sp.tiles, kSortBlock, &grid);
+      embed_scatter_kernel<<<dim3(grid), kSortBlock, 0, s>>>(in, shift, sp.bits, sp.tiles, hist,
+                                                             total, u32(p.keys[cur]), u32(p.pos[cur]),
+                                                             z);
+      cur ^= 1;
+    }
   }
   const uint32_t *keys = u32(p.keys[cur ^ 1]), *pos = u32(p.pos[cur ^ 1]);
   float* part = reinterpret_cast<float*>(base + p.part);
-  return with_types(a, [&](auto t, auto to) {
+  const auto go = [&](auto t, auto to, auto add) {
     using T = decltype(t);
     using TO = decltype(to);
-    if (!a.accumulate) {
-      const int64_t n = a.V * a.d * (int64_t)sizeof(TO) / 16;
-      embed_zero_kernel<<<dim3((unsigned)std::min<int64_t>((n + kBlock - 1) / kBlock, 4096)),
-                          kBlock, 0, s>>>(static_cast<uint4*>(grad), n);
-    }
+    constexpr bool kAdd = decltype(add)::value;
     const int col_parts = (int)((a.d + kWaveCols - 1) / kWaveCols);
     const int64_t units = pieces_of(a) * col_parts;
     // units of 64 threads: fewer than 2^32 threads a launch (checked by the caller)
-    embed_sum_kernel<T, TO><<<dim3((unsigned)((units + 3) / 4)), kBlock, 0, s>>>(
+    const int64_t late = std::min(3 * share, a.V - zeroed), zero1 = a.V - late;
+    const int64_t all = units + (zero1 - zeroed + kZeroRows - 1) / kZeroRows;
+    embed_sum_kernel<T, TO, kAdd><<<dim3((unsigned)((all + 3) / 4)), kBlock, 0, s>>>(
         keys, pos, static_cast<const T*>(dout), static_cast<TO*>(grad), part, a.N, a.V, a.d,
-        a.scale, a.accumulate, units, col_parts);
-    embed_join_kernel<TO><<<dim3((unsigned)pieces_of(a), (unsigned)((a.d + 255) / 256)), kBlock, 0,
-                            s>>>(keys, part, static_cast<TO*>(grad), a.N, a.V, a.d, a.scale,
-                                 a.accumulate);
+        a.scale, piece_of(a), units, col_parts, zeroed, zero1);
+    const unsigned pieces = (unsigned)pieces_of(a), cols = (unsigned)((a.d + 255) / 256);
+    const int64_t waves = (late + kZeroRows - 1) / kZeroRows;
+    const unsigned extra = (unsigned)((waves + 4 * cols - 1) / (4 * cols));
+    embed_join_kernel<TO, kAdd><<<dim3(pieces + extra, cols), kBlock, 0, s>>>(
+        keys, part, static_cast<TO*>(grad), a.N, a.V, a.d, a.scale, piece_of(a),
+        pieces, zero1);
     return hipGetLastError();
+  };
+  return with_types(a, [&](auto t, auto to) {
+    return a.accumulate ? go(t, to, std::true_type{}) : go(t, to, std::false_type{});
   });
 }
 
