@@ -103,86 +103,99 @@ __global__ __launch_bounds__(kBlock) void act8_load_kernel(const int8_t* __restr
 // [64 tokens] bf16 (128-byte rows: a k-tile of the mainloop), zeros behind the last token.
 constexpr int kTokens = kRowBytes / 2;
 
-// A lane takes 4 columns of 8 tokens: load(first token, first column, tokens that are
-// there), then out(place of a column's 8 tokens, column).  The 8 lanes that share columns
-// are neighbours, so that they write whole 128-byte rows; a workgroup has 128 columns.
-template <class Load, class Out>
-__device__ __forceinline__ void to_blocks(int64_t rows, int64_t n, Load&& load, Out&& out) {
-  const int64_t block = blockIdx.x, c0 = blockIdx.y * (int64_t)128 + 4 * (threadIdx.x >> 3);
-  const int oct = threadIdx.x & 7;
-  if (c0 >= n) return;
-  const int64_t t0 = block * kTokens + 8 * oct;
-  load(t0, c0, (int)max<int64_t>(0, min<int64_t>(8, rows - t0)));
-#pragma unroll
-  for (int c = 0; c < 4; ++c) out((block * n + c0 + c) * kTokens + 8 * oct, c);
-}
+// A lane takes 4 columns (c0 ..) of 8 tokens (t0 ..), of which `live` are there.  The 8
+// lanes that share columns are neighbours, so that they write whole 128-byte rows.
+struct BlockLane {
+  int64_t t0, c0, at;  // at: place of the first column's 8 tokens
+  int live;
+  bool any;
+  __device__ __forceinline__ BlockLane(int64_t columns, int64_t rows, int64_t n) {
+    const int oct = threadIdx.x & 7;
+    c0 = columns * 128 + 4 * (threadIdx.x >> 3);
+    t0 = blockIdx.x * (int64_t)kTokens + 8 * oct;
+    at = (blockIdx.x * n + c0) * kTokens + 8 * oct;
+    live = (int)max<int64_t>(0, min<int64_t>(8, rows - t0));
+    any = c0 < n;
+  }
+};
 
-__global__ __launch_bounds__(kBlock) void act8_blocks_kernel(const int8_t* __restrict__ codes,
-                                                             const uint8_t* __restrict__ exps,
-                                                             uint16_t* __restrict__ x, int64_t rows,
-                                                             int64_t d) {
+// 128 columns of x, out [..][d].
+__device__ __forceinline__ void decode_block(const int8_t* __restrict__ codes,
+                                             const uint8_t* __restrict__ exps,
+                                             uint16_t* __restrict__ out, int64_t rows, int64_t d,
+                                             int64_t columns) {
+  const BlockLane l(columns, rows, d);
+  if (!l.any) return;
+  const int64_t groups = (d + kAct8Group - 1) / kAct8Group;
+  uint32_t w[8], e[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    w[t] = e[t] = 0;
+    if (t < l.live) {
+      w[t] = *reinterpret_cast<const uint32_t*>(codes + (l.t0 + t) * d + l.c0);
+      e[t] = exps[(l.t0 + t) * groups + l.c0 / kAct8Group];
+    }
+  }
   float v[8][4];
-  to_blocks(
-      rows, d,
-      [&](int64_t t0, int64_t c0, int live) {
-        const int64_t groups = (d + kAct8Group - 1) / kAct8Group;
-        uint32_t w[8], e[8];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          w[t] = e[t] = 0;
-          if (t < live) {
-            w[t] = *reinterpret_cast<const uint32_t*>(codes + (t0 + t) * d + c0);
-            e[t] = exps[(t0 + t) * groups + c0 / kAct8Group];
-          }
-        }
+  for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+    for (int c = 0; c < 4; ++c)
+      v[t][c] = (float)((int32_t)(w[t] << (24 - 8 * c)) >> 24) * __uint_as_float(e[t] << 23);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            v[t][c] = (float)((int32_t)(w[t] << (24 - 8 * c)) >> 24) * __uint_as_float(e[t] << 23);
-      },
-      [&](int64_t at, int c) {
-        *reinterpret_cast<uint4*>(x + at) =
-            make_uint4(pack_bf16x2(v[0][c], v[1][c]), pack_bf16x2(v[2][c], v[3][c]),
-                       pack_bf16x2(v[4][c], v[5][c]), pack_bf16x2(v[6][c], v[7][c]));
-      });
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(out + l.at + c * kTokens) =
+        make_uint4(pack_bf16x2(v[0][c], v[1][c]), pack_bf16x2(v[2][c], v[3][c]),
+                   pack_bf16x2(v[4][c], v[5][c]), pack_bf16x2(v[6][c], v[7][c]));
 }
 
-// An fp32 dy as three bf16 terms whose sum it is: the leading 8 bits of what is left,
-// three times; an infinity or NaN goes into the first alone.  Terms `part` values apart.
-__global__ __launch_bounds__(kBlock) void act8_terms_kernel(const float* __restrict__ dy,
-                                                            int64_t dys, uint16_t* __restrict__ out,
-                                                            int64_t part, int64_t rows, int64_t n) {
+// 128 columns of an fp32 dy as three bf16 terms whose sum it is: the leading 8 bits of
+// what is left, three times; an infinity or NaN goes into the first alone.  Terms `part`
+// values apart.
+__device__ __forceinline__ void split_block(const float* __restrict__ dy, int64_t dys,
+                                            uint16_t* __restrict__ out, int64_t part, int64_t rows,
+                                            int64_t n, int64_t columns) {
+  const BlockLane l(columns, rows, n);
+  if (!l.any) return;
   float v[8][4];
-  to_blocks(
-      rows, n,
-      [&](int64_t t0, int64_t c0, int live) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          float4 f = make_float4(0, 0, 0, 0);
-          if (t < live) f = *reinterpret_cast<const float4*>(dy + (t0 + t) * dys + c0);
-          v[t][0] = f.x, v[t][1] = f.y, v[t][2] = f.z, v[t][3] = f.w;
-        }
-      },
-      [&](int64_t at, int c) {
+  for (int t = 0; t < 8; ++t) {
+    float4 f = make_float4(0, 0, 0, 0);
+    if (t < l.live) f = *reinterpret_cast<const float4*>(dy + (l.t0 + t) * dys + l.c0);
+    v[t][0] = f.x, v[t][1] = f.y, v[t][2] = f.z, v[t][3] = f.w;
+  }
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          uint32_t top[8];
+  for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const uint32_t u = __float_as_uint(v[t][c]), m = u & 0x7fffffffu;
-            // a NaN whose upper bits are an infinity's stays one
-            top[t] = m > 0x7f800000u ? 0x7fc00000u : u & 0xffff0000u;
-            v[t][c] = m >= 0x7f800000u ? 0.0f : v[t][c] - __uint_as_float(top[t]);
-          }
-          *reinterpret_cast<uint4*>(out + k * part + at) =
-              make_uint4(top[0] >> 16 | top[1], top[2] >> 16 | top[3], top[4] >> 16 | top[5],
-                         top[6] >> 16 | top[7]);
-        }
-      });
+    for (int k = 0; k < 3; ++k) {
+      uint32_t top[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const uint32_t u = __float_as_uint(v[t][c]), m = u & 0x7fffffffu;
+        // a NaN whose upper bits are an infinity's stays one
+        top[t] = m > 0x7f800000u ? 0x7fc00000u : u & 0xffff0000u;
+        v[t][c] = m >= 0x7f800000u ? 0.0f : v[t][c] - __uint_as_float(top[t]);
+      }
+      *reinterpret_cast<uint4*>(out + k * part + l.at + c * kTokens) =
+          make_uint4(top[0] >> 16 | top[1], top[2] >> 16 | top[3], top[4] >> 16 | top[5],
+                     top[6] >> 16 | top[7]);
+    }
 }
 
-using WTile = TileShape<256, 256, 2, 4>;
+// Blocks of x (the first x_columns of the grid's rows), and with dy of its terms.
+__global__ __launch_bounds__(kBlock) void act8_operands_kernel(
+    const int8_t* __restrict__ codes, const uint8_t* __restrict__ exps, uint16_t* __restrict__ x,
+    int64_t rows, int64_t d, unsigned x_columns, const float* __restrict__ dy, int64_t dys,
+    uint16_t* __restrict__ terms, int64_t part, int64_t n) {
+  if (blockIdx.y < x_columns)
+    decode_block(codes, exps, x, rows, d, blockIdx.y);
+  else
+    split_block(dy, dys, terms, part, rows, n, blockIdx.y - x_columns);
+}
+
+// Tiles of the gradient: a workgroup a CU, or two with a quarter of it each.
+using WideTile = TileShape<256, 256, 2, 4>;
+using SmallTile = TileShape<128, 128, 2, 2>;
 constexpr int kEpiCols = 64;
 constexpr int kEpiStride = kEpiCols + 8;  // floats per staged row
 
@@ -212,32 +225,56 @@ struct PartLoader {
     for (int q = 0; q < kPer; ++q) l.issue_one(r, stage, q);
   }
 };
-using BlockLoader = DirectLoader<256, WTile::kWaves>;
-using RowLoader = KMajorLoader<uint16_t, WTile::kWaves>;
-// 256 columns from n0 of an operand of N columns in blocks.
-__device__ __forceinline__ BlockLoader block_loader(const uint16_t* p, int64_t N, int64_t n0,
-                                                    int64_t k0) {
-  BlockLoader l;
+// kCols columns from n0 of an operand of N columns in blocks, k-tiles from k0.
+template <class S, int kCols>
+__device__ __forceinline__ DirectLoader<kCols, S::kWaves> block_loader(const uint16_t* p, int64_t N,
+                                                                       int64_t n0, int64_t k0) {
+  DirectLoader<kCols, S::kWaves> l;
   l.init(p + (k0 * N + n0) * kTokens, kRowBytes, N * kRowBytes, (N - n0) * kRowBytes, 0);
   return l;
 }
-// The same of rows [rows][ld] of N columns.
-__device__ __forceinline__ RowLoader row_loader(const uint16_t* p, int64_t ld, int64_t rows,
-                                                int64_t N, int64_t n0, int64_t k0) {
-  RowLoader l;
-  l.init(p + k0 * kTokens * ld + n0, kRowBytes, ld * 2, kTokens * ld * 2,
-         ((rows - k0 * kTokens - 1) * ld + N - n0) * 2);
-  return l;
-}
+// S::BN columns from n0 of rows [rows][ld] of N columns: stage row 64 (c / 64) + t holds
+// token t of the k-tile, columns 64 (c / 64) .. (KMajorLoader of gemm_core.h, for any
+// number of columns).
+template <class S>
+struct RowLoader {
+  static constexpr int kPer = S::BN / S::kWaves / 8;
+  const char* base;
+  int64_t kt_stride, valid_bytes;
+  uint32_t voff[kPer];
+  uint32_t lds_row0;
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld, int64_t rows, int64_t N,
+                                       int64_t n0, int64_t k0) {
+    base = reinterpret_cast<const char*>(p + k0 * kTokens * ld + n0);
+    kt_stride = kTokens * ld * 2;
+    valid_bytes = ((rows - k0 * kTokens - 1) * ld + N - n0) * 2;
+    const int lane = threadIdx.x & 63;
+    lds_row0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (S::BN / S::kWaves);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int row = (int)lds_row0 + 8 * q + (lane >> 3);
+      const int c = (lane & 7) ^ lds_swz_tr(row);
+      voff[q] = (uint32_t)((row / kTokens) * kRowBytes + (row % kTokens) * ld * 2 + c * 16);
+    }
+  }
+  __device__ __forceinline__ rsrc_t rsrc(int64_t kt, bool live = true) const {
+    return make_rsrc(base + kt * kt_stride, live ? valid_bytes - kt * kt_stride : 0);
+  }
+  __device__ __forceinline__ void issue_one(rsrc_t r, lds_char* stage, int q) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r, (__attribute__((address_space(3))) void*)(stage + (lds_row0 + 8 * q) * kRowBytes), 16,
+        voff[q], 0, 0, 0);
+  }
+};
 
 // A k-tile's products with x's fragments read as rows and dy's transposed from token rows
 // (kRows), or both as rows.  Reads for the next 16 tokens are spread between the matrix
 // instructions, hook(q) follows instruction q.  The transposing reads are inline assembly,
 // each block with its wait: the compiler lets the builtin wait for every direct-to-LDS load
-// in flight, also those into the other stage (2560 x 7680 at 32K tokens: 1438 us with it, 1118 without).
-template <bool kRows>
+// in flight, also those into the other stage (2560 x 7680 at 32K tokens: 1438 us with it,
+// 1118 without).
+template <class S, bool kRows>
 struct GradMma {
-  using S = WTile;
   using Plain = Mma16<S, false, false>;
   static constexpr int kSteps = Plain::kSteps;
   // A lane's addresses in a stage's first 16 token rows: [columns 32 apart][tokens 4 apart]
@@ -278,24 +315,25 @@ struct GradMma {
     if constexpr (!kRows) {
       Plain::ktile_spread(acc, sA, sB, p, hook);
     } else {
-      static_assert(S::MB == 4 && S::NB == 2, "the reads below");
-      bf16x8_t a[2][4], b[2][2];
+      static_assert(S::NB == 2, "the reads below");
+      constexpr int kPerStep = 2 * S::MB;
+      bf16x8_t a[2][S::MB], b[2][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[0][i] = Plain::read_a(sA, p, i, 0);
+      for (int i = 0; i < S::MB; ++i) a[0][i] = Plain::read_a(sA, p, i, 0);
       read_rows(b[0], sB, 0);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
+        for (int m = 0; m < kPerStep; ++m) {
           const int i = m >> 1, j = m & 1;
           acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[s & 1][i], b[s & 1][j],
                                                                 acc.v[i][j], 0, 0, 0);
           if (s + 1 < kSteps) {
-            if (m < 4) a[(s + 1) & 1][m] = Plain::read_a(sA, p, m, s + 1);
-            if (m == 5) read_rows(b[(s + 1) & 1], sB, s + 1);
+            if (m < S::MB) a[(s + 1) & 1][m] = Plain::read_a(sA, p, m, s + 1);
+            if (m == kPerStep - S::MB + S::MB / 4) read_rows(b[(s + 1) & 1], sB, s + 1);
           }
-          hook(8 * s + m);
+          hook(kPerStep * s + m);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -305,10 +343,9 @@ struct GradMma {
 
 // The mainloop of gemm_core.h on these fragments: k-tile kt + 1's loads one after each of
 // kt's first matrix instructions.
-template <class Mma, class LA, class LB>
-__device__ __forceinline__ void grad_mainloop(Accum<WTile>& acc, LA& la, LB& lb, int64_t nk,
+template <class Mma, class S, class LA, class LB>
+__device__ __forceinline__ void grad_mainloop(Accum<S>& acc, LA& la, LB& lb, int64_t nk,
                                               lds_char* smem, const LanePos& p) {
-  using S = WTile;
   constexpr int kLoads = LA::kPer + LB::kPer;
   static_assert(kLoads <= Mma::kSteps * S::MB * S::NB, "the loads fit the k-tile's MFMAs");
   Mma mma;
@@ -335,7 +372,7 @@ __device__ __forceinline__ void grad_mainloop(Accum<WTile>& acc, LA& la, LB& lb,
 
 // Tiles of the gradient; the first `whole` by one workgroup each, the others by
 // `slices` workgroups, `slice` k-tiles each, that leave their sums in `part`
-// [tile][slice][256][256].
+// [tile][slice][tile's rows and columns].
 struct GradArgs {
   const uint16_t* x;   // blocks of [M]
   const uint16_t* dy;  // rows dys apart (bf16), or terms in blocks of [N]
@@ -348,10 +385,9 @@ struct GradArgs {
   bool accumulate;
 };
 
-template <typename TO, bool kTerms>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void
+template <typename TO, class S, bool kTerms>
+__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 act8_grad_kernel(GradArgs g) {
-  using S = WTile;
   static_assert(S::kLdsBytes >= S::BM * kEpiStride * 4, "epilogue stage fits the pipeline's LDS");
   constexpr int kParts = kTerms ? 3 : 1;
   __shared__ __attribute__((aligned(16))) char smem_raw[S::kLdsBytes];
@@ -372,13 +408,16 @@ act8_grad_kernel(GradArgs g) {
   Accum<S> acc;
   acc.zero();
   const LanePos p = lane_pos<S>();
-  PartLoader<BlockLoader, kParts> la{block_loader(g.x, g.M, m0, k0), n, 0};
+  const auto lx = block_loader<S, S::BM>(g.x, g.M, m0, k0);
+  PartLoader<DirectLoader<S::BM, S::kWaves>, kParts> la{lx, n, 0};
   if constexpr (kTerms) {
-    PartLoader<BlockLoader, kParts> lb{block_loader(g.dy, g.N, n0, k0), n, g.dy_part * 2};
-    grad_mainloop<GradMma<false>>(acc, la, lb, n * kParts, smem, p);
+    const auto ly = block_loader<S, S::BN>(g.dy, g.N, n0, k0);
+    PartLoader<DirectLoader<S::BN, S::kWaves>, kParts> lb{ly, n, g.dy_part * 2};
+    grad_mainloop<GradMma<S, false>>(acc, la, lb, n * kParts, smem, p);
   } else {
-    PartLoader<RowLoader, kParts> lb{row_loader(g.dy, g.dys, g.rows, g.N, n0, k0), n, 0};
-    grad_mainloop<GradMma<true>>(acc, la, lb, n, smem, p);
+    PartLoader<RowLoader<S>, 1> lb;
+    lb.l.init(g.dy, g.dys, g.rows, g.N, n0, k0);
+    grad_mainloop<GradMma<S, true>>(acc, la, lb, n, smem, p);
   }
   float* const part =
       slice < 0 ? nullptr
@@ -423,9 +462,8 @@ act8_grad_kernel(GradArgs g) {
 }
 
 // The tiles that came in slices, added in order: 8 rows of a tile a workgroup.
-template <typename TO>
+template <typename TO, class S>
 __global__ __launch_bounds__(kBlock) void act8_sum_kernel(GradArgs g) {
-  using S = WTile;
   constexpr int kEach = S::BM * S::BN / (8 * kBlock);  // workgroups of a tile
   const int tiles_m = (int)((g.M + S::BM - 1) / S::BM), tiles_n = (int)((g.N + S::BN - 1) / S::BN);
   const int tile = blockIdx.x / kEach;
@@ -484,50 +522,88 @@ hipError_t in_launches(int64_t rows, int64_t per, F&& f) {
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 int64_t ktiles_of(const Act8Grad& g) { return (g.rows + kTokens - 1) / kTokens; }
-int64_t grad_tiles(const Act8Grad& g) {
-  return ((g.d_in + 255) / 256) * ((g.d_out + 255) / 256);
+int64_t grad_tiles(const Act8Grad& g, int64_t side) {
+  return ((g.d_in + side - 1) / side) * ((g.d_out + side - 1) / side);
 }
 
-// A workgroup owns a CU: tiles that fill whole rounds of 256 CUs are one workgroup's
-// each, in step with one another along the tokens (they share their operands in L2); what
-// is left over is cut along the tokens, so that the last round is short.  Some 1.6 us for
-// 64 tokens of a tile and 10 around it; a slice more costs a write and a read of its
-// 256 KB of sums.
-struct Slices {
-  int whole, slices;
-  int64_t slice;  // k-tiles of a slice
+// How the gradient is cut: tiles of 256 or 128, `whole` of them a workgroup's each, the
+// others in `slices` of `slice` k-tiles.
+struct Cut {
+  int side, whole, slices;
+  int64_t slice;
 };
-Slices slices_of(const Act8Grad& g) {
-  constexpr int kCus = 256;
-  const int64_t tiles = grad_tiles(g), n = ktiles_of(g);
-  const double us = g.dt == Dtype::F32 ? 3 * 1.6 : 1.6;
-  const int rest = (int)(tiles % kCus);
-  Slices best{(int)(tiles - rest), 1, n};
-  double least = 0;
-  for (int64_t s = 1; s <= 64 && (s == 1 || n >= 2 * s); ++s) {
-    const int64_t slice = (n + s - 1) / s, used = (n + slice - 1) / slice;
-    const double rounds = (double)((rest * used + kCus - 1) / kCus);
-    const double t = rounds * ((double)slice * us + 10.0) +
-                     (used > 1 ? (double)(rest * used) * 0.5e6 / 4e6 + 5.0 : 0.0);
-    if (s == 1 || t < least) best.slices = (int)used, best.slice = slice, least = t;
+
+// The cut that takes the least time by what was measured of its parts: tiles that fill
+// whole rounds of the chip (256 workgroups of wide tiles, 512 of small ones) run whole, in
+// step with one another along the tokens, so that they share their operands in L2; what is
+// left over is cut along the tokens as well, so that the last round is short.  A slice
+// more costs a write and a read of its sums.  Calls in us with wide / small tiles (bf16):
+//   1 x 1024 x 1536 19 / 13,  200 x 2560 x 4096 30 / 24,  1000 x 1024 x 1536 37 / 21,
+//   2048 x 2560 x 2560 66 / 44,  3000 x 5120 x 7680 255 / 254,  8192 x 2560 x 7680 304 / 322,
+//   32768 x 1024 x 4096 263 / 334,  32768 x 2560 x 7680 1106 / 1412
+Cut cut_of(const Act8Grad& g) {
+  const int64_t n = ktiles_of(g);
+  const double terms = g.dt == Dtype::F32 ? 3.0 : 1.0;
+  // whether the operands stay in the 256 MB last-level cache
+  const bool cached = (double)g.rows * (g.d_in + terms * g.d_out) * 2.0 < 256e6;
+  Cut best{};
+  double least = -1;
+  for (const int side : {256, 128}) {
+    const int64_t round = side == 256 ? 256 : 512, tiles = grad_tiles(g, side);
+    // us of a k-tile (small ones take twice the operands for their work: more where those
+    // come from memory) and around them, MB of a tile's sums
+    const double ktile = terms * (side == 256 ? 1.6 : cached ? 0.9 : 1.1);
+    const double around = side == 256 ? 14.0 : 5.0;
+    const double sums = (double)side * side * 8e-6;
+    const int64_t rest = tiles % round;
+    const double before = (double)(tiles / round) * ((double)n * ktile + around);
+    for (int64_t s = 1; s <= 64 && (s == 1 || (rest && n >= 2 * s)); ++s) {
+      const int64_t slice = (n + s - 1) / s, used = (n + slice - 1) / slice;
+      const double rounds = (double)((rest * used + round - 1) / round);
+      const double us = before + rounds * ((double)slice * ktile + around) +
+                        (used > 1 ? (double)(rest * used) * sums / 4.0 + 4.0 : 0.0);
+      if (least >= 0 && us >= least) continue;
+      least = us;
+      best = Cut{side, (int)(used == 1 ? tiles : tiles - rest), (int)used, slice};
+    }
   }
-  if (best.slices == 1) best.whole = (int)tiles;
   return best;
 }
 
 // Workspace: x and dy's terms in blocks, the slices' sums.
 struct GradPlan {
   size_t dy, part, bytes;
-  Slices s;
+  Cut cut;
 };
 GradPlan grad_plan(const Act8Grad& g) {
   GradPlan p;
-  p.s = slices_of(g);
+  p.cut = cut_of(g);
   const size_t tokens = (size_t)ktiles_of(g) * kTokens;
   p.dy = align256(tokens * g.d_in * 2);
   p.part = p.dy + (g.dt == Dtype::F32 ? align256(3 * tokens * g.d_out * 2) : 0);
-  p.bytes = p.part + (size_t)(grad_tiles(g) - p.s.whole) * p.s.slices * (256 * 256 * sizeof(float));
+  p.bytes = p.part + (size_t)(grad_tiles(g, p.cut.side) - p.cut.whole) * p.cut.slices *
+                         ((size_t)p.cut.side * p.cut.side * sizeof(float));
   return p;
+}
+
+template <class S>
+hipError_t launch_products(const Act8Grad& g, const GradArgs& a, hipStream_t s) {
+  const int64_t rest = grad_tiles(g, S::BM) - a.whole;
+  const dim3 grid((unsigned)(a.whole + rest * a.slices));
+  const dim3 sums((unsigned)(rest * (S::BM * S::BN / (8 * kBlock))));
+  if (g.dt == Dtype::F32)
+    act8_grad_kernel<float, S, true><<<grid, S::kThreads, 0, s>>>(a);
+  else if (g.grad_dt == Dtype::F32)
+    act8_grad_kernel<float, S, false><<<grid, S::kThreads, 0, s>>>(a);
+  else
+    act8_grad_kernel<uint16_t, S, false><<<grid, S::kThreads, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || rest == 0) return e;
+  if (g.grad_dt == Dtype::F32)
+    act8_sum_kernel<float, S><<<sums, kBlock, 0, s>>>(a);
+  else
+    act8_sum_kernel<uint16_t, S><<<sums, kBlock, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -567,48 +643,29 @@ hipError_t launch_act8_weight_grad(const Act8Grad& g, const int8_t* codes, const
   const int64_t n = ktiles_of(g);
   GradArgs a{};
   a.x = reinterpret_cast<uint16_t*>(base), a.rows = g.rows, a.M = g.d_in, a.N = g.d_out;
-  a.ktiles = n, a.slice = p.s.slice, a.whole = p.s.whole, a.slices = p.s.slices;
+  a.ktiles = n, a.slice = p.cut.slice, a.whole = p.cut.whole, a.slices = p.cut.slices;
   a.part = reinterpret_cast<float*>(base + p.part);
   a.out = grad, a.accumulate = g.accumulate;
-  uint16_t* const x = reinterpret_cast<uint16_t*>(base);
-  const int64_t groups = (g.d_in + kAct8Group - 1) / kAct8Group;
-  const auto columns = [](int64_t n) { return (unsigned)((n + 127) / 128); };
-  hipError_t e = in_launches(n, 1, [&](int64_t at, int64_t, dim3 grid) {
-    grid.y = columns(g.d_in);
-    const int64_t t = at * kTokens;
-    act8_blocks_kernel<<<grid, kBlock, 0, s>>>(codes + t * g.d_in, exps + t * groups,
-                                               x + t * g.d_in, g.rows - t, g.d_in);
-  });
-  if (e != hipSuccess) return e;
-  if (g.dt == Dtype::F32) {
-    uint16_t* const terms = reinterpret_cast<uint16_t*>(base + p.dy);
+  uint16_t *const x = reinterpret_cast<uint16_t*>(base), *terms = nullptr;
+  const bool split = g.dt == Dtype::F32;
+  if (split) {
+    terms = reinterpret_cast<uint16_t*>(base + p.dy);
     a.dy = terms, a.dy_part = n * kTokens * g.d_out;
-    e = in_launches(n, 1, [&](int64_t at, int64_t, dim3 grid) {
-      grid.y = columns(g.d_out);
-      const int64_t t = at * kTokens;
-      act8_terms_kernel<<<grid, kBlock, 0, s>>>(static_cast<const float*>(dy) + t * g.dys, g.dys,
-                                                terms + t * g.d_out, a.dy_part, g.rows - t,
-                                                g.d_out);
-    });
-    if (e != hipSuccess) return e;
   } else {
     a.dy = static_cast<const uint16_t*>(dy), a.dys = g.dys;
   }
-  const int64_t rest = grad_tiles(g) - a.whole;
-  const dim3 grid((unsigned)(a.whole + rest * a.slices)), sums((unsigned)(rest * 32));
-  if (g.dt == Dtype::F32)
-    act8_grad_kernel<float, true><<<grid, 512, 0, s>>>(a);
-  else if (g.grad_dt == Dtype::F32)
-    act8_grad_kernel<float, false><<<grid, 512, 0, s>>>(a);
-  else
-    act8_grad_kernel<uint16_t, false><<<grid, 512, 0, s>>>(a);
-  e = hipGetLastError();
-  if (e != hipSuccess || rest == 0) return e;
-  if (g.grad_dt == Dtype::F32)
-    act8_sum_kernel<float><<<sums, kBlock, 0, s>>>(a);
-  else
-    act8_sum_kernel<uint16_t><<<sums, kBlock, 0, s>>>(a);
-  return hipGetLastError();
+  const int64_t groups = (g.d_in + kAct8Group - 1) / kAct8Group;
+  const unsigned x_columns = (unsigned)((g.d_in + 127) / 128);
+  const hipError_t e = in_launches(n, 1, [&](int64_t at, int64_t, dim3 grid) {
+    grid.y = x_columns + (split ? (unsigned)((g.d_out + 127) / 128) : 0);
+    const int64_t t = at * kTokens;
+    act8_operands_kernel<<<grid, kBlock, 0, s>>>(
+        codes + t * g.d_in, exps + t * groups, x + t * g.d_in, g.rows - t, g.d_in, x_columns,
+        split ? static_cast<const float*>(dy) + t * g.dys : nullptr, g.dys,
+        split ? terms + t * g.d_out : nullptr, a.dy_part, g.d_out);
+  });
+  if (e != hipSuccess) return e;
+  return p.cut.side == 256 ? launch_products<WideTile>(g, a, s) : launch_products<SmallTile>(g, a, s);
 }
 
 }  // namespace ttt

@@ -303,7 +303,7 @@ def gatedrec_forward(x, decay_gate, input_gate, rate, state=None, state_out=None
     desc, need = _gatedrec_plan(x.shape, x.stride(), decay_gate.stride(), input_gate.stride(),
                                 None, x.dtype, False)
     B, T, d = x.shape
-    h = torch.empty((B, T, d), dtype=x.dtype, device=x.device)
+    h = torch.empty_like(x, memory_format=torch.contiguous_format)
     if state_out is None:
         state_out = torch.empty((B, d), dtype=torch.float32, device=x.device)
     saved = torch.empty((B, -(-T // GATEDREC_TILE), d), dtype=torch.float32,
@@ -332,7 +332,7 @@ def gatedrec_backward(x, decay_gate, input_gate, rate, dh, saved, dstate_out=Non
     _same_device(x, dh, saved)
     desc, need = _gatedrec_plan(x.shape, x.stride(), decay_gate.stride(), input_gate.stride(),
                                 dh.stride(), x.dtype, True)
-    new = lambda: torch.empty((B, T, d), dtype=x.dtype, device=x.device)  # noqa: E731
+    new = lambda: torch.empty_like(x, memory_format=torch.contiguous_format)  # noqa: E731
     g = {"x": new(), "decay_gate": new(), "input_gate": new(),
          "rate": torch.empty(d, dtype=torch.float32, device=x.device),
          "state": torch.empty((B, d), dtype=torch.float32, device=x.device)}
@@ -409,7 +409,7 @@ def act8_store(x, stream=None):
         raise ValueError("x must be bfloat16 or float32 rows")
     rows, d, xs = _rows(x)
     desc = _act8_plan(rows, d, x.dtype, d if rows == 1 else xs)
-    codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    codes = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
     exps = torch.empty((*x.shape[:-1], -(-d // ACT8_GROUP)), dtype=torch.uint8, device=x.device)
     ttt_act8_store(desc, x, codes, exps)
     return codes, exps
@@ -424,7 +424,7 @@ def act8_load(codes, exps, dtype=torch.bfloat16, stream=None):
     if dtype not in _FLOATS:
         raise ValueError("dtype must be bfloat16 or float32")
     d = codes.shape[-1]
-    x = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    x = torch.empty_like(codes, dtype=dtype)
     ttt_act8_load(_act8_plan(codes.numel() // d, d, dtype, d), codes, exps, x)
     return x
 
