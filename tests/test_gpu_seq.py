@@ -95,7 +95,8 @@ def test_embed_forward_shapes_and_values():
 # sort and many, one digit and two, columns of a wave and more
 EMBED_SHAPES = [(1, 1, 8), (3, 1, 64), (31, 5, 64), (32, 5, 128), (33, 2, 136), (64, 64, 200),
                 (500, 600, 520), (700, 3, 1000), (4096, 300, 64), (4097, 511, 72), (9000, 512, 64),
-                (9000, 40000, 72), (20000, 7, 40), (300, 131072, 64), (513, 50, 2560)]
+                (9000, 40000, 72), (20000, 7, 40), (300, 131072, 64), (513, 50, 2560),
+                (8192, 700, 24), (8193, 700, 24), (9000, 300000, 8), (700, 1 << 20, 8)]
 
 
 @pytest.mark.parametrize("dtype,gd", [(BF16, F32), (BF16, BF16), (F32, F32)])
@@ -411,7 +412,8 @@ def test_act8_values():
     tops = []
     for e in (-149, -140, -133, -132, -126, -119, -20, 0, 1, 100, 120, 121):
         for m in (126.5, 127.0, 127.00001, 127.5, 128.0, 64.0, 63.5, 1.0):
-            v = np.float32(m * 2.0 ** e)
+            with np.errstate(over="ignore"):
+                v = np.float32(m * 2.0 ** e)
             if np.isfinite(v):
                 tops.append(v)
     tops += [np.float32(0), np.finfo(np.float32).max, np.float32(2.0 ** -149)]
@@ -467,6 +469,36 @@ def test_act8_weight_grad(rows, d_in, d_out, dtype, gd):
         keep = f64(start)
         grad = seq.act8_weight_grad(codes, exps, dy, grad=start)
         assert grad is start and rel(f64(grad), want + keep) <= TOL_F32
+
+
+# wide tiles: whole ones and a rest in slices, slices alone; small tiles: whole ones, with a
+# rest in slices, and more than one round of them
+@pytest.mark.parametrize("rows,d_in,d_out,dtype,gd", [
+    (8229, 2600, 6664, BF16, F32), (8229, 2600, 6664, BF16, BF16), (8229, 2600, 6664, F32, F32),
+    (33001, 1032, 4104, BF16, F32), (17001, 1032, 4104, F32, F32), (130, 3000, 6000, BF16, F32),
+    (700, 2568, 3336, F32, F32), (4000, 4104, 2056, BF16, F32)])
+def test_act8_weight_grad_large(rows, d_in, d_out, dtype, gd):
+    say(rows, d_in, d_out, dtype, gd)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    codes, exps = seq.act8_store(torch.randn(rows, d_in, generator=g, device="cuda"))
+    wide = torch.randn(rows, d_out + 8, generator=g, device="cuda").to(dtype)
+    dy = wide[:, 8:]
+    x64 = seq.act8_load(codes, exps, F32).double()
+    want = x64.t().contiguous() @ dy.double()
+    got = seq.act8_weight_grad(codes, exps, dy, grad_dtype=gd)
+    # against the norm of each row and column too, so that no tile hides behind the others
+    off = got.double() - want
+    for dim in (0, 1):
+        e = float((off.norm(dim=dim) / want.norm(dim=dim)).max())
+        say("  %.2e" % e)
+        assert e <= TOL[gd]
+    assert torch.equal(seq.act8_weight_grad(codes, exps, dy, grad_dtype=gd), got)
+    if gd == F32:
+        start = torch.randn(d_in, d_out, generator=g, device="cuda") * rows ** 0.5
+        keep = start.double()
+        seq.act8_weight_grad(codes, exps, dy, grad=start)
+        assert float(((start.double() - keep - want).norm() / want.norm())) <= TOL_F32
 
 
 def test_act8_weight_grad_rows_of_more_dimensions():

@@ -6,11 +6,13 @@ import contextlib
 import ctypes
 import os
 import re
+import subprocess
 
 import numpy as np
 import pytest
 import torch
 
+from chunk_wise_weight_chunked_amd import build as hipbuild
 from chunk_wise_weight_chunked_amd import seq
 from chunk_wise_weight_chunked_amd import ttt_mlp as tm
 
@@ -430,3 +432,106 @@ def test_act8_reference():
     x[1, 3] = np.nan
     codes, exps = ref.act8(x)
     assert exps[1, 0] == 255 and np.isnan(ref.act8_value(codes, exps)[1, :32]).all()
+
+
+# ---------------------------------------------------- the waits of the compiled kernels
+
+
+def kernels_of(source, tmp_path):
+    """{name: lines} of the gfx950 code that build.py's own compiler and flags make."""
+    out = tmp_path / (source + ".s")
+    flags = [f for f in hipbuild.HIPCC_FLAGS if f != "-shared"]
+    cmd = [hipbuild.hipcc(), *flags, "--cuda-device-only", "-S",
+           os.path.join(hipbuild.CSRC, source), "-o", str(out)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    parts = re.split(r"^(?=_Z\w+:)", out.read_text(), flags=re.M)[1:]
+    return {p.split(":", 1)[0]: p.split(".Lfunc_end")[0].splitlines() for p in parts}
+
+
+@pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="hipcc not available")
+def test_no_load_into_lds_is_in_flight_at_a_barrier(tmp_path):
+    """The products fill LDS tiles by direct loads and let other waves read them after a barrier:
+    vmcnt(0) stands between a direct load and the next barrier, in the order of the code (whose
+    loops end with no load in flight); and every transposing read has its own wait behind it, in
+    the same block."""
+    found = barriers = reads = 0
+    for name, lines in kernels_of("act8.hip", tmp_path).items():
+        if not any(re.search(r"buffer_load\w* .*\blds$", x) for x in lines):
+            continue
+        found += 1
+        assert not any("scratch_" in x for x in lines), name  # nothing spilled either
+        flying, pending = False, 0
+        for x in lines:
+            if "ds_read_b64_tr_b16" in x:
+                pending += 1
+                reads += 1
+            elif pending and re.search(r"s_waitcnt.*lgkmcnt\(0\)", x):
+                pending = 0
+            elif pending:
+                assert "mfma" not in x and "s_barrier" not in x, (name, x)
+            if re.search(r"buffer_load\w* .*\blds$", x):
+                flying = True
+            elif re.search(r"s_waitcnt.*vmcnt\(0\)", x):
+                flying = False
+            elif "s_barrier" in x:
+                assert not flying, (name, x)
+                barriers += "s_barrier" in x
+        assert not flying, name
+    assert found == 6 and barriers >= 3 * found and reads >= 4 * 4, (found, barriers, reads)
+
+
+@pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="hipcc not available")
+def test_no_packed_arithmetic(tmp_path):
+    for source in ("embed.hip", "gatedrec.hip", "act8.hip"):
+        for name, lines in kernels_of(source, tmp_path).items():
+            assert not any(re.search(r"v_pk_(add|mul|fma)_f32", x) for x in lines), name
+
+
+# ------------------------------------------- the recurrence's links, on the CPU
+def test_the_state_found_does_not_depend_on_when_it_is_looked_for():
+    """state_before of gatedrec.hip, its steps in Python: whatever part of the tiles in front has
+    published its state, its map or nothing, what is found is the same number to the bit, or
+    nothing yet; and with every tile in front published something is found."""
+    rng = np.random.default_rng(7)
+    f32 = np.float32
+    kAhead = 8
+
+    def apply(dec, h, u):
+        near = np.signbit(dec)
+        return f32(f32(f32(np.float64(dec) * np.float64(h) + np.float64(u)))
+                   + (h if near else f32(0)))
+
+    n = 30
+    dec = [f32(-abs(rng.normal()) * 0.1) if rng.random() < 0.5 else f32(rng.random() * 0.7)
+           for _ in range(n)]
+    u = [f32(rng.normal()) for _ in range(n)]
+    states, s = [], f32(rng.normal())
+    for j in range(n):  # behind tile j
+        s = apply(dec[j], s, u[j])
+        states.append(s)
+
+    def look(k, word):
+        found, s = False, f32(0)
+        for i in reversed(range(kAhead)):
+            kind, d, h = word[k - 1 - min(i, k - 1)]
+            found = kind == "state" or (found and kind != "unset")
+            s = h if kind == "state" else apply(d, s, h) if kind == "map" else s
+        return s if found else None
+
+    for k in range(1, n):
+        for _ in range(50):
+            word = []
+            for j in range(n):
+                kind = rng.choice(["unset", "map", "state"])
+                if j == 0 and kind == "map":
+                    kind = "state"  # the first tile has no map
+                word.append((kind, dec[j], states[j] if kind == "state" else u[j]))
+            got = look(k, word)
+            assert got is None or got == states[k - 1]
+    # maps alone behind the first tile's state: found as far as kAhead reaches, then in turn
+    word = [("state", None, states[0])] + [("map", dec[j], u[j]) for j in range(1, n)]
+    for j in range(1, n):
+        before = look(j, word)
+        assert before is not None and before == states[j - 1]
+        word[j] = ("state", None, apply(dec[j], before, u[j]))
