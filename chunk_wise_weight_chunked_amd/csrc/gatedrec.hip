@@ -237,6 +237,7 @@ __device__ __forceinline__ TileAt tile_at(const RecArgs& a, const Links& links, 
     w = ticket;
   }
   const uint32_t strips = (uint32_t)((a.d + kStrip - 1) / kStrip), row = strips * (uint32_t)a.B;
+  w = min(w, gridDim.x - 1);  // whatever happens to the counter, a tile of this call
   TileAt at;
   at.k = w / row;
   at.b = w % row / strips;
@@ -248,10 +249,12 @@ __device__ __forceinline__ TileAt tile_at(const RecArgs& a, const Links& links, 
 // The state in front of tile k of a channel (k > 0), from the words of tiles k - 1,
 // k - 2, ... at `word`, `step` words apart: from the nearest of kAhead that has its
 // state, the tiles behind that one applied in order, just as they do it themselves, so
-// that the result does not depend on which one it was.
+// that the result does not depend on which one it was.  The wait ends by itself (tile_at);
+// only where another call clears the same words meanwhile, which no workspace allows, it
+// ends here, after some seconds and with NaN.
 __device__ __forceinline__ float state_before(const uint64_t* word, int64_t step, int64_t k) {
-  constexpr int kAhead = 8;
-  for (;;) {
+  constexpr int kAhead = 8, kTries = 1 << 22;
+  for (int tries = 0; tries < kTries; ++tries) {
     uint64_t w[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) w[i] = get_word(word + min<int64_t>(i, k - 1) * step);
@@ -265,7 +268,9 @@ __device__ __forceinline__ float state_before(const uint64_t* word, int64_t step
       s = hi == kState ? f : decayed(__uint_as_float(hi), s, f);
     }
     if (found) return s;
+    __builtin_amdgcn_s_sleep(1);
   }
+  return __builtin_nanf("");
 }
 
 // What a lane of a tile works on.

@@ -704,3 +704,70 @@ def test_rows_behind_the_last_are_left_alone():
     ws = room(seq.ttt_act8_weight_grad_workspace_size(w), torch.uint8)
     seq.ttt_act8_weight_grad(w, codes, exps, dy, grad, ws, ws.numel() - 64)
     assert rest(grad, d * m) and rest(ws, ws.numel() - 64)
+
+
+# ---------------------------------------------------------- offsets beyond 32 bits
+def test_embed_tables_beyond_32_bits():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    V, d = 1_200_007, 2048  # 2.46e9 values, 9.8 GB in fp32
+    table = torch.empty(V, d, dtype=BF16, device="cuda").normal_(generator=g)
+    ids = torch.randint(0, V, (3000,), generator=g, device="cuda")
+    ids[:40] = torch.arange(V - 40, V, device="cuda")
+    ids[40:80] = torch.arange(40, device="cuda")
+    assert torch.equal(seq.embed_forward(ids, table), table[ids])
+    dout = torch.randn(3000, d, generator=g, device="cuda")
+    del table
+    got = seq.embed_backward(dout, ids, V, 2.0)
+    rows, inverse = torch.unique(ids, return_inverse=True)
+    want = torch.zeros(len(rows), d, dtype=torch.float64, device="cuda")
+    want.index_add_(0, inverse, dout.double(), alpha=2.0)
+    assert float((got[rows].double() - want).norm() / want.norm()) <= TOL_F32
+    got[rows] = 0
+    assert not got.any()
+    keep = torch.ones(V, d, device="cuda")
+    seq.embed_backward(dout, ids, V, 2.0, grad=keep)
+    assert float((keep[rows].double() - 1 - want).norm() / want.norm()) <= TOL_F32
+    keep[rows] = 1
+    assert (keep == 1).all()
+
+
+def test_gatedrec_sequences_beyond_32_bits():
+    """The last tokens of a call of 2^31 values and more are those of a call of their own from
+    the state in front of them."""
+    T, d = (1 << 20) + 300, 2056
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    new = lambda: torch.empty(1, T, d, dtype=BF16, device="cuda").normal_(generator=g)  # noqa: E731
+    x, dg, ig, dh = new(), new(), new(), new()
+    rate = torch.rand(d, generator=g, device="cuda") * 0.2 + 1e-3
+    h, S, saved = seq.gatedrec_forward(x, dg, ig, rate, save=True)
+    j = T // 128 - 3
+    a = 128 * j
+    last = [t[:, a:].contiguous() for t in (x, dg, ig, dh)]
+    h2, S2, saved2 = seq.gatedrec_forward(*last[:3], rate, state=saved[:, j].contiguous(), save=True)
+    assert torch.equal(h2, h[:, a:]) and torch.equal(S2, S) and torch.equal(saved2, saved[:, j:])
+    ds = torch.randn(1, d, generator=g, device="cuda")
+    got = seq.gatedrec_backward(x, dg, ig, rate, dh, saved, dstate_out=ds)
+    want = seq.gatedrec_backward(*last[:3], rate, last[3], saved2, dstate_out=ds)
+    for n in ("x", "decay_gate", "input_gate"):
+        assert torch.equal(got[n][:, a:], want[n]), n
+
+
+def test_act8_beyond_32_bits():
+    rows, d = 1_100_003, 2048  # 2.25e9 values
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.empty(rows, d, dtype=BF16, device="cuda").normal_(generator=g)
+    codes, exps = seq.act8_store(x)
+    c2, e2 = seq.act8_store(x[-300:].contiguous())
+    assert torch.equal(codes[-300:], c2) and torch.equal(exps[-300:], e2)
+    assert torch.equal(seq.act8_load(codes, exps)[-300:], seq.act8_load(c2, e2))
+    dy = torch.randn(rows, 40, generator=g, device="cuda").to(BF16)
+    got = seq.act8_weight_grad(codes, exps, dy)
+    want = torch.zeros(d, 40, dtype=torch.float64, device="cuda")
+    for a in range(0, rows, 100000):
+        part = slice(a, a + 100000)
+        want += seq.act8_load(codes[part], exps[part], F32).double().t().contiguous() @ dy[part].double()
+    # sums of 1.1 million products: the slices' partial sums keep the chains short, as before
+    assert float((got.double() - want).norm() / want.norm()) <= 4 * TOL_F32
