@@ -27,6 +27,7 @@ constexpr int kWaveCols = 512;   // columns of a wave: 8 a lane
 constexpr int kSortBlock = 1024;  // tokens that a workgroup of the sort orders, one a lane
 constexpr int kSortWaves = kSortBlock / 64;
 constexpr int kMaxBins = 512;
+constexpr int kFewTiles = 64;    // 31984 tokens 69.5 us, 72.9 with another launch; 65000 139.6, 141.1
 
 __device__ __forceinline__ int64_t id_at(const void* ids, bool wide, int64_t n) {
   return wide ? static_cast<const int64_t*>(ids)[n] : static_cast<const int32_t*>(ids)[n];
@@ -88,9 +89,8 @@ struct Zeros {
   }
 };
 
-// hist[bin][tile]: tokens of a tile with this digit.
+// hist[tile][bin]: tokens of a tile with this digit.
 __global__ __launch_bounds__(kSortBlock) void embed_hist_kernel(SortIn in, int shift, int bins,
-                                                                int64_t tiles,
                                                                 uint32_t* __restrict__ hist,
                                                                 Zeros zeros) {
   __shared__ uint32_t count[kMaxBins];
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kSortBlock) void embed_hist_kernel(SortIn in, int s
   const int64_t n = (int64_t)blockIdx.x * kSortBlock + threadIdx.x;
   if (n < in.N) atomicAdd(&count[(in.key(n) >> shift) & (bins - 1)], 1u);
   __syncthreads();
-  if (b < bins) hist[b * tiles + blockIdx.x] = count[b];
+  if (b < bins) hist[(int64_t)blockIdx.x * bins + b] = count[b];
 }
 
 // Exclusive sums of v over the workgroup's threads (kThreads a multiple of 64),
@@ -130,29 +130,42 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* wave_s
   return before + x - v;
 }
 
-// hist[bin][tile] -> tokens of this digit in the tiles in front; total[bin].
-__global__ __launch_bounds__(kBlock) void embed_scan_kernel(uint32_t* __restrict__ hist,
-                                                            int64_t tiles,
-                                                            uint32_t* __restrict__ total,
-                                                            Zeros zeros) {
-  __shared__ uint32_t wave_sum[kBlock / 64];
-  if (zeros.fill<kBlock>()) return;
-  uint32_t run = 0;
-  uint32_t* const h = hist + blockIdx.x * tiles;
-  for (int64_t t0 = 0; t0 < tiles; t0 += kBlock) {
-    const int64_t t = t0 + threadIdx.x;
-    const uint32_t v = t < tiles ? h[t] : 0;
-    uint32_t sum;
-    const uint32_t e = block_exclusive<kBlock>(v, wave_sum, &sum);
-    if (t < tiles) h[t] = run + e;
-    run += sum;
+// hist[tile][bin] -> tokens of this digit in the tiles in front; total[bin].  64 digits a
+// workgroup, a wave walks its share of the tiles.
+__global__ __launch_bounds__(kSortBlock) void embed_scan_kernel(uint32_t* __restrict__ hist,
+                                                                int bins, int64_t tiles,
+                                                                uint32_t* __restrict__ total) {
+  __shared__ uint32_t sum[kSortWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int bin = blockIdx.x * 64 + lane;
+  const int64_t share = (tiles + kSortWaves - 1) / kSortWaves;
+  const int64_t t0 = wave * share, t1 = min(t0 + share, tiles);
+  uint32_t n = 0;
+  if (bin < bins)
+#pragma unroll 8
+    for (int64_t t = t0; t < t1; ++t) n += hist[t * bins + bin];
+  sum[wave][lane] = n;
+  __syncthreads();
+  uint32_t at = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) {
+    if (w < wave) at += sum[w][lane];
+    all += sum[w][lane];
   }
-  if (threadIdx.x == 0) total[blockIdx.x] = run;
+  if (bin >= bins) return;
+  if (wave == 0) total[bin] = all;
+#pragma unroll 8
+  for (int64_t t = t0; t < t1; ++t) {
+    const uint32_t c = hist[t * bins + bin];
+    hist[t * bins + bin] = at;
+    at += c;
+  }
 }
 
 // The tile's tokens to their places.  A token's rank among those of its digit is the
 // count of the lower lanes of its wave with that digit, found by a ballot for each bit,
-// and of the waves and tiles in front.
+// and of the waves and tiles in front.  Without `total`, hist still holds the tiles' own
+// counts, and the workgroup adds up those in front of it itself.
 __global__ __launch_bounds__(kSortBlock) void embed_scatter_kernel(
     SortIn in, int shift, int bits, int64_t tiles, const uint32_t* __restrict__ hist,
     const uint32_t* __restrict__ total, uint32_t* __restrict__ keys_out,
@@ -166,8 +179,18 @@ __global__ __launch_bounds__(kSortBlock) void embed_scatter_kernel(
   const bool live = n < in.N, has = threadIdx.x < (unsigned)bins;
   const uint32_t key = live ? in.key(n) : 0;
   const uint32_t place = live && in.pos ? in.pos[n] : (uint32_t)n;
-  const uint32_t mine = has ? total[threadIdx.x] : 0;
-  const uint32_t tile = has ? hist[threadIdx.x * tiles + blockIdx.x] : 0;
+  uint32_t mine = 0, tile = 0;
+  if (has && total) {
+    mine = total[threadIdx.x];
+    tile = hist[(int64_t)blockIdx.x * bins + threadIdx.x];
+  } else if (has) {
+#pragma unroll 8
+    for (int t = 0; t < (int)tiles; ++t) {
+      const uint32_t c = hist[t * bins + threadIdx.x];
+      mine += c;
+      tile += t < (int)blockIdx.x ? c : 0;
+    }
+  }
   for (int i = lane; i < bins; i += 64) count[wave][i] = 0;
   const uint32_t digit = (key >> shift) & (bins - 1);
   uint64_t same = __ballot(live);
@@ -401,13 +424,45 @@ __global__ __launch_bounds__(kBlock) void embed_sum_kernel(
   }
 }
 
+// Sums of 64 pieces (from a multiple of 64 on) that hold one id alone, [group][d]: an id
+// of very many tokens is then joined from them.
+constexpr int kGroup = 64;
+__global__ __launch_bounds__(kBlock) void embed_group_kernel(const uint32_t* __restrict__ keys,
+                                                             const float* __restrict__ part,
+                                                             float* __restrict__ group, int64_t N,
+                                                             int64_t d, int piece) {
+  __shared__ float4 s[4][64];
+  const int64_t p = (int64_t)blockIdx.x * kGroup;
+  if ((p + kGroup) * piece > N || keys[p * piece] != keys[(p + kGroup) * piece - 1]) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t col = (int64_t)blockIdx.y * 256 + 4 * lane;
+  float4 a = make_float4(0, 0, 0, 0);
+  if (col < d) {
+#pragma unroll 8
+    for (int q = wave; q < kGroup; q += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(part + 2 * (p + q) * d + col);
+      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+    }
+  }
+  s[wave][lane] = a;
+  __syncthreads();
+  if (wave > 0 || col >= d) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) {
+    const float4 v = s[w][lane];
+    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+  }
+  *reinterpret_cast<float4*>(group + blockIdx.x * d + col) = a;
+}
+
 // The rows of ids that reach over pieces: the workgroups of the piece in which
 // one begins add its pieces' sums, 4 waves every fourth and then each other's,
-// 256 columns each.
+// 256 columns each; of the whole groups of pieces behind it their groups' (group, or null).
 template <typename TO, bool kAdd>
 __global__ __launch_bounds__(kBlock) void embed_join_kernel(
     const uint32_t* __restrict__ keys, const float* __restrict__ part, TO* __restrict__ grad,
-    int64_t N, int64_t V, int64_t d, float scale, int piece, unsigned pieces, int64_t zero0) {
+    const float* __restrict__ group, int64_t N, int64_t V, int64_t d, float scale, int piece,
+    unsigned pieces, int64_t zero0) {
   __shared__ float s[4][256];
   if (blockIdx.x >= pieces) {  // the last rows' zeros
     const int64_t v0 = zero0 + kZeroRows * (((int64_t)(blockIdx.x - pieces) * gridDim.y +
@@ -435,13 +490,23 @@ __global__ __launch_bounds__(kBlock) void embed_join_kernel(
   }
   const int64_t col = (int64_t)blockIdx.y * 256 + 4 * lane;
   float4 a = make_float4(0, 0, 0, 0);
+  // pieces p .. head - 1 and tail .. end, groups head / kGroup .. tail / kGroup - 1; the
+  // id fills the groups: it begins in front of them and goes on to end, whose last tokens
+  // may be another's, so that end is in none
+  int64_t head = end + 1, tail = end + 1;
+  if (group && end / kGroup > p / kGroup + 1)
+    head = (p / kGroup + 1) * kGroup, tail = end / kGroup * kGroup;
   if (col < d) {
-#pragma unroll 8
-    for (int64_t q = p + wave; q <= end; q += 4) {
-      const int64_t slot = 2 * q + (q == p && inside ? 1 : 0);
-      const float4 v = *reinterpret_cast<const float4*>(part + slot * d + col);
+    const auto add = [&](const float* from) {
+      const float4 v = *reinterpret_cast<const float4*>(from + col);
       a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-    }
+    };
+#pragma unroll 8
+    for (int64_t q = p + wave; q < head; q += 4) add(part + (2 * q + (q == p && inside ? 1 : 0)) * d);
+#pragma unroll 8
+    for (int64_t g = head / kGroup + wave; g < tail / kGroup; g += 4) add(group + g * d);
+#pragma unroll 8
+    for (int64_t q = tail + wave; q <= end; q += 4) add(part + 2 * q * d);
   }
   *reinterpret_cast<float4*>(&s[wave][4 * lane]) = a;
   __syncthreads();
@@ -479,9 +544,14 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 int piece_of(const EmbedArgs& a) { return a.N <= kSmall ? 8 : kPiece; }
 int64_t pieces_of(const EmbedArgs& a) { return (a.N + piece_of(a) - 1) / piece_of(a); }
 
-// Workspace: two sets of keys and places, the digits' counts, the partial sums.
+// Whether an id can have so many pieces that adding them one by one shows: with all tokens
+// of one id 131072 x 1024 take 101 us in groups and 166 without, 1000000 x 64 348 and 937; a
+// launch more costs a call of 131072 different ones 2 of 245 us.
+bool grouped(const EmbedArgs& a) { return pieces_of(a) >= 4096; }
+
+// Workspace: two sets of keys and places, the digits' counts, the pieces' and groups' sums.
 struct GradPlan {
-  size_t keys[2], pos[2], hist, total, part, bytes;
+  size_t keys[2], pos[2], hist, total, part, group, bytes;
 };
 GradPlan grad_plan(const EmbedArgs& a) {
   const SortPlan sp = sort_plan(a);
@@ -496,6 +566,8 @@ GradPlan grad_plan(const EmbedArgs& a) {
   p.hist = take(((size_t)sp.tiles << sp.bits) * 4);
   p.total = take(((size_t)1 << sp.bits) * 4);
   p.part = take((size_t)(2 * pieces_of(a) * a.d) * sizeof(float));
+  p.group = at;
+  if (grouped(a)) take((size_t)(pieces_of(a) / kGroup * a.d) * sizeof(float));
   p.bytes = at;
   return p;
 }
@@ -546,7 +618,7 @@ hipError_t launch_embed_backward(const EmbedArgs& a, const void* ids, const void
   // (some 4 us each, 16 MB); the launches behind it leave out those that have tokens.
   const int64_t row = a.d * (int64_t)dtype_bytes(a.out_dt) / 16;
   const int64_t share = std::min<int64_t>(((int64_t)1 << 20) / row,
-                                          a.V / (3 * sp.passes + 4));  // rows a launch
+                                          a.V / (2 * sp.passes + 4));  // rows a launch
   int64_t zeroed = a.accumulate ? a.V : 0;
   const auto zeros = [&](int64_t own, int threads, unsigned* grid) {
     const int64_t rows = std::min(share, a.V - zeroed);
@@ -564,18 +636,21 @@ hipError_t launch_embed_backward(const EmbedArgs& a, const void* ids, const void
                                                         u32(p.pos[0]), z);
     cur = 1;
   } else {
+    // where a workgroup adds up the counts of all tiles as fast as another launch would
+    const bool few = sp.tiles <= kFewTiles;
     for (int i = 0; i < sp.passes; ++i) {
       const int shift = i * sp.bits;
       const SortIn in{i ? nullptr : ids, u32(p.keys[cur ^ 1]), i ? u32(p.pos[cur ^ 1]) : nullptr,
                       a.wide_ids, a.N, a.V};
       Zeros z = zeros(sp.tiles, kSortBlock, &grid);
-      embed_hist_kernel<<<dim3(grid), kSortBlock, 0, s>>>(in, shift, bins, sp.tiles, hist, z);
-      z = zeros(bins, kBlock, &grid);
-      embed_scan_kernel<<<dim3(grid), kBlock, 0, s>>>(hist, sp.tiles, total, z);
+      embed_hist_kernel<<<dim3(grid), kSortBlock, 0, s>>>(in, shift, bins, hist, z);
+      if (!few)
+        embed_scan_kernel<<<dim3((unsigned)((bins + 63) / 64)), kSortBlock, 0, s>>>(hist, bins,
+                                                                                    sp.tiles, total);
       z = zeros(sp.tiles, kSortBlock, &grid);
-      embed_scatter_kernel<<<dim3(grid), kSortBlock, 0, s>>>(in, shift, sp.bits, sp.tiles, hist,
-                                                             total, u32(p.keys[cur]), u32(p.pos[cur]),
-                                                             z);
+      embed_scatter_kernel<<<dim3(grid), kSortBlock, 0, s>>>(
+          in, shift, sp.bits, sp.tiles, hist, few ? nullptr : total, u32(p.keys[cur]),
+          u32(p.pos[cur]), z);
       cur ^= 1;
     }
   }
@@ -596,8 +671,12 @@ hipError_t launch_embed_backward(const EmbedArgs& a, const void* ids, const void
     const unsigned pieces = (unsigned)pieces_of(a), cols = (unsigned)((a.d + 255) / 256);
     const int64_t waves = (late + kZeroRows - 1) / kZeroRows;
     const unsigned extra = (unsigned)((waves + 4 * cols - 1) / (4 * cols));
+    float* const group = grouped(a) ? reinterpret_cast<float*>(base + p.group) : nullptr;
+    if (group)
+      embed_group_kernel<<<dim3(pieces / kGroup, cols), kBlock, 0, s>>>(keys, part, group, a.N, a.d,
+                                                                        piece_of(a));
     embed_join_kernel<TO, kAdd><<<dim3(pieces + extra, cols), kBlock, 0, s>>>(
-        keys, part, static_cast<TO*>(grad), a.N, a.V, a.d, a.scale, piece_of(a),
+        keys, part, static_cast<TO*>(grad), group, a.N, a.V, a.d, a.scale, piece_of(a),
         pieces, zero1);
     return hipGetLastError();
   };

@@ -132,6 +132,27 @@ def test_embed_backward(N, V, d, dtype, gd):
         assert torch.isnan(grad[none]).all()
 
 
+@pytest.mark.parametrize("lead", [0, 1, 31, 2047, 2048, 5000])
+def test_embed_backward_ids_of_very_many_tokens(lead):
+    """One id with nearly all tokens, begun anywhere in the sorted order, between rare ones."""
+    N, V, d = 140000, 50, 24
+    g = gen(lead)
+    ids = torch.full((N,), 20)
+    at = torch.randperm(N, generator=g)
+    ids[at[:lead]] = torch.randint(0, 20, (lead,), generator=g)
+    ids[at[lead:lead + 700]] = torch.randint(21, V, (700,), generator=g)
+    dout = normal(g, N, d)
+    want = ref.embed_grad(f64(dout), ids.numpy(), V, 1.0)
+    got = f64(seq.embed_backward(dout, ids.cuda(), V))
+    for v in range(V):
+        if want[v].any():
+            assert rel(got[v], want[v]) <= TOL_F32, v
+    assert rel(got, want) <= TOL_F32
+    start = normal(g, V, d)
+    want = want + f64(start)
+    assert rel(f64(seq.embed_backward(dout, ids.cuda(), V, grad=start)), want) <= TOL_F32
+
+
 def test_embed_backward_is_the_forwards():
     """<dout, embed(table)> is linear in the table: its differences are the gradient."""
     g = gen(5)
