@@ -419,9 +419,22 @@ act8_grad_kernel(GradArgs g) {
     lb.l.init(g.dy, g.dys, g.rows, g.N, n0, k0);
     grad_mainloop<GradMma<S, true>>(acc, la, lb, n, smem, p);
   }
-  float* const part =
-      slice < 0 ? nullptr
-                : g.part + ((int64_t)(tile - g.whole) * g.slices + slice) * (S::BM * S::BN);
+  if (slice >= 0) {
+    // as the accumulators hold them: act8_sum_kernel finds the rows and columns
+    float* const part = g.part + ((int64_t)(tile - g.whole) * g.slices + slice) * (S::BM * S::BN) +
+                        (threadIdx.x >> 6) * (S::WM * S::WN) + 4 * p.lane;
+#pragma unroll
+    for (int i = 0; i < S::MB; ++i)
+#pragma unroll
+      for (int j = 0; j < S::NB; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const floatx16_t& v = acc.v[i][j];
+          *reinterpret_cast<float4*>(part + ((i * S::NB + j) * 4 + q) * 256) =
+              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+    return;
+  }
   for (int q = 0; q < S::BN / kEpiCols; ++q) {
     __syncthreads();  // the mainloop's (or the previous pass's) reads of LDS are done
 #pragma unroll
@@ -443,10 +456,6 @@ act8_grad_kernel(GradArgs g) {
       const floatx4_t lo = lds_load<floatx4_t>(smem + ((uint32_t)t * kEpiStride + c) * 4);
       const floatx4_t hi = lds_load<floatx4_t>(smem + ((uint32_t)t * kEpiStride + c + 4) * 4);
       float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-      if (part) {
-        Piece<float>::store(part + t * S::BN + kEpiCols * q + c, v);
-        continue;
-      }
       TO* const to = static_cast<TO*>(g.out) + (m0 + t) * g.N + cb + c;
       if (g.accumulate) {
         Piece<TO> old;
@@ -461,39 +470,35 @@ act8_grad_kernel(GradArgs g) {
   }
 }
 
-// The tiles that came in slices, added in order: 8 rows of a tile a workgroup.
+// The tiles that came in slices, added in order: a lane has 4 rows of a column, as they
+// lie in an accumulator.
 template <typename TO, class S>
 __global__ __launch_bounds__(kBlock) void act8_sum_kernel(GradArgs g) {
-  constexpr int kEach = S::BM * S::BN / (8 * kBlock);  // workgroups of a tile
+  constexpr int kEach = S::BM * S::BN / (4 * kBlock);  // workgroups of a tile
   const int tiles_m = (int)((g.M + S::BM - 1) / S::BM), tiles_n = (int)((g.N + S::BN - 1) / S::BN);
   const int tile = blockIdx.x / kEach;
   const TileCoord tc = grouped_tile(g.whole + tile, tiles_m, tiles_n, 8);
-  const int at = (blockIdx.x % kEach) * (8 * kBlock) + 8 * threadIdx.x;
-  const int64_t row = (int64_t)tc.m * S::BM + at / S::BN, col = (int64_t)tc.n * S::BN + at % S::BN;
-  if (row >= g.M || col >= g.N) return;
-  const float* p = g.part + (int64_t)tile * g.slices * (S::BM * S::BN) + at;
-  float f[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-#pragma unroll 4
+  const int at = (blockIdx.x % kEach) * kBlock + threadIdx.x, lane = at & 63;
+  const int q = (at >> 6) & 3, block = at >> 8;
+  const int j = block % S::NB, i = block / S::NB % S::MB, wave = block / (S::NB * S::MB);
+  const int64_t row = (int64_t)tc.m * S::BM + wave / S::WAVES_N * S::WM + 32 * i + 8 * q +
+                      4 * (lane >> 5);
+  const int64_t col = (int64_t)tc.n * S::BN + wave % S::WAVES_N * S::WN + 32 * j + (lane & 31);
+  if (col >= g.N) return;
+  const float* p = g.part + (int64_t)tile * g.slices * (S::BM * S::BN) + 4 * (int64_t)at;
+  float4 f = make_float4(0, 0, 0, 0);
+#pragma unroll 8
   for (int s = 0; s < g.slices; ++s) {
-    Piece<float> q;
-    q.load(p + (int64_t)s * (S::BM * S::BN));
-    float v[8];
-    q.get(v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] += v[j];
+    const float4 v = *reinterpret_cast<const float4*>(p + (int64_t)s * (S::BM * S::BN));
+    f.x += v.x, f.y += v.y, f.z += v.z, f.w += v.w;
   }
-  TO* const to = static_cast<TO*>(g.out) + row * g.N + col;
-  if (g.accumulate) {
-    Piece<TO> old;
-    old.load(to);
-    float v[8];
-    old.get(v);
+  const float sum[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] += v[j];
+  for (int e = 0; e < 4; ++e) {
+    if (row + e >= g.M) break;
+    TO* const to = static_cast<TO*>(g.out) + (row + e) * g.N + col;
+    Elem<TO>::store(to, g.accumulate ? Elem<TO>::to_f32(*to) + sum[e] : sum[e]);
   }
-  Piece<TO>::store(to, f);
 }
 
 template <typename F>
@@ -590,7 +595,7 @@ template <class S>
 hipError_t launch_products(const Act8Grad& g, const GradArgs& a, hipStream_t s) {
   const int64_t rest = grad_tiles(g, S::BM) - a.whole;
   const dim3 grid((unsigned)(a.whole + rest * a.slices));
-  const dim3 sums((unsigned)(rest * (S::BM * S::BN / (8 * kBlock))));
+  const dim3 sums((unsigned)(rest * (S::BM * S::BN / (4 * kBlock))));
   if (g.dt == Dtype::F32)
     act8_grad_kernel<float, S, true><<<grid, S::kThreads, 0, s>>>(a);
   else if (g.grad_dt == Dtype::F32)
