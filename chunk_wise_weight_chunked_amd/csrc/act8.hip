@@ -103,15 +103,16 @@ __global__ __launch_bounds__(kBlock) void act8_load_kernel(const int8_t* __restr
 // [64 tokens] bf16 (128-byte rows: a k-tile of the mainloop), zeros behind the last token.
 constexpr int kTokens = kRowBytes / 2;
 
-// A lane takes 4 columns (c0 ..) of 8 tokens (t0 ..), of which `live` are there.  The 8
+// A lane takes kCols columns (c0 ..) of 8 tokens (t0 ..), of which `live` are there.  The 8
 // lanes that share columns are neighbours, so that they write whole 128-byte rows.
+template <int kCols>
 struct BlockLane {
   int64_t t0, c0, at;  // at: place of the first column's 8 tokens
   int live;
   bool any;
   __device__ __forceinline__ BlockLane(int64_t columns, int64_t rows, int64_t n) {
     const int oct = threadIdx.x & 7;
-    c0 = columns * 128 + 4 * (threadIdx.x >> 3);
+    c0 = columns * (32 * kCols) + kCols * (threadIdx.x >> 3);
     t0 = blockIdx.x * (int64_t)kTokens + 8 * oct;
     at = (blockIdx.x * n + c0) * kTokens + 8 * oct;
     live = (int)max<int64_t>(0, min<int64_t>(8, rows - t0));
@@ -119,34 +120,35 @@ struct BlockLane {
   }
 };
 
-// 128 columns of x, out [..][d].
+constexpr int kXColumns = 256;
+// kXColumns columns of x, out [..][d].
 __device__ __forceinline__ void decode_block(const int8_t* __restrict__ codes,
                                              const uint8_t* __restrict__ exps,
                                              uint16_t* __restrict__ out, int64_t rows, int64_t d,
                                              int64_t columns) {
-  const BlockLane l(columns, rows, d);
+  constexpr int kCols = kXColumns / 32;
+  const BlockLane<kCols> l(columns, rows, d);
   if (!l.any) return;
   const int64_t groups = (d + kAct8Group - 1) / kAct8Group;
-  uint32_t w[8], e[8];
+  uint2 w[8];
+  uint32_t e[8];
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
-    w[t] = e[t] = 0;
+    w[t] = make_uint2(0, 0), e[t] = 0;
     if (t < l.live) {
-      w[t] = *reinterpret_cast<const uint32_t*>(codes + (l.t0 + t) * d + l.c0);
+      w[t] = *reinterpret_cast<const uint2*>(codes + (l.t0 + t) * d + l.c0);
       e[t] = exps[(l.t0 + t) * groups + l.c0 / kAct8Group];
     }
   }
-  float v[8][4];
 #pragma unroll
-  for (int t = 0; t < 8; ++t)
+  for (int c = 0; c < kCols; ++c) {
+    float v[8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      v[t][c] = (float)((int32_t)(w[t] << (24 - 8 * c)) >> 24) * __uint_as_float(e[t] << 23);
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4*>(out + l.at + c * kTokens) =
-        make_uint4(pack_bf16x2(v[0][c], v[1][c]), pack_bf16x2(v[2][c], v[3][c]),
-                   pack_bf16x2(v[4][c], v[5][c]), pack_bf16x2(v[6][c], v[7][c]));
+    for (int t = 0; t < 8; ++t)
+      v[t] = (float)((int32_t)((c < 4 ? w[t].x : w[t].y) << (24 - 8 * (c & 3))) >> 24) *
+             __uint_as_float(e[t] << 23);
+    Piece<uint16_t>::store(out + l.at + c * kTokens, v);
+  }
 }
 
 // 128 columns of an fp32 dy as three bf16 terms whose sum it is: the leading 8 bits of
@@ -155,7 +157,7 @@ __device__ __forceinline__ void decode_block(const int8_t* __restrict__ codes,
 __device__ __forceinline__ void split_block(const float* __restrict__ dy, int64_t dys,
                                             uint16_t* __restrict__ out, int64_t part, int64_t rows,
                                             int64_t n, int64_t columns) {
-  const BlockLane l(columns, rows, n);
+  const BlockLane<4> l(columns, rows, n);
   if (!l.any) return;
   float v[8][4];
 #pragma unroll
@@ -660,7 +662,7 @@ hipError_t launch_act8_weight_grad(const Act8Grad& g, const int8_t* codes, const
     a.dy = static_cast<const uint16_t*>(dy), a.dys = g.dys;
   }
   const int64_t groups = (g.d_in + kAct8Group - 1) / kAct8Group;
-  const unsigned x_columns = (unsigned)((g.d_in + 127) / 128);
+  const unsigned x_columns = (unsigned)((g.d_in + kXColumns - 1) / kXColumns);
   const hipError_t e = in_launches(n, 1, [&](int64_t at, int64_t, dim3 grid) {
     grid.y = x_columns + (split ? (unsigned)((g.d_out + 127) / 128) : 0);
     const int64_t t = at * kTokens;
