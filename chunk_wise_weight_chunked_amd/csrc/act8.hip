@@ -152,8 +152,8 @@ __device__ __forceinline__ void decode_block(const int8_t* __restrict__ codes,
 }
 
 // 128 columns of an fp32 dy as three bf16 terms whose sum it is: the leading 8 bits of
-// what is left, three times; an infinity or NaN goes into the first alone.  Terms `part`
-// values apart.
+// what is left, three times (multiples of 2^-133, bf16's smallest, towards 0); an infinity
+// or NaN goes into the first alone.  Terms `part` values apart.
 __device__ __forceinline__ void split_block(const float* __restrict__ dy, int64_t dys,
                                             uint16_t* __restrict__ out, int64_t part, int64_t rows,
                                             int64_t n, int64_t columns) {

@@ -350,8 +350,9 @@ __global__ __launch_bounds__(kBlock) void embed_sum_kernel(
   const int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) +
                        __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // wave-uniform
   if (unit >= units) {
-    const int64_t v0 = zero0 + (unit - units) * kZeroRows;
-    if (v0 < zero1) zero_rows(keys, grad, N, zero1, d, v0);
+    const int64_t step = ((int64_t)gridDim.x * (kBlock / 64) - units) * kZeroRows;
+    for (int64_t v0 = zero0 + (unit - units) * kZeroRows; v0 < zero1; v0 += step)
+      zero_rows(keys, grad, N, zero1, d, v0);
     return;
   }
   const int64_t p = unit / col_parts;
@@ -662,9 +663,11 @@ hipError_t launch_embed_backward(const EmbedArgs& a, const void* ids, const void
     constexpr bool kAdd = decltype(add)::value;
     const int col_parts = (int)((a.d + kWaveCols - 1) / kWaveCols);
     const int64_t units = pieces_of(a) * col_parts;
-    // units of 64 threads: fewer than 2^32 threads a launch (checked by the caller)
+    // waves: a launch's threads are counted in 32 bits, units are 2^25 at most, and the
+    // waves for zeros go on with further rows where 2^22 do not take them all
     const int64_t late = std::min(3 * share, a.V - zeroed), zero1 = a.V - late;
-    const int64_t all = units + (zero1 - zeroed + kZeroRows - 1) / kZeroRows;
+    const int64_t all = units + std::min<int64_t>((zero1 - zeroed + kZeroRows - 1) / kZeroRows,
+                                                  (int64_t)1 << 22);
     embed_sum_kernel<T, TO, kAdd><<<dim3((unsigned)((all + 3) / 4)), kBlock, 0, s>>>(
         keys, pos, static_cast<const T*>(dout), static_cast<TO*>(grad), part, a.N, a.V, a.d,
         a.scale, piece_of(a), units, col_parts, zeroed, zero1);

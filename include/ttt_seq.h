@@ -166,8 +166,10 @@ ttt_status_t ttt_act8_load(const ttt_act8_desc_t* desc, const int8_t* codes, con
 
 /* The gradient of a weight [d_in][d_out] from the activations kept in front of it:
  *   grad (+)= x8^T dy
- * Every product of a code and a bf16 dy is exact, as is x8 times any fp32 dy in the fp32
- * matrix product; sums are fp32, rounded once.
+ * On the bf16 matrix cores: every product of x8 and a bf16 dy is exact; an fp32 dy is taken
+ * as the three bf16 values whose sum it is (what it has below multiples of 2^-133, the
+ * smallest of bf16, is left out: values below 2^-109 alone have that).  Sums are fp32,
+ * rounded once.
  *   rows, d_in  as rows and d above; rows * d_in and rows * d_out <= 2^40
  *   d_out    a multiple of 8, 8 <= d_out <= 2^20; d_in * d_out <= 2^36
  *   dy_stride  values between rows of dy: a multiple of 8, d_out <= dy_stride <= 2^20

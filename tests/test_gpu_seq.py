@@ -522,6 +522,23 @@ def test_act8_weight_grad_large(rows, d_in, d_out, dtype, gd):
         assert float(((start.double() - keep - want).norm() / want.norm())) <= TOL_F32
 
 
+@pytest.mark.parametrize("power", [-100, -115, -126, -130])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_act8_weight_grad_tiny(power, dtype):
+    """Gradients near the end of the types' ranges: an fp32 dy counts in multiples of 2^-133."""
+    g = gen(7)
+    codes, exps = seq.act8_store(normal(g, 700, 256))
+    dy = normal(g, 700, 264)
+    dy = (dy.double() * 2.0 ** power).to(dtype)
+    x64 = ref.act8_value(codes.cpu().numpy(), exps.cpu().numpy())
+    want = x64.T @ f64(dy)
+    got = f64(seq.act8_weight_grad(codes, exps, dy))
+    # each of 700 additions may round to a multiple of 2^-149; dy's rest is below 2^-133
+    lost = abs(x64).sum(0)[:, None] * 2.0 ** -133 if dtype == F32 else 0.0
+    size = (want ** 2).mean() ** 0.5
+    assert (abs(got - want) <= 8 * TOL_F32 * size + 3 * 700 * 2.0 ** -149 + lost).all()
+
+
 def test_act8_weight_grad_rows_of_more_dimensions():
     g = gen(3)
     x, dy = normal(g, 3, 50, 64, dtype=BF16), normal(g, 3, 50, 40, dtype=BF16)
@@ -751,6 +768,27 @@ def test_embed_tables_beyond_32_bits():
     assert float((keep[rows].double() - 1 - want).norm() / want.norm()) <= TOL_F32
     keep[rows] = 1
     assert (keep == 1).all()
+
+
+def test_embed_backward_over_a_thousand_million_rows():
+    """Every row of a gradient that takes more waves for its zeros than one launch has."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    V, d = (1 << 30) + 12345, 8
+    ids = torch.randint(0, V, (1000,), generator=g, device="cuda")
+    ids[:3] = torch.tensor([0, V - 1, V - 1], device="cuda")
+    dout = torch.randn(1000, d, generator=g, device="cuda").to(BF16)
+    grad = torch.ones(V, d, dtype=BF16, device="cuda")
+    desc = seq.make_embed_desc(1000, V, d, BF16, BF16)
+    ws = torch.empty(seq.ttt_embed_backward_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    seq.ttt_embed_backward(desc, ids, dout, grad, ws)
+    rows, inverse = torch.unique(ids, return_inverse=True)
+    want = torch.zeros(len(rows), d, dtype=torch.float64, device="cuda")
+    want.index_add_(0, inverse, dout.double())
+    # one rounding of a sum of one to three values of bf16, all but exact in fp32
+    assert torch.equal(grad[rows], want.float().to(BF16))
+    grad[rows] = 0
+    assert not any(bool(part.any()) for part in grad.split(1 << 27))
 
 
 def test_gatedrec_sequences_beyond_32_bits():
