@@ -57,12 +57,13 @@ __device__ __forceinline__ float decayed(float dec, float h, float u) {
 // 2^64 (1 - a^2) from a and its z: near a = 1 by the same polynomial of 2 z.  The roots'
 // instructions take values below 2^-126 as 0, which 2^64 times the smallest is not: b
 // comes as 2^32 b, its inverse as 2^-32 / b.
-__device__ __forceinline__ float root_arg(float z, float a) {
+// floor: what it is at least.
+__device__ __forceinline__ float root_arg(float z, float a, float floor) {
   float p = __builtin_fmaf(z, -0x1.2ee444p+59f, -0x1.38ae68p+61f);
   p = __builtin_fmaf(z, p, -0x1.c6947ap+62f);
   p = __builtin_fmaf(z, p, -0x1.ebfb70p+63f);
   p = __builtin_fmaf(z, p, -0x1.62e430p+64f);
-  const float near = z * p, far = __builtin_fmaf(-a, a, 1.0f) * 0x1p64f;
+  const float near = __builtin_fmaf(z, p, floor), far = __builtin_fmaf(-a, a, 1.0f) * 0x1p64f;
   return z > -0.25f ? near : far;
 }
 
@@ -83,7 +84,14 @@ __device__ __forceinline__ float sigmoid_scaled(float x) {
 }
 // b i from z, a and the input gate
 __device__ __forceinline__ float gated(float z, float a, float gate) {
-  return __builtin_amdgcn_sqrtf(root_arg(z, a)) * sigmoid_scaled(gate);
+  return __builtin_amdgcn_sqrtf(root_arg(z, a, 0.0f)) * sigmoid_scaled(gate);
+}
+
+// Two values as bf16 (RNE), by one instruction.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{lo, hi}, b2));
 }
 
 // kPer values of a lane: 16 bytes.
@@ -92,10 +100,10 @@ struct Lane;
 template <>
 struct Lane<uint16_t> {
   static constexpr int kPer = 8;
-  __device__ __forceinline__ static uint32_t word(const float f[2]) { return pack_bf16x2(f[0], f[1]); }
+  __device__ __forceinline__ static uint32_t word(const float f[2]) { return pack2(f[0], f[1]); }
   __device__ __forceinline__ static void put(uint16_t* p, const float f[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                              pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]),
+                                              pack2(f[6], f[7]));
   }
 };
 template <>
@@ -257,7 +265,7 @@ __device__ __forceinline__ float state_before(const uint64_t* word, int64_t step
   for (int tries = 0; tries < kTries; ++tries) {
     uint64_t w[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) w[i] = get_word(word + min<int64_t>(i, k - 1) * step);
+    for (int i = 0; i < kAhead; ++i) w[i] = get_word(word + (i < k ? i : k - 1) * step);
     bool found = false;
     float s = 0.0f;
 #pragma unroll
@@ -291,11 +299,44 @@ __device__ __forceinline__ LaneAt<S> lane_at(const RecArgs& a, const TileAt& at)
   l.t0 = at.j * kRecTile + l.run * S::kRun;
   const bool live = l.c0 < a.d;
   const int64_t n = tokens_of(a, at.b);
-  l.n = live ? (int)min<int64_t>(max<int64_t>(n - l.t0, 0), S::kRun) : 0;
-  l.rows = live ? (int)min<int64_t>(max<int64_t>(a.T - l.t0, 0), S::kRun) : 0;
+  const auto inside = [&](int64_t end) {
+    const int64_t left = end - l.t0;
+    return !live || left < 0 ? 0 : left < S::kRun ? (int)left : S::kRun;
+  };
+  l.n = inside(n), l.rows = inside(a.T);
 #pragma unroll
   for (int c = 0; c < S::kPer; ++c) l.rate[c] = live ? log_rate(a.rate, l.c0 + c) : -0.0f;
   return l;
+}
+// has(t) for a run's tokens that count, none(t) for the others; a whole run asks once.
+template <class S, class Has, class None>
+__device__ __forceinline__ void with_tokens(const LaneAt<S>& l, Has&& has, None&& none) {
+  if (l.n == S::kRun) {
+#pragma unroll
+    for (int t = 0; t < S::kRun; ++t) has(t);
+  } else {
+#pragma unroll
+    for (int t = 0; t < S::kRun; ++t) {
+      none(t);
+      if (t < l.n) has(t);
+    }
+  }
+}
+// And for what is stored: none(t) for the rows behind the last token, as far as T.
+template <class S, class Has, class None>
+__device__ __forceinline__ void put_tokens(const LaneAt<S>& l, Has&& has, None&& none) {
+  if (l.n == S::kRun) {
+#pragma unroll
+    for (int t = 0; t < S::kRun; ++t) has(t);
+  } else {
+#pragma unroll
+    for (int t = 0; t < S::kRun; ++t) {
+      if (t < l.n)
+        has(t);
+      else if (t < l.rows)
+        none(t);
+    }
+  }
 }
 template <class S>
 __device__ __forceinline__ const typename S::T* row_of(const RecOperand& o, const LaneAt<S>& l) {
@@ -401,16 +442,14 @@ rec_forward_kernel(RecArgs a, Links links, const float* s_in, float* s_out, T* _
   const LaneAt<S> l = lane_at<S>(a, at);
   uint4 vx[S::kRun], vg[S::kRun], vi[S::kRun];
   const T *x = row_of(a.x, l), *g = row_of(a.decay, l), *in = row_of(a.input, l);
-#pragma unroll
-  for (int t = 0; t < S::kRun; ++t) {
+  with_tokens(l, [&](int t) {
+    vg[t] = get16(g + t * a.decay.st);
+    vi[t] = get16(in + t * a.input.st);
+    vx[t] = get16(x + t * a.x.st);
+  }, [&](int t) {
     vg[t] = no_token<T>();
     vx[t] = vi[t] = make_uint4(0, 0, 0, 0);
-    if (t < l.n) {
-      vg[t] = get16(g + t * a.decay.st);
-      vi[t] = get16(in + t * a.input.st);
-      vx[t] = get16(x + t * a.x.st);
-    }
-  }
+  });
   // Inside a run of a few tokens a itself will do; from run to run the sum of z counts.
   float dec[S::kRun][S::kPer], u[S::kRun][S::kPer], Z[S::kPer], H[S::kPer];
 #pragma unroll
@@ -437,17 +476,11 @@ rec_forward_kernel(RecArgs a, Links links, const float* s_in, float* s_out, T* _
 #pragma unroll
   for (int c = 0; c < S::kPer; ++c) s[c] = rs.h[l.run][l.lane * S::kPer + c];
   T* out = h + l.b * hsb + l.t0 * hst + l.c0;
+  put_tokens(l, [&](int t) {
 #pragma unroll
-  for (int t = 0; t < S::kRun; ++t) {
-    if (t >= l.rows) break;
-    float f[S::kPer];
-#pragma unroll
-    for (int c = 0; c < S::kPer; ++c) {
-      s[c] = __builtin_fmaf(dec[t][c], s[c], u[t][c]);
-      f[c] = t < l.n ? s[c] : 0.0f;
-    }
-    Lane<T>::put(out + t * hst, f);
-  }
+    for (int c = 0; c < S::kPer; ++c) s[c] = __builtin_fmaf(dec[t][c], s[c], u[t][c]);
+    Lane<T>::put(out + t * hst, s);
+  }, [&](int t) { *reinterpret_cast<uint4*>(out + t * hst) = make_uint4(0, 0, 0, 0); });
 }
 
 // The gradients of a tile, from the saved state in front of it; the tile's sums of
@@ -470,17 +503,15 @@ rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, con
     uint4 vg[S::kRun], vi[S::kRun];
     const T *x = row_of(a.x, l), *g = row_of(a.decay, l), *in = row_of(a.input, l),
             *dh = row_of(a.dh, l);
-#pragma unroll
-    for (int t = 0; t < S::kRun; ++t) {
+    with_tokens(l, [&](int t) {
+      vg[t] = get16(g + t * a.decay.st);
+      vi[t] = get16(in + t * a.input.st);
+      vx[t] = get16(x + t * a.x.st);
+      vd[t] = get16(dh + t * a.dh.st);
+    }, [&](int t) {
       vg[t] = no_token<T>();
       vx[t] = vi[t] = vd[t] = make_uint4(0, 0, 0, 0);
-      if (t < l.n) {
-        vg[t] = get16(g + t * a.decay.st);
-        vi[t] = get16(in + t * a.input.st);
-        vx[t] = get16(x + t * a.x.st);
-        vd[t] = get16(dh + t * a.dh.st);
-      }
-    }
+    });
     // C: what comes from behind the run, from 0: the sum of its dh, each through the decays
     // up to its token (A)
     float Z[S::kPer], H[S::kPer], C[S::kPer], A[S::kPer];
@@ -551,17 +582,17 @@ rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, con
       for (int t = S::kRun - 1; t >= 0; --t) {
         const float x = chunk_value<T>(vx[t], k), lam = chunk_value<T>(vd[t], k) + c;
         // y = l a (h - i x a / b), with i = (b i) / b; where b is 0 so is what they stand
-        // beside (2^62: above all others, and finite)
+        // beside (1 / b counts as 2^94: above all others, and finite)
         const float al = dec[t] * lam;
-        const float inv = fminf(__builtin_amdgcn_rsqf(root_arg(l.rate[k] * r[t][k], dec[t])),
-                                0x1p62f) * 0x1p32f;
+        const float inv =
+            __builtin_amdgcn_rsqf(root_arg(l.rate[k] * r[t][k], dec[t], 0x1p-124f)) * 0x1p32f;
         const float i = bi[t][k] * inv;
         const float y = al * __builtin_fmaf(-dec[t], i * x * inv, s[t]);
         const float yr = t < l.n ? y * r[t][k] : 0.0f;
         fx[t][q] = lam * bi[t][k];
-        fi[t][q] = fx[t][q] * x * (1.0f - i);
-        fg[t][q] = yr * (l.rate[k] * (1.0f / kLog2e)) * (1.0f - r[t][k]);
-        if (t >= l.n) fx[t][q] = fi[t][q] = fg[t][q] = 0.0f;
+        const float fxx = fx[t][q] * x, yz = yr * (l.rate[k] * (1.0f / kLog2e));
+        fi[t][q] = __builtin_fmaf(-fxx, i, fxx);
+        fg[t][q] = __builtin_fmaf(-yz, r[t][k], yz);
         dr -= yr;
         c = al;
       }
@@ -577,16 +608,15 @@ rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, con
     }
   }
   const int64_t row = (l.b * a.T + l.t0) * a.d + l.c0;
-  const auto put = [&](T* p, const uint32_t* o) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+  const auto put = [&](T* p, int t, const uint32_t* o) {
+    *reinterpret_cast<uint4*>(p + row + t * a.d) = make_uint4(o[0], o[1], o[2], o[3]);
   };
-#pragma unroll
-  for (int t = 0; t < S::kRun; ++t) {
-    if (t >= l.rows) break;
-    put(dx + row + t * a.d, ox[t]);
-    put(dg + row + t * a.d, og[t]);
-    put(di + row + t * a.d, oi[t]);
-  }
+  put_tokens(l, [&](int t) {
+    put(dx, t, ox[t]), put(dg, t, og[t]), put(di, t, oi[t]);
+  }, [&](int t) {
+    const uint32_t none[4] = {0, 0, 0, 0};
+    put(dx, t, none), put(dg, t, none), put(di, t, none);
+  });
   __syncthreads();
   const int64_t ch = at.strip * kStrip + threadIdx.x;
   if (threadIdx.x < kStrip && ch < a.d) {
