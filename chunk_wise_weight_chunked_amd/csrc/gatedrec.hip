@@ -30,8 +30,6 @@ namespace ttt {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kForward = 256;   // threads of a tile
-constexpr int kBackward = 256;
 constexpr int kStrip = 64;  // channels of a tile
 
 // Exponents are base 2 throughout: z is log2 a = -rate log2(e) r.
@@ -124,7 +122,8 @@ template <typename T>
 __device__ __forceinline__ uint4 get16(const T* p) { return *reinterpret_cast<const uint4*>(p); }
 
 // Lane layout of a tile on kThreads: kLanes lanes across the strip's channels, kRuns
-// runs of kRun tokens.
+// runs of kRun tokens.  kRecTile tokens have kBlock threads; a call of fewer tokens than a
+// half or a quarter of that, one tile a sequence, as many fewer.
 template <typename T_, int kThreads_>
 struct TileLayout {
   using T = T_;
@@ -132,7 +131,8 @@ struct TileLayout {
   static constexpr int kPer = Lane<T>::kPer;
   static constexpr int kLanes = kStrip / kPer;
   static constexpr int kRuns = kThreads / kLanes;
-  static constexpr int kRun = kRecTile / kRuns;
+  static constexpr int kTile = kRecTile * kThreads / kBlock;  // tokens
+  static constexpr int kRun = kTile / kRuns;
   static constexpr int kParts = kThreads / 64;  // waves, each folds kRuns / kParts runs
 };
 
@@ -142,7 +142,8 @@ __device__ __forceinline__ int64_t tokens_of(const RecArgs& a, int64_t b) {
   return n < 0 ? 0 : n > a.T ? a.T : n;
 }
 
-// The recurrent form: a lane walks the tokens of its channels.
+// The recurrent form: a lane walks the tokens of its channels, kStepAhead loaded at a time.
+constexpr int kStepAhead = 4;
 template <typename T>
 __global__ __launch_bounds__(kBlock) void rec_step_kernel(RecArgs a, const float* s_in,
                                                           float* s_out, T* __restrict__ h,
@@ -168,22 +169,32 @@ __global__ __launch_bounds__(kBlock) void rec_step_kernel(RecArgs a, const float
   const T* g = static_cast<const T*>(a.decay.p) + b * a.decay.sb + c0;
   const T* in = static_cast<const T*>(a.input.p) + b * a.input.sb + c0;
   T* out = h + b * hsb + c0;
-  for (int64_t t = 0; t < a.T; ++t) {
-    float f[kPer];
-    if (t < n) {
-      const uint4 vx = get16(x + t * a.x.st), vg = get16(g + t * a.decay.st),
-                  vi = get16(in + t * a.input.st);
+  for (int64_t t0 = 0; t0 < a.T; t0 += kStepAhead) {
+    uint4 vx[kStepAhead], vg[kStepAhead], vi[kStepAhead];
+#pragma unroll
+    for (int i = 0; i < kStepAhead; ++i) {
+      vx[i] = vg[i] = vi[i] = make_uint4(0, 0, 0, 0);
+      if (t0 + i < n) {
+        vx[i] = get16(x + (t0 + i) * a.x.st);
+        vg[i] = get16(g + (t0 + i) * a.decay.st);
+        vi[i] = get16(in + (t0 + i) * a.input.st);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kStepAhead; ++i) {
+      if (t0 + i >= a.T) break;
+      if (t0 + i >= n) {
+        *reinterpret_cast<uint4*>(out + (t0 + i) * hst) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
 #pragma unroll
       for (int c = 0; c < kPer; ++c) {
-        const float z = rate[c] * sigmoid(chunk_value<T>(vg, c));
-        const float u = gated(z, __builtin_amdgcn_exp2f(z), chunk_value<T>(vi, c));
-        f[c] = s[c] = decayed(decay_of(z), s[c], u * chunk_value<T>(vx, c));
+        const float z = rate[c] * sigmoid(chunk_value<T>(vg[i], c));
+        const float u = gated(z, __builtin_amdgcn_exp2f(z), chunk_value<T>(vi[i], c));
+        s[c] = decayed(decay_of(z), s[c], u * chunk_value<T>(vx[i], c));
       }
-    } else {
-#pragma unroll
-      for (int c = 0; c < kPer; ++c) f[c] = 0.0f;
+      Lane<T>::put(out + (t0 + i) * hst, s);
     }
-    Lane<T>::put(out + t * hst, f);
   }
   if (s_out) {
 #pragma unroll
@@ -296,7 +307,7 @@ __device__ __forceinline__ LaneAt<S> lane_at(const RecArgs& a, const TileAt& at)
   l.lane = threadIdx.x % S::kLanes, l.run = threadIdx.x / S::kLanes;
   l.b = at.b, l.j = at.j;
   l.c0 = at.strip * kStrip + l.lane * S::kPer;
-  l.t0 = at.j * kRecTile + l.run * S::kRun;
+  l.t0 = at.j * S::kTile + l.run * S::kRun;
   const bool live = l.c0 < a.d;
   const int64_t n = tokens_of(a, at.b);
   const auto inside = [&](int64_t end) {
@@ -367,7 +378,7 @@ __device__ __forceinline__ void put_run(Runs<S>& rs, const LaneAt<S>& l, const f
 // h: the waves fold their runs, the first wave folds the waves' and links the tile with
 // the ones before it, the waves go through their runs once more.  first: the state of
 // the channel in front of the first tile; done(channel, state in front of the tile,
-// state behind it) in the first wave; beside(channel) in the second one meanwhile.
+// state behind it) in the first wave; beside(channel) in the last one, meanwhile if it is another.
 template <bool kReverse, class S, class First, class Done, class Beside>
 __device__ __forceinline__ void link_tile(Runs<S>& rs, const RecArgs& a, const Links& links,
                                           const TileAt& at, First&& first, Done&& done,
@@ -418,7 +429,7 @@ __device__ __forceinline__ void link_tile(Runs<S>& rs, const RecArgs& a, const L
     }
     done(c, before, decayed(whole, before, ph));
   }
-  if (wave == 1 && c < a.d) beside(c);
+  if (wave == kParts - 1 && c < a.d) beside(c);
   __syncthreads();
   float s = rs.part_h[wave][ch];
 #pragma unroll
@@ -432,11 +443,11 @@ __device__ __forceinline__ void link_tile(Runs<S>& rs, const RecArgs& a, const L
 }
 
 // A tile's outputs.
-template <typename T>
-__global__ __launch_bounds__(kForward) __attribute__((amdgpu_waves_per_eu(4))) void
+template <typename T, int kThreads>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 4 : 3))) void
 rec_forward_kernel(RecArgs a, Links links, const float* s_in, float* s_out, T* __restrict__ h,
                    int64_t hsb, int64_t hst, float* __restrict__ saved) {
-  using S = TileLayout<T, kForward>;
+  using S = TileLayout<T, kThreads>;
   __shared__ Runs<S> rs;
   const TileAt at = tile_at(a, links, false);
   const LaneAt<S> l = lane_at<S>(a, at);
@@ -487,12 +498,12 @@ rec_forward_kernel(RecArgs a, Links links, const float* s_in, float* s_out, T* _
 // drate in `part` [B][tiles][d].  A lane holds its tokens' x and dh as loaded, and their
 // r and b i; it goes through its channels one after the other at the end, so that
 // the states and results of few are in registers beside them.
-template <typename T>
-__global__ __launch_bounds__(kBackward) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 3 : 2))) void
+template <typename T, int kThreads>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 3 : 2))) void
 rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, const float* ds_out,
                     float* ds_in, T* __restrict__ dx, T* __restrict__ dg, T* __restrict__ di,
                     float* __restrict__ part) {
-  using S = TileLayout<T, kBackward>;
+  using S = TileLayout<T, kThreads>;
   __shared__ Runs<S> rs;
   __shared__ __attribute__((aligned(16))) float hs[S::kRuns][kStrip];
   const TileAt at = tile_at(a, links, true);
@@ -627,31 +638,36 @@ rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, con
   }
 }
 
-// out[c] = sum over rows of part [rows][d]: 64 columns a workgroup, 16 lanes of
-// rows.
+// out[slice][c] = sum over a slice's rows of part [rows][d]: 16 columns a workgroup, 64 lanes
+// of rows.
+constexpr int64_t kRateSlice = 2048;
+constexpr int kRateRows = 64, kRateCols = 4 * kBlock / kRateRows;
 __global__ __launch_bounds__(kBlock) void rec_rate_kernel(const float* __restrict__ part,
                                                           float* __restrict__ out, int64_t rows,
-                                                          int64_t d) {
-  __shared__ float4 s[16][16];
-  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
-  const int64_t c = blockIdx.x * (int64_t)64 + cx * 4;
+                                                          int64_t slice, int64_t d) {
+  __shared__ float4 s[kRateRows][kRateCols / 4];
+  const int cx = threadIdx.x % (kRateCols / 4), ry = threadIdx.x / (kRateCols / 4);
+  const int64_t c = blockIdx.x * (int64_t)kRateCols + cx * 4, r0 = blockIdx.y * slice;
+  const int64_t end = rows - r0 < slice ? rows : r0 + slice;
   float4 a = make_float4(0, 0, 0, 0);
   if (c < d) {
 #pragma unroll 4
-    for (int64_t r = ry; r < rows; r += 16) {
+    for (int64_t r = r0 + ry; r < end; r += kRateRows) {
       const float4 p = *reinterpret_cast<const float4*>(part + r * d + c);
       a.x += p.x, a.y += p.y, a.z += p.z, a.w += p.w;
     }
   }
   s[ry][cx] = a;
-  __syncthreads();
-  if (ry == 0 && c < d) {
-    for (int i = 1; i < 16; ++i) {
-      const float4 p = s[i][cx];
+#pragma unroll
+  for (int n = kRateRows / 2; n > 0; n /= 2) {
+    __syncthreads();
+    if (ry < n) {
+      const float4 p = s[ry + n][cx];
       a.x += p.x, a.y += p.y, a.z += p.z, a.w += p.w;
+      s[ry][cx] = a;
     }
-    *reinterpret_cast<float4*>(out + c) = a;
   }
+  if (ry == 0 && c < d) *reinterpret_cast<float4*>(out + blockIdx.y * d + c) = a;
 }
 
 int64_t tiles_of(const RecArgs& a) { return (a.T + kRecTile - 1) / kRecTile; }
@@ -660,6 +676,24 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 template <typename F>
 hipError_t with_type(Dtype dt, F&& f) {
   return dt == Dtype::F32 ? f(float{}) : f(uint16_t{});
+}
+// Whether a call takes the recurrent form.  A lane's tokens take it 0.8 us each, or what
+// the memory takes for them; a tile takes 8 us whatever it holds, and many at once 2.5 ns
+// each.  us of 2560 channels, recurrent / tiles: 1 sequence of 8 tokens 9.9 / 8.4, 64 of 4 8.4 /
+// 10.3, 64 of 6 9.0 / 10.7, 64 of 8 10.6 / 10.4, 64 of 12 14.7 / 10.6, 512 of 8 27 / 49, 512 of
+// 16 48 / 53.
+bool steps(const RecArgs& a) { return a.T <= (a.B * a.d >= ((int64_t)1 << 20) ? 16 : 6); }
+
+// f with the threads of a tile of a call (64 sequences of 32 tokens of 2560 channels 13.6 us,
+// 25 in tiles of 128; 64 tokens 20.8 and 26.3; 512 of 32 tokens 79.5 and 172).
+template <typename F>
+void with_threads(const RecArgs& a, F&& f) {
+  if (a.T * 4 <= kRecTile)
+    f(std::integral_constant<int, kBlock / 4>{});
+  else if (a.T * 2 <= kRecTile)
+    f(std::integral_constant<int, kBlock / 2>{});
+  else
+    f(std::integral_constant<int, kBlock>{});
 }
 
 }  // namespace
@@ -686,6 +720,12 @@ hipError_t clear_links(const RecArgs& a, void* ws, Links* links, hipStream_t s) 
 dim3 tile_grid(const RecArgs& a) {
   return dim3((unsigned)(a.B * tiles_of(a) * ((a.d + kStrip - 1) / kStrip)));
 }
+// Slices of the tiles' sums of drate: more than one, added up by a launch of its own, where
+// one workgroup's loads would show.
+int64_t rate_slices(const RecArgs& a) {
+  const int64_t rows = a.B * tiles_of(a);
+  return rows <= kRateSlice ? 1 : (rows + kRateSlice - 1) / kRateSlice;
+}
 }  // namespace
 
 size_t gatedrec_forward_bytes(const RecArgs& a) { return link_bytes(a); }
@@ -696,7 +736,7 @@ hipError_t launch_gatedrec_forward(const RecArgs& a, const float* s_in, float* s
   return with_type(a.dt, [&](auto t) {
     using T = decltype(t);
     T* out = static_cast<T*>(h);
-    if (a.T <= kRecStepTokens) {
+    if (steps(a)) {
       const int64_t n = a.B * (a.d / Lane<T>::kPer);
       rec_step_kernel<T><<<dim3((unsigned)((n + kBlock - 1) / kBlock)), kBlock, 0, s>>>(
           a, s_in, s_out, out, hsb, hst, saved);
@@ -705,15 +745,19 @@ hipError_t launch_gatedrec_forward(const RecArgs& a, const float* s_in, float* s
     Links links;
     const hipError_t e = clear_links(a, ws, &links, s);
     if (e != hipSuccess) return e;
-    rec_forward_kernel<T><<<tile_grid(a), kForward, 0, s>>>(a, links, s_in, s_out, out, hsb, hst,
+    with_threads(a, [&](auto threads) {
+      constexpr int n = decltype(threads)::value;
+      rec_forward_kernel<T, n><<<tile_grid(a), n, 0, s>>>(a, links, s_in, s_out, out, hsb, hst,
                                                           saved);
+    });
     return hipGetLastError();
   });
 }
 
-// The links, and the tiles' sums of drate.
+// The links, the tiles' sums of drate, and their slices' sums.
 size_t gatedrec_backward_bytes(const RecArgs& a) {
-  return link_bytes(a) + (size_t)(a.B * tiles_of(a) * a.d) * sizeof(float);
+  const int64_t rows = a.B * tiles_of(a), slices = rate_slices(a);
+  return link_bytes(a) + (size_t)((rows + (slices > 1 ? slices : 0)) * a.d) * sizeof(float);
 }
 
 hipError_t launch_gatedrec_backward(const RecArgs& a, const float* saved, const float* ds_out,
@@ -725,11 +769,19 @@ hipError_t launch_gatedrec_backward(const RecArgs& a, const float* saved, const 
     const hipError_t e = clear_links(a, ws, &links, s);
     if (e != hipSuccess) return e;
     float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + link_bytes(a));
-    rec_backward_kernel<T><<<tile_grid(a), kBackward, 0, s>>>(
-        a, links, saved, ds_out, ds_in, static_cast<T*>(dx), static_cast<T*>(ddecay),
-        static_cast<T*>(dinput), part);
-    rec_rate_kernel<<<dim3((unsigned)((a.d + 63) / 64)), kBlock, 0, s>>>(part, drate,
-                                                                         a.B * links.tiles, a.d);
+    with_threads(a, [&](auto threads) {
+      constexpr int n = decltype(threads)::value;
+      rec_backward_kernel<T, n><<<tile_grid(a), n, 0, s>>>(
+          a, links, saved, ds_out, ds_in, static_cast<T*>(dx), static_cast<T*>(ddecay),
+          static_cast<T*>(dinput), part);
+    });
+    const unsigned columns = (unsigned)((a.d + kRateCols - 1) / kRateCols);
+    const int64_t rows = a.B * links.tiles, slices = rate_slices(a);
+    float* const sums = slices > 1 ? part + rows * a.d : drate;
+    rec_rate_kernel<<<dim3(columns, (unsigned)slices), kBlock, 0, s>>>(
+        part, sums, rows, slices > 1 ? kRateSlice : rows, a.d);
+    if (slices > 1)
+      rec_rate_kernel<<<dim3(columns), kBlock, 0, s>>>(sums, drate, slices, slices, a.d);
     return hipGetLastError();
   });
 }

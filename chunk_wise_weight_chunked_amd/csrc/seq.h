@@ -26,7 +26,6 @@ hipError_t launch_embed_backward(const EmbedArgs& a, const void* ids, const void
 
 // ------------------------------------------------- gated linear recurrence
 constexpr int kRecTile = 128;     // tokens of a tile: a state is saved in front of each
-constexpr int kRecStepTokens = 8; // tokens of a call that runs without tiles, at most
 
 // One [B][T][d] operand, channels contiguous.
 struct RecOperand {

@@ -177,9 +177,10 @@ def test_embed_backward_infinities_stay_in_their_rows():
 
 
 # ----------------------------------------------------- gated linear recurrence
-# (B, T, d): up to 8 tokens without tiles; part of a tile, whole ones, many; one strip of
-# 64 channels, parts of one, several
-REC_SHAPES = [(1, 1, 8), (3, 1, 200), (2, 5, 64), (1, 8, 72), (2, 9, 8), (1, 31, 64), (2, 100, 136),
+# (B, T, d): few tokens without tiles; one tile of up to 32, 64 or 128 tokens, many tiles; one
+# strip of 64 channels, parts of one, several
+REC_SHAPES = [(1, 1, 8), (3, 1, 200), (2, 5, 64), (2, 6, 72), (3, 7, 64), (1, 8, 72), (2, 9, 8),
+              (1, 31, 64), (3, 32, 136), (2, 33, 64), (3, 64, 72), (1, 65, 8), (2, 100, 136),
               (1, 127, 64), (3, 128, 72), (1, 129, 8), (2, 257, 64), (1, 700, 200), (2, 1100, 64),
               (1, 4500, 72)]
 
@@ -258,6 +259,41 @@ def test_gatedrec_lengths(T, dtype):
         if state is not None:
             assert torch.equal(S[0], st[0]) and torch.equal(S[5], st[5])  # no tokens
             assert torch.equal(got["state"][0], ds[0])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [7, 16, 17, 33, 65])
+def test_gatedrec_many_sequences(T, dtype):
+    """More of them than workgroups fit the chip, of which some are looked at."""
+    B, d = 1 << 17, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    new = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, dg, ig, dh = (new(B, T, d).to(dtype) for _ in range(4))
+    rate, st, ds = new(d).abs() + 0.05, new(B, d), new(B, d)
+    ln = torch.randint(0, T + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    h, S, saved = seq.gatedrec_forward(x, dg, ig, rate, state=st, lengths=ln, save=True)
+    got = seq.gatedrec_backward(x, dg, ig, rate, dh, saved, dstate_out=ds, lengths=ln)
+    some = torch.cat([torch.arange(40), torch.randint(0, B, (100,), generator=gen(T)),
+                      torch.arange(B - 40, B)]).cuda()
+    lens = ln[some].tolist()
+    a = [f64(t[some]) for t in (x, dg, ig)]
+    h64, S64 = ref.gatedrec(*a, f64(rate), f64(st[some]), lens)
+    assert rel(f64(h[some]), h64) <= TOL[dtype] and rel(f64(S[some]), S64) <= TOL_F32
+    want = ref.gatedrec_grads(*a, f64(rate), f64(dh[some]), f64(st[some]), f64(ds[some]), lens)
+    for name, w in zip(("x", "decay_gate", "input_gate"), want):
+        assert rel(f64(got[name][some]), w) <= TOL[dtype], name
+    assert rel(f64(got["state"][some]), want[4]) <= TOL_F32
+    # the rest by calls of their own, and the rate's gradient as their sum
+    drate = torch.zeros(d, dtype=torch.float64, device="cuda")
+    for p in torch.arange(B, device="cuda").split(B // 4):
+        own = [t[p].contiguous() for t in (x, dg, ig)]
+        h2, S2, saved2 = seq.gatedrec_forward(*own, rate, state=st[p], lengths=ln[p], save=True)
+        assert rel(f64(h2), f64(h[p])) <= TOL[dtype] and rel(f64(S2), f64(S[p])) <= TOL_F32
+        own = seq.gatedrec_backward(*own, rate, dh[p], saved2, dstate_out=ds[p], lengths=ln[p])
+        assert all(torch.equal(own[n], got[n][p]) for n in ("x", "decay_gate", "input_gate", "state"))
+        drate += own["rate"].double()
+    assert rel(f64(got["rate"]), f64(drate)) <= TOL_F32
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
