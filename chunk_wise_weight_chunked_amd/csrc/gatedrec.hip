@@ -15,8 +15,8 @@
 // h -> e^Z h + H with Z the sum of its z: two numbers a channel, that compose.
 //
 // Both directions are bound by HBM and read their inputs once: a workgroup loads a
-// tile, publishes its map, takes the state in front of it from the tiles in front (from the
-// nearest that knows its own, through the maps of those between) and writes the tile's
+// tile, publishes its map, takes the state in front of it from the tiles in front (through
+// their maps, from the nearest place whose state is known) and writes the tile's
 // results from its registers.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -47,6 +47,15 @@ __device__ __forceinline__ float decay_of(float z) {
   return z > -0.5f ? near : far;  // a z of -0 gives -0
 }
 __device__ __forceinline__ bool near_one(float dec) { return __float_as_uint(dec) >> 31; }
+// The decay over two runs.
+__device__ __forceinline__ float decay_both(float d1, float d2) {
+  const bool n1 = near_one(d1), n2 = near_one(d2);
+  // a1 a2 - 1, never positive, and a1 a2 where that is far from 0
+  const float near = -fabsf(__builtin_fmaf(d1, d2, d1 + d2));
+  const float both = near < -0.5f ? 1.0f + near : near;
+  const float far = __builtin_fmaf(d1, d2, n1 ? d2 : n2 ? d1 : 0.0f);
+  return n1 && n2 ? both : far;
+}
 // a h + u
 __device__ __forceinline__ float decayed(float dec, float h, float u) {
   return __builtin_fmaf(dec, h, u) + (near_one(dec) ? h : 0.0f);
@@ -203,11 +212,18 @@ __global__ __launch_bounds__(kBlock) void rec_step_kernel(RecArgs a, const float
 }
 
 // ------------------------------------------------- tiles and what links them
-// A tile's word for the tiles behind it (backward: in front of it), one for each
-// channel: the decay over the tile and the state behind it from 0, or once it is known
-// the state behind it, marked by +inf, which no decay is.  Both halves come and go in
-// one 64-bit access, so a word needs no other ordering; it starts as kUnset, a NaN that
-// no decay is stored as.
+// A tile leaves a word for the tiles behind it (backward: in front of it), one for each
+// channel: its map, the decay over the tile and the state behind it from 0.  kGroup tiles
+// make a group, whose word is the group's map or, once it is known, the state behind it,
+// marked by +inf, which no decay is.  So the state in front of a tile comes through the
+// groups in front of its own, from the nearest that has its state, and through its own group's
+// maps: always by the same products, whatever was there first, and over 48 tiles in the
+// time that a word takes from one workgroup to another (about 1 us: 131072 tokens of 64
+// channels take 45 us, 133 where tiles take their states from the 8 in front of them;
+// 32768 of 200 with gradients 89 and 118, of 2560 440 and 434).
+// Both halves of a word come and go in one 64-bit access, so it needs no other ordering; it
+// starts as kUnset, a NaN that no decay is stored as.
+constexpr int kGroup = 8;
 constexpr uint64_t kUnset = ~0ull;
 constexpr uint32_t kState = 0x7f800000u;
 __device__ __forceinline__ uint64_t word_of(float dec, float h) {
@@ -234,9 +250,10 @@ __global__ __launch_bounds__(kBlock) void rec_clear_kernel(uint4* __restrict__ w
 }
 
 struct Links {
-  uint64_t* words;   // [B][tiles][d], null where there is one tile
+  uint64_t* maps;    // [B][tiles][d], null where there is one tile
+  uint64_t* states;  // [B][groups][d]: group g's has the word of g - 1, the first one a state
   uint32_t* begun;
-  int64_t tiles;
+  int64_t tiles, groups;
 };
 
 // The workgroup's tile.  Tiles are handed out in the order in which workgroups begin,
@@ -249,7 +266,7 @@ struct TileAt {
 __device__ __forceinline__ TileAt tile_at(const RecArgs& a, const Links& links, bool reverse) {
   __shared__ uint32_t ticket;
   uint32_t w = blockIdx.x;
-  if (links.words) {
+  if (links.maps) {
     if (threadIdx.x == 0)
       ticket = __hip_atomic_fetch_add(links.begun, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
@@ -265,18 +282,43 @@ __device__ __forceinline__ TileAt tile_at(const RecArgs& a, const Links& links, 
   return at;
 }
 
-// The state in front of tile k of a channel (k > 0), from the words of tiles k - 1,
-// k - 2, ... at `word`, `step` words apart: from the nearest of kAhead that has its
-// state, the tiles behind that one applied in order, just as they do it themselves, so
-// that the result does not depend on which one it was.  The wait ends by itself (tile_at);
-// only where another call clears the same words meanwhile, which no workspace allows, it
-// ends here, after some seconds and with NaN.
+// Waits end by themselves (tile_at); only where another call clears the same words
+// meanwhile, which no workspace allows, they end here, after some seconds and with NaN.
+constexpr int kTries = 1 << 22;
+
+// The map over a group's first n tiles (1 <= n < kGroup), from their words, `step` words apart.
+__device__ __forceinline__ void map_before(const uint64_t* word, int64_t step, int n, float* dec,
+                                           float* h) {
+  for (int tries = 0; tries < kTries; ++tries) {
+    uint64_t w[kGroup - 1];
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i)
+      if (i < n) w[i] = get_word(word + i * step);
+    bool all = true;
+    *dec = -0.0f, *h = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i) {
+      if (i >= n) break;
+      const float d = __uint_as_float((uint32_t)(w[i] >> 32));
+      all = all && w[i] != kUnset;
+      *dec = decay_both(*dec, d);
+      *h = decayed(d, *h, __uint_as_float((uint32_t)w[i]));
+    }
+    if (all) return;
+    __builtin_amdgcn_s_sleep(1);
+  }
+  *dec = *h = __builtin_nanf("");
+}
+
+// The state in front of a group, from its word and those of the k groups in front of it at
+// `word`, `word` - step, ...: from the nearest of kAhead that is a state, the maps behind
+// that one applied in order.
 __device__ __forceinline__ float state_before(const uint64_t* word, int64_t step, int64_t k) {
-  constexpr int kAhead = 8, kTries = 1 << 22;
+  constexpr int kAhead = 6;
   for (int tries = 0; tries < kTries; ++tries) {
     uint64_t w[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) w[i] = get_word(word + (i < k ? i : k - 1) * step);
+    for (int i = 0; i < kAhead; ++i) w[i] = get_word(word - (i < k ? i : k) * step);
     bool found = false;
     float s = 0.0f;
 #pragma unroll
@@ -290,6 +332,32 @@ __device__ __forceinline__ float state_before(const uint64_t* word, int64_t step
     __builtin_amdgcn_s_sleep(1);
   }
   return __builtin_nanf("");
+}
+
+// The state in front of a tile of a channel, from the tile's map: what the tiles behind it
+// need is left to them, as soon as it is known.
+template <class First>
+__device__ __forceinline__ float link(const Links& links, const TileAt& at, int64_t d, int64_t c,
+                                      float dec, float h, First&& first) {
+  const int64_t g = at.k / kGroup;
+  const int in = (int)(at.k % kGroup);
+  uint64_t* const map = links.maps + (at.b * links.tiles + at.k) * d + c;
+  uint64_t* const state = links.states + (at.b * links.groups + g) * d + c;
+  const bool last = in == kGroup - 1 && g + 1 < links.groups;
+  if (in < kGroup - 1 && at.k + 1 < links.tiles) put_word(map, word_of(dec, h));
+  float before = -0.0f, from0 = 0.0f;  // the map over the group's tiles in front
+  if (in > 0) map_before(map - in * d, d, in, &before, &from0);
+  const float all = decay_both(before, dec), all0 = decayed(dec, from0, h);
+  if (last) put_word(state + d, word_of(all, all0));
+  float s;
+  if (at.k == 0) {
+    s = first(c);
+    put_word(state, state_word(s));
+  } else {
+    s = state_before(state, d, g);
+  }
+  if (last) put_word(state + d, state_word(decayed(all, s, all0)));
+  return in > 0 ? decayed(before, s, from0) : s;
 }
 
 // What a lane of a tile works on.
@@ -407,19 +475,7 @@ __device__ __forceinline__ void link_tile(Runs<S>& rs, const RecArgs& a, const L
       z += zp;
     }
     const float whole = decay_of(z);
-    float s;
-    if (links.words) {
-      uint64_t* const word = links.words + (at.b * links.tiles + at.k) * a.d + c;
-      if (at.k == 0) {
-        s = first(c);
-      } else {
-        if (at.k + 1 < links.tiles) put_word(word, word_of(whole, ph));
-        s = state_before(word - a.d, -a.d, at.k);
-      }
-      if (at.k + 1 < links.tiles) put_word(word, state_word(decayed(whole, s, ph)));
-    } else {
-      s = first(c);
-    }
+    float s = links.maps ? link(links, at, a.d, c, whole, ph, first) : first(c);
     const float before = s;
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
@@ -671,6 +727,7 @@ __global__ __launch_bounds__(kBlock) void rec_rate_kernel(const float* __restric
 }
 
 int64_t tiles_of(const RecArgs& a) { return (a.T + kRecTile - 1) / kRecTile; }
+int64_t groups_of(int64_t tiles) { return (tiles + kGroup - 1) / kGroup; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <typename F>
@@ -698,19 +755,21 @@ void with_threads(const RecArgs& a, F&& f) {
 
 }  // namespace
 
-// The words that link the tiles, and behind them the counter.
+// The words that link the tiles and groups, and behind them the counter.
 size_t link_bytes(const RecArgs& a) {
-  return tiles_of(a) > 1 ? align256((size_t)(a.B * tiles_of(a) * a.d) * sizeof(uint64_t)) + 256 : 0;
+  const int64_t tiles = tiles_of(a), words = a.B * (tiles + groups_of(tiles)) * a.d;
+  return tiles > 1 ? align256((size_t)words * sizeof(uint64_t)) + 256 : 0;
 }
 
 namespace {
 // The workspace's links, cleared.
 hipError_t clear_links(const RecArgs& a, void* ws, Links* links, hipStream_t s) {
-  links->tiles = tiles_of(a);
-  links->words = nullptr, links->begun = nullptr;
+  links->tiles = tiles_of(a), links->groups = groups_of(links->tiles);
+  links->maps = links->states = nullptr, links->begun = nullptr;
   if (links->tiles == 1) return hipSuccess;
   const size_t bytes = link_bytes(a) - 256;
-  links->words = static_cast<uint64_t*>(ws);
+  links->maps = static_cast<uint64_t*>(ws);
+  links->states = links->maps + a.B * links->tiles * a.d;
   links->begun = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + bytes);
   const int64_t n = (int64_t)(bytes / 16);
   rec_clear_kernel<<<dim3((unsigned)std::min<int64_t>((n + kBlock - 1) / kBlock, 2048)), kBlock, 0,

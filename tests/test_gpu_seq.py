@@ -841,12 +841,15 @@ def test_gatedrec_sequences_beyond_32_bits():
     a = 128 * j
     last = [t[:, a:].contiguous() for t in (x, dg, ig, dh)]
     h2, S2, saved2 = seq.gatedrec_forward(*last[:3], rate, state=saved[:, j].contiguous(), save=True)
-    assert torch.equal(h2, h[:, a:]) and torch.equal(S2, S) and torch.equal(saved2, saved[:, j:])
+    # the state behind a tile comes by the products of its place in the call: each of the two is
+    # off by TOL_F32 at most, and a bf16 result beside a tie by one step, 2^-8, more
+    assert rel(f64(saved2), f64(saved[:, j:])) <= 2 * TOL_F32 and rel(f64(S2), f64(S)) <= 2 * TOL_F32
+    assert rel(f64(h2), f64(h[:, a:])) <= TOL[BF16]
     ds = torch.randn(1, d, generator=g, device="cuda")
     got = seq.gatedrec_backward(x, dg, ig, rate, dh, saved, dstate_out=ds)
     want = seq.gatedrec_backward(*last[:3], rate, last[3], saved2, dstate_out=ds)
     for n in ("x", "decay_gate", "input_gate"):
-        assert torch.equal(got[n][:, a:], want[n]), n
+        assert rel(f64(got[n][:, a:]), f64(want[n])) <= TOL[BF16], n
 
 
 def test_act8_beyond_32_bits():
