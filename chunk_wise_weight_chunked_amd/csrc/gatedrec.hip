@@ -77,8 +77,7 @@ __device__ __forceinline__ float root_arg(float z, float a, float floor) {
 constexpr float kLog2e = 0x1.715476p+0f;
 // -log2(e) rate; z is never positive: a rate below 0 counts as NaN.  2^100 is as good as
 // any above it, and 0 times it is 0.
-__device__ __forceinline__ float log_rate(const float* rate, int64_t c) {
-  const float r = rate[c];
+__device__ __forceinline__ float log_rate(float r) {
   return r >= 0.0f ? -kLog2e * fminf(r, 0x1p100f) : __builtin_nanf("");
 }
 __device__ __forceinline__ float sigmoid(float x) {
@@ -167,7 +166,7 @@ __global__ __launch_bounds__(kBlock) void rec_step_kernel(RecArgs a, const float
   float s[kPer], rate[kPer];
 #pragma unroll
   for (int c = 0; c < kPer; ++c) {
-    rate[c] = log_rate(a.rate, c0 + c);
+    rate[c] = log_rate(a.rate[c0 + c]);
     s[c] = s_in ? s_in[b * a.d + c0 + c] : 0.0f;
   }
   if (saved) {
@@ -270,7 +269,7 @@ __device__ __forceinline__ TileAt tile_at(const RecArgs& a, const Links& links, 
     if (threadIdx.x == 0)
       ticket = __hip_atomic_fetch_add(links.begun, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
-    w = ticket;
+    w = __builtin_amdgcn_readfirstlane(ticket);  // so that what follows from it is scalar
   }
   const uint32_t strips = (uint32_t)((a.d + kStrip - 1) / kStrip), row = strips * (uint32_t)a.B;
   w = min(w, gridDim.x - 1);  // whatever happens to the counter, a tile of this call
@@ -364,54 +363,81 @@ __device__ __forceinline__ float link(const Links& links, const TileAt& at, int6
 template <class S>
 struct LaneAt {
   int64_t b, j, c0, t0;  // t0: its run's first token
+  int64_t last;          // the last token that counts (0 if none does), from t0
   int lane, run;
+  bool live;             // channels inside d; others work on the first ones' and put nothing
+  bool whole;            // the same for the workgroup: all tokens of the tile count
   int n;                 // tokens of its run that count
   int rows;              // tokens of its run inside T
-  float rate[S::kPer];  // as log_rate gives it
+  float rate[S::kPer];   // as given
 };
 template <class S>
 __device__ __forceinline__ LaneAt<S> lane_at(const RecArgs& a, const TileAt& at) {
   LaneAt<S> l;
   l.lane = threadIdx.x % S::kLanes, l.run = threadIdx.x / S::kLanes;
   l.b = at.b, l.j = at.j;
-  l.c0 = at.strip * kStrip + l.lane * S::kPer;
+  const int64_t c0 = at.strip * kStrip + l.lane * S::kPer;
+  l.live = c0 < a.d;
+  l.c0 = l.live ? c0 : 0;
   l.t0 = at.j * S::kTile + l.run * S::kRun;
-  const bool live = l.c0 < a.d;
   const int64_t n = tokens_of(a, at.b);
   const auto inside = [&](int64_t end) {
     const int64_t left = end - l.t0;
-    return !live || left < 0 ? 0 : left < S::kRun ? (int)left : S::kRun;
+    return left < 0 ? 0 : left < S::kRun ? (int)left : S::kRun;
   };
+  l.whole = (at.j + 1) * S::kTile <= n;
+  l.last = (n > 0 ? n - 1 : 0) - l.t0;
   l.n = inside(n), l.rows = inside(a.T);
 #pragma unroll
-  for (int c = 0; c < S::kPer; ++c) l.rate[c] = live ? log_rate(a.rate, l.c0 + c) : -0.0f;
+  for (int c = 0; c < S::kPer; c += 4) {
+    const float4 r = *reinterpret_cast<const float4*>(a.rate + l.c0 + c);
+    l.rate[c] = r.x, l.rate[c + 1] = r.y, l.rate[c + 2] = r.z, l.rate[c + 3] = r.w;
+  }
   return l;
 }
-// has(t) for a run's tokens that count, none(t) for the others; a whole run asks once.
-template <class S, class Has, class None>
-__device__ __forceinline__ void with_tokens(const LaneAt<S>& l, Has&& has, None&& none) {
-  if (l.n == S::kRun) {
-#pragma unroll
-    for (int t = 0; t < S::kRun; ++t) has(t);
-  } else {
-#pragma unroll
-    for (int t = 0; t < S::kRun; ++t) {
-      none(t);
-      if (t < l.n) has(t);
-    }
-  }
+// f(whole): the code of a tile of which all tokens count, and that of the others.  Each for
+// itself up to its sums, so that the work on the first tokens begins when they are there:
+// where the two meet behind the loads, the compiler waits for all of them.
+template <class S, class F>
+__device__ __forceinline__ void on_run(const LaneAt<S>& l, F&& f) {
+  if (l.whole)
+    f(std::true_type{});
+  else
+    f(std::false_type{});
 }
-// And for what is stored: none(t) for the rows behind the last token, as far as T.
-template <class S, class Has, class None>
-__device__ __forceinline__ void put_tokens(const LaneAt<S>& l, Has&& has, None&& none) {
-  if (l.n == S::kRun) {
+// load(t, i) for a run's tokens t, of which it reads the i-th from t0, and none(t) for those
+// that do not count.  All loads come first, without a branch between them: where a token does
+// not count they read the last one that does (or row 0 of a sequence without tokens) for nothing.
+template <bool kWhole, class S, class Load, class None>
+__device__ __forceinline__ void load_tokens(const LaneAt<S>& l, Load&& load, None&& none) {
 #pragma unroll
-    for (int t = 0; t < S::kRun; ++t) has(t);
+  for (int t = 0; t < S::kRun; ++t) load(t, kWhole || t < l.last ? t : l.last);
+  if constexpr (!kWhole) {
+#pragma unroll
+    for (int t = 0; t < S::kRun; ++t)
+      if (t >= l.n) none(t);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+// log_rate of a channel, behind the tokens' loads (and not waited for in front of them).
+template <class S>
+__device__ __forceinline__ float rate_after(const LaneAt<S>& l, int c) {
+  float r = l.rate[c];
+  asm volatile("" : "+v"(r));
+  return log_rate(r);
+}
+// put(t) for a run's tokens, none(t) for the rows behind the last token, as far as T.
+template <class S, class Put, class None>
+__device__ __forceinline__ void put_tokens(const LaneAt<S>& l, Put&& put, None&& none) {
+  if (!l.live) return;
+  if (l.whole) {
+#pragma unroll
+    for (int t = 0; t < S::kRun; ++t) put(t);
   } else {
 #pragma unroll
     for (int t = 0; t < S::kRun; ++t) {
       if (t < l.n)
-        has(t);
+        put(t);
       else if (t < l.rows)
         none(t);
     }
@@ -507,30 +533,38 @@ rec_forward_kernel(RecArgs a, Links links, const float* s_in, float* s_out, T* _
   __shared__ Runs<S> rs;
   const TileAt at = tile_at(a, links, false);
   const LaneAt<S> l = lane_at<S>(a, at);
-  uint4 vx[S::kRun], vg[S::kRun], vi[S::kRun];
-  const T *x = row_of(a.x, l), *g = row_of(a.decay, l), *in = row_of(a.input, l);
-  with_tokens(l, [&](int t) {
-    vg[t] = get16(g + t * a.decay.st);
-    vi[t] = get16(in + t * a.input.st);
-    vx[t] = get16(x + t * a.x.st);
-  }, [&](int t) {
-    vg[t] = no_token<T>();
-    vx[t] = vi[t] = make_uint4(0, 0, 0, 0);
-  });
   // Inside a run of a few tokens a itself will do; from run to run the sum of z counts.
   float dec[S::kRun][S::kPer], u[S::kRun][S::kPer], Z[S::kPer], H[S::kPer];
-#pragma unroll
-  for (int c = 0; c < S::kPer; ++c) Z[c] = -0.0f, H[c] = 0.0f;
-#pragma unroll
-  for (int t = 0; t < S::kRun; ++t)
+  on_run(l, [&](auto whole) {
+    uint4 vx[S::kRun], vg[S::kRun], vi[S::kRun];
+    const T *x = row_of(a.x, l), *g = row_of(a.decay, l), *in = row_of(a.input, l);
+    load_tokens<whole>(l, [&](int t, int64_t i) {
+      vg[t] = get16(g + i * a.decay.st);
+      vi[t] = get16(in + i * a.input.st);
+      vx[t] = get16(x + i * a.x.st);
+    }, [&](int t) {
+      vg[t] = no_token<T>();
+      vx[t] = vi[t] = make_uint4(0, 0, 0, 0);
+    });
+    float rate[S::kPer];
 #pragma unroll
     for (int c = 0; c < S::kPer; ++c) {
-      const float z = l.rate[c] * sigmoid(chunk_value<T>(vg[t], c));
-      dec[t][c] = __builtin_amdgcn_exp2f(z);
-      u[t][c] = gated(z, dec[t][c], chunk_value<T>(vi[t], c)) * chunk_value<T>(vx[t], c);
-      Z[c] += z;
-      H[c] = __builtin_fmaf(dec[t][c], H[c], u[t][c]);
+      rate[c] = rate_after(l, c);
+      Z[c] = -0.0f, H[c] = 0.0f;
     }
+#pragma unroll
+    for (int t = 0; t < S::kRun; ++t) {
+      __builtin_amdgcn_sched_barrier(0);  // one token after the other, as they come
+#pragma unroll
+      for (int c = 0; c < S::kPer; ++c) {
+        const float z = rate[c] * sigmoid(chunk_value<T>(vg[t], c));
+        dec[t][c] = __builtin_amdgcn_exp2f(z);
+        u[t][c] = gated(z, dec[t][c], chunk_value<T>(vi[t], c)) * chunk_value<T>(vx[t], c);
+        Z[c] += z;
+        H[c] = __builtin_fmaf(dec[t][c], H[c], u[t][c]);
+      }
+    }
+  });
   put_run(rs, l, Z, H);
   link_tile<false>(
       rs, a, links, at, [&](int64_t c) { return s_in ? s_in[at.b * a.d + c] : 0.0f; },
@@ -565,32 +599,36 @@ rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, con
   const TileAt at = tile_at(a, links, true);
   const LaneAt<S> l = lane_at<S>(a, at);
   uint4 vx[S::kRun], vd[S::kRun];
-  float r[S::kRun][S::kPer], bi[S::kRun][S::kPer];
-  {
+  float r[S::kRun][S::kPer], bi[S::kRun][S::kPer], rate[S::kPer];
+  // C: what comes from behind the run, from 0: the sum of its dh, each through the decays
+  // up to its token (A)
+  float Z[S::kPer], H[S::kPer], C[S::kPer];
+  on_run(l, [&](auto whole) {
     uint4 vg[S::kRun], vi[S::kRun];
     const T *x = row_of(a.x, l), *g = row_of(a.decay, l), *in = row_of(a.input, l),
             *dh = row_of(a.dh, l);
-    with_tokens(l, [&](int t) {
-      vg[t] = get16(g + t * a.decay.st);
-      vi[t] = get16(in + t * a.input.st);
-      vx[t] = get16(x + t * a.x.st);
-      vd[t] = get16(dh + t * a.dh.st);
+    load_tokens<whole>(l, [&](int t, int64_t i) {
+      vg[t] = get16(g + i * a.decay.st);
+      vi[t] = get16(in + i * a.input.st);
+      vx[t] = get16(x + i * a.x.st);
+      vd[t] = get16(dh + i * a.dh.st);
     }, [&](int t) {
       vg[t] = no_token<T>();
       vx[t] = vi[t] = vd[t] = make_uint4(0, 0, 0, 0);
     });
-    // C: what comes from behind the run, from 0: the sum of its dh, each through the decays
-    // up to its token (A)
-    float Z[S::kPer], H[S::kPer], C[S::kPer], A[S::kPer];
+    float A[S::kPer];
 #pragma unroll
-    for (int c = 0; c < S::kPer; ++c) Z[c] = -0.0f, H[c] = C[c] = 0.0f, A[c] = 1.0f;
+    for (int c = 0; c < S::kPer; ++c) {
+      rate[c] = rate_after(l, c);
+      Z[c] = -0.0f, H[c] = C[c] = 0.0f, A[c] = 1.0f;
+    }
 #pragma unroll
     for (int t = 0; t < S::kRun; ++t) {
       __builtin_amdgcn_sched_barrier(0);  // registers: one token at a time
 #pragma unroll
       for (int c = 0; c < S::kPer; ++c) {
         r[t][c] = sigmoid(chunk_value<T>(vg[t], c));
-        const float z = l.rate[c] * r[t][c], dec = __builtin_amdgcn_exp2f(z);
+        const float z = rate[c] * r[t][c], dec = __builtin_amdgcn_exp2f(z);
         bi[t][c] = gated(z, dec, chunk_value<T>(vi[t], c));
         Z[c] += z;
         H[c] = __builtin_fmaf(dec, H[c], bi[t][c] * chunk_value<T>(vx[t], c));
@@ -598,10 +636,10 @@ rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, con
         C[c] = __builtin_fmaf(A[c], chunk_value<T>(vd[t], c), C[c]);
       }
     }
-    put_run(rs, l, Z, C);
+  });
+  put_run(rs, l, Z, C);
 #pragma unroll
-    for (int c = 0; c < S::kPer; ++c) hs[l.run][l.lane * S::kPer + c] = H[c];
-  }
+  for (int c = 0; c < S::kPer; ++c) hs[l.run][l.lane * S::kPer + c] = H[c];
   const auto tile_row = [&](int64_t c) { return (at.b * links.tiles + at.j) * a.d + c; };
   link_tile<true>(
       rs, a, links, at, [&](int64_t c) { return ds_out ? ds_out[at.b * a.d + c] : 0.0f; },
@@ -641,7 +679,7 @@ rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, con
 #pragma unroll
       for (int t = 0; t < S::kRun; ++t) {
         s[t] = f;
-        dec[t] = __builtin_amdgcn_exp2f(l.rate[k] * r[t][k]);
+        dec[t] = __builtin_amdgcn_exp2f(rate[k] * r[t][k]);
         f = __builtin_fmaf(dec[t], f, bi[t][k] * chunk_value<T>(vx[t], k));
       }
       float c = rs.h[l.run][at_k], dr = 0.0f;
@@ -652,12 +690,12 @@ rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, con
         // beside (1 / b counts as 2^94: above all others, and finite)
         const float al = dec[t] * lam;
         const float inv =
-            __builtin_amdgcn_rsqf(root_arg(l.rate[k] * r[t][k], dec[t], 0x1p-124f)) * 0x1p32f;
+            __builtin_amdgcn_rsqf(root_arg(rate[k] * r[t][k], dec[t], 0x1p-124f)) * 0x1p32f;
         const float i = bi[t][k] * inv;
         const float y = al * __builtin_fmaf(-dec[t], i * x * inv, s[t]);
         const float yr = t < l.n ? y * r[t][k] : 0.0f;
         fx[t][q] = lam * bi[t][k];
-        const float fxx = fx[t][q] * x, yz = yr * (l.rate[k] * (1.0f / kLog2e));
+        const float fxx = fx[t][q] * x, yz = yr * (rate[k] * (1.0f / kLog2e));
         fi[t][q] = __builtin_fmaf(-fxx, i, fxx);
         fg[t][q] = __builtin_fmaf(-yz, r[t][k], yz);
         dr -= yr;
