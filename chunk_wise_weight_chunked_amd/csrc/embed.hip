@@ -9,7 +9,7 @@
 // a piece's rows in registers: an id whose tokens lie in one piece gets its row
 // written at once, the sums of ids that reach over pieces go to the workspace and
 // are added in order by a last launch.  No atomic sums: the result does not
-// depend on what runs when.
+// depend on what runs when.  Up to 64 tokens take one launch without a sort.
 //
 // The lookup of 131072 rows of 2560 bf16 values takes 185 us (4.35 TB/s, five bytes written
 // for each read).  The gradient of 32768 tokens of 2560 into 50001 fp32 rows takes 182 us: the
@@ -317,6 +317,18 @@ __device__ __forceinline__ void put_row(TO* row, const float sum[8], float scale
   Piece<TO>::store(row, f);
 }
 
+// Zeros in the rows v0 + i of the bits i of `none`.
+template <typename TO>
+__device__ __forceinline__ void put_zeros(TO* __restrict__ grad, int64_t d, int64_t v0,
+                                          uint64_t none) {
+  const int64_t n = d * (int64_t)sizeof(TO) / 16;
+  while (none) {
+    uint4* const row = reinterpret_cast<uint4*>(grad + (v0 + __builtin_ctzll(none)) * d);
+    none &= none - 1;
+    for (int64_t i = threadIdx.x & 63; i < n; i += 64) row[i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
 // Zeros for rows without tokens: a wave takes kZeroRows rows from v0 on and looks each up
 // in the sorted tokens' ids.
 constexpr int kZeroRows = 16;
@@ -330,13 +342,8 @@ __device__ __forceinline__ void zero_rows(const uint32_t* __restrict__ keys, TO*
     const int64_t mid = (lo + hi) >> 1;
     if ((int64_t)keys[mid] < v) lo = mid + 1; else hi = mid;
   }
-  uint64_t none = __ballot(lane < kZeroRows && v < V && (lo == N || (int64_t)keys[lo] != v));
-  const int64_t n = d * (int64_t)sizeof(TO) / 16;
-  while (none) {
-    uint4* const row = reinterpret_cast<uint4*>(grad + (v0 + __builtin_ctzll(none)) * d);
-    none &= none - 1;
-    for (int64_t i = lane; i < n; i += 64) row[i] = make_uint4(0, 0, 0, 0);
-  }
+  put_zeros(grad, d, v0,
+            __ballot(lane < kZeroRows && v < V && (lo == N || (int64_t)keys[lo] != v)));
 }
 
 // A wave sums kWaveCols columns of a piece of the sorted tokens; behind those waves come
@@ -529,6 +536,69 @@ __global__ __launch_bounds__(kBlock) void embed_join_kernel(
   put_row<TO, kAdd>(grad + (int64_t)id * d + c, sum, scale, there);
 }
 
+// The whole gradient of up to 64 tokens: every wave has all ids, one a lane.  A wave sums
+// kWaveCols columns of one id's tokens in the order of their places; behind those waves come
+// the ones for the zeros.  (1024 columns, here / in the launches above: 64 tokens added 5.6 /
+// 13.5 us, 64 into 2000 rows 7.8 / 17; 64 of one id into 2000 rows of 2560 7.3 / 13.8, added.)
+constexpr int kFew = 64;
+template <typename T, typename TO, bool kAdd>
+__global__ __launch_bounds__(kBlock) void embed_few_kernel(SortIn in, const T* __restrict__ dout,
+                                                           TO* __restrict__ grad, int64_t d,
+                                                           float scale, int64_t units,
+                                                           int col_parts) {
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = (int64_t)blockIdx.x * (kBlock / 64) +
+                       __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // wave-uniform
+  const uint32_t key = lane < (int)in.N ? in.key(lane) : (uint32_t)in.V;
+  if (unit >= units) {
+    if constexpr (!kAdd) {
+      const int64_t step = ((int64_t)gridDim.x * (kBlock / 64) - units) * kZeroRows;
+      for (int64_t v0 = (unit - units) * kZeroRows; v0 < in.V; v0 += step) {
+        bool has = false;
+        for (int t = 0; t < (int)in.N; ++t)
+          has |= (int64_t)(uint32_t)__builtin_amdgcn_readlane(key, t) == v0 + lane;
+        put_zeros(grad, d, v0, __ballot(lane < kZeroRows && v0 + lane < in.V && !has));
+      }
+    }
+    return;
+  }
+  const int first = (int)(unit / col_parts);
+  const uint32_t id = __builtin_amdgcn_readlane(key, first);
+  uint64_t mine = __ballot(key == id);
+  if (id >= (uint32_t)in.V || __builtin_ctzll(mine) != first) return;  // none, or another wave's
+  const int64_t col = (unit % col_parts) * kWaveCols + 8 * lane;
+  if (col >= d) return;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  Piece<TO> there;
+  there.zero();
+  TO* const to = grad + (int64_t)id * d + col;
+  if constexpr (kAdd) there.load(to);
+  constexpr int kAhead = 8;
+  while (mine) {
+    Piece<T> row[kAhead];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      row[i].zero();
+      if (!mine) continue;
+      row[i].load(dout + (int64_t)__builtin_ctzll(mine) * d + col);
+      mine &= mine - 1;
+      n = i + 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (i >= n) break;
+      float f[8];
+      row[i].get(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += f[j];
+    }
+  }
+  put_row<TO, kAdd>(to, sum, scale, there);
+}
+
 // ---------------------------------------------------------------- host side
 struct SortPlan {
   int passes, bits;  // passes of `bits` bits each
@@ -544,8 +614,8 @@ SortPlan sort_plan(const EmbedArgs& a) {
   return p;
 }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-// Tokens of a piece: few tokens make more waves of shorter chains (64 tokens 13 us with
-// pieces of 8, 20 with 32; 4000 23 and 30), many tokens fewer sums that the join adds.
+// Tokens of a piece: few tokens make more waves of shorter chains (4000 tokens 23 us with
+// pieces of 8, 30 with 32), many tokens fewer sums that the join adds.
 int piece_of(const EmbedArgs& a) { return a.N <= kSmall ? 8 : kPiece; }
 int64_t pieces_of(const EmbedArgs& a) { return (a.N + piece_of(a) - 1) / piece_of(a); }
 
@@ -609,10 +679,31 @@ hipError_t launch_embed_forward(const EmbedArgs& a, const void* ids, const void*
   });
 }
 
-size_t embed_backward_bytes(const EmbedArgs& a) { return grad_plan(a).bytes; }
+size_t embed_backward_bytes(const EmbedArgs& a) { return a.N <= kFew ? 0 : grad_plan(a).bytes; }
 
 hipError_t launch_embed_backward(const EmbedArgs& a, const void* ids, const void* dout, void* grad,
                                  void* ws, hipStream_t s) {
+  const auto typed = [&](auto&& go) {
+    return with_types(a, [&](auto t, auto to) {
+      return a.accumulate ? go(t, to, std::true_type{}) : go(t, to, std::false_type{});
+    });
+  };
+  const int col_parts = (int)((a.d + kWaveCols - 1) / kWaveCols);
+  // waves for n rows' zeros: a launch's threads are counted in 32 bits, and where 2^22 waves do
+  // not take them all, they go on with further ones
+  const auto zero_waves = [](int64_t n) {
+    return std::min<int64_t>((n + kZeroRows - 1) / kZeroRows, (int64_t)1 << 22);
+  };
+  if (a.N <= kFew)
+    return typed([&](auto t, auto to, auto add) {
+      using T = decltype(t);
+      using TO = decltype(to);
+      const int64_t units = a.N * col_parts, all = units + (add ? 0 : zero_waves(a.V));
+      embed_few_kernel<T, TO, add><<<dim3((unsigned)((all + 3) / 4)), kBlock, 0, s>>>(
+          SortIn{ids, nullptr, nullptr, a.wide_ids, a.N, a.V}, static_cast<const T*>(dout),
+          static_cast<TO*>(grad), a.d, a.scale, units, col_parts);
+      return hipGetLastError();
+    });
   const SortPlan sp = sort_plan(a);
   const GradPlan p = grad_plan(a);
   char* const base = static_cast<char*>(ws);
@@ -661,17 +752,13 @@ hipError_t launch_embed_backward(const EmbedArgs& a, const void* ids, const void
   }
   const uint32_t *keys = u32(p.keys[cur ^ 1]), *pos = u32(p.pos[cur ^ 1]);
   float* part = reinterpret_cast<float*>(base + p.part);
-  const auto go = [&](auto t, auto to, auto add) {
+  return typed([&](auto t, auto to, auto add) {
     using T = decltype(t);
     using TO = decltype(to);
     constexpr bool kAdd = decltype(add)::value;
-    const int col_parts = (int)((a.d + kWaveCols - 1) / kWaveCols);
-    const int64_t units = pieces_of(a) * col_parts;
-    // waves: a launch's threads are counted in 32 bits, units are 2^25 at most, and the
-    // waves for zeros go on with further rows where 2^22 do not take them all
+    const int64_t units = pieces_of(a) * col_parts;  // 2^25 at most
     const int64_t late = std::min(3 * share, a.V - zeroed), zero1 = a.V - late;
-    const int64_t all = units + std::min<int64_t>((zero1 - zeroed + kZeroRows - 1) / kZeroRows,
-                                                  (int64_t)1 << 22);
+    const int64_t all = units + zero_waves(zero1 - zeroed);
     embed_sum_kernel<T, TO, kAdd><<<dim3((unsigned)((all + 3) / 4)), kBlock, 0, s>>>(
         keys, pos, static_cast<const T*>(dout), static_cast<TO*>(grad), part, a.N, a.V, a.d,
         a.scale, piece_of(a), units, col_parts, zeroed, zero1);
@@ -686,9 +773,6 @@ hipError_t launch_embed_backward(const EmbedArgs& a, const void* ids, const void
         keys, part, static_cast<TO*>(grad), group, a.N, a.V, a.d, a.scale, piece_of(a),
         pieces, zero1);
     return hipGetLastError();
-  };
-  return with_types(a, [&](auto t, auto to) {
-    return a.accumulate ? go(t, to, std::true_type{}) : go(t, to, std::false_type{});
   });
 }
 

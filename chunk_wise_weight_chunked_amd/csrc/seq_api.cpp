@@ -210,7 +210,7 @@ ttt_status_t ttt_embed_backward(const ttt_embed_desc_t* desc, const void* ids, c
   BufferList b;
   b.in("dout", dout, (size_t)(a.N * a.d) * ttt::dtype_bytes(a.dt));
   b.out("grad", grad, (size_t)(a.V * a.d) * ttt::dtype_bytes(a.out_dt));
-  b.out("ws", ws, need);
+  if (need) b.out("ws", ws, need);
   if (ttt_status_t st = check_ids(b, desc, ids)) return st;
   const hipError_t e =
       ttt::launch_embed_backward(a, ids, dout, grad, ws, static_cast<hipStream_t>(stream));

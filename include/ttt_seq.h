@@ -60,7 +60,7 @@ ttt_status_t ttt_embed_forward(const ttt_embed_desc_t* desc, const void* ids, co
  * their places, in pieces of a fixed length: no atomic sums.  Tokens whose id is
  * outside [0, vocab) give nothing.
  *   dout  [tokens][d];  grad [vocab][d]
- *   ws    ttt_embed_backward_workspace_size(desc) bytes */
+ *   ws    ttt_embed_backward_workspace_size(desc) bytes (for few tokens 0, ws may then be NULL) */
 ttt_status_t ttt_embed_backward_workspace_size(const ttt_embed_desc_t* desc, size_t* bytes);
 ttt_status_t ttt_embed_backward(const ttt_embed_desc_t* desc, const void* ids, const void* dout,
                                 void* grad, void* ws, size_t ws_bytes, void* stream);
@@ -85,8 +85,8 @@ ttt_status_t ttt_embed_backward(const ttt_embed_desc_t* desc, const void* ids, c
  *   rate     fp32 [d] on the device, >= 0 in use (0: the state is kept and nothing
  *            enters; a negative rate gives NaN)
  *   lengths  int32 [B] on the device, or NULL: sequence b has lengths[b] tokens
- *            (values outside [0, T] are taken as the nearer end); the rows behind them
- *            are not read, their h and gradients are 0, and the state stops at the last
+ *            (values outside [0, T] are taken as the nearer end); what the rows
+ *            behind them hold does not matter, their h and gradients are 0, and the state stops at the last
  *            token.  A sequence of 0 tokens keeps its state.
  * States are fp32 [B][d].  An infinity or NaN stays in its channel, reaches its own
  * token and those that the formula gives it to, and may become NaN there. */
