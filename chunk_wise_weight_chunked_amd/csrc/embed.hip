@@ -5,14 +5,14 @@
 //
 // The lookup copies rows: bound by HBM.  The gradient sorts the tokens by id
 // (least significant digit first, stable, so that equal ids keep the order of
-// their places), cuts the sorted tokens into pieces of 8 or 32 and lets a wave sum
+// their places), cuts the sorted tokens into pieces of 8 to 32 and lets a wave sum
 // a piece's rows in registers: an id whose tokens lie in one piece gets its row
 // written at once, the sums of ids that reach over pieces go to the workspace and
 // are added in order by a last launch.  No atomic sums: the result does not
 // depend on what runs when.  Up to 64 tokens take one launch without a sort.
 //
 // The lookup of 131072 rows of 2560 bf16 values takes 185 us (4.35 TB/s, five bytes written
-// for each read).  The gradient of 32768 tokens of 2560 into 50001 fp32 rows takes 182 us: the
+// for each read).  The gradient of 32768 tokens of 2560 into 50001 fp32 rows takes 181 us: the
 // sort's launches, each some 4 to 8 us of waiting for the one before, and 4.2 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -188,11 +188,17 @@ __global__ __launch_bounds__(kSortBlock) void embed_scatter_kernel(
     mine = total[threadIdx.x];
     tile = hist[(int64_t)blockIdx.x * bins + threadIdx.x];
   } else if (has) {
-#pragma unroll 8
-    for (int t = 0; t < (int)tiles; ++t) {
-      const uint32_t c = hist[t * bins + threadIdx.x];
-      mine += c;
-      tile += t < (int)blockIdx.x ? c : 0;
+    constexpr int kLoads = 32;  // at a time
+    for (int t0 = 0; t0 < (int)tiles; t0 += kLoads) {
+      uint32_t c[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        c[i] = hist[min(t0 + i, (int)tiles - 1) * bins + threadIdx.x];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        mine += t0 + i < (int)tiles ? c[i] : 0;
+        tile += t0 + i < (int)blockIdx.x ? c[i] : 0;
+      }
     }
   }
   for (int i = lane; i < bins; i += 64) count[wave][i] = 0;
@@ -226,9 +232,10 @@ __global__ __launch_bounds__(kSortBlock) void embed_scatter_kernel(
 
 // All passes for up to kSmall tokens in one workgroup: tokens in LDS, wave w has the
 // tokens w 64 rounds .. of each pass in rounds of 64, and counts a digit's tokens of its
-// earlier rounds as well.  (A gradient of d = 1024 added to, one workgroup / the launches
-// above: 1000 tokens 15 / 21 us, 4100 26 / 39, 8000 39 / 40.)
-constexpr int kSmallRounds = 8;
+// earlier rounds as well.  (512 columns of 50001 rows added to, one workgroup / the
+// launches above: 1000 tokens 15 / 25 us, 4000 22 / 25, 6000 28 / 27, 8192 34 / 29; of 1000
+// rows 6000 22 / 25, 8192 27 / 25.)
+constexpr int kSmallRounds = 6;
 constexpr int kSmall = kSmallRounds * kSortBlock;
 __global__ __launch_bounds__(kSortBlock) void embed_sort_kernel(SortIn in, int passes, int bits,
                                                                 uint32_t* __restrict__ keys_out,
@@ -489,6 +496,10 @@ __global__ __launch_bounds__(kBlock) void embed_join_kernel(
   if (id >= (uint32_t)V || keys[last + 1] != id) return;
   const bool inside = keys[n0] != id;  // begins behind the piece's first token
   if (!inside && n0 > 0 && keys[n0 - 1] == id) return;  // began in an earlier piece
+  const int64_t c = (int64_t)blockIdx.y * 256 + 8 * threadIdx.x;  // what a thread puts in the end
+  Piece<TO> there;
+  there.zero();
+  if (kAdd && threadIdx.x < 32 && c < d) there.load(grad + (int64_t)id * d + c);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   int64_t end = p;  // the id's last piece: those behind p begin with it
   for (;;) {
@@ -522,7 +533,6 @@ __global__ __launch_bounds__(kBlock) void embed_join_kernel(
   }
   *reinterpret_cast<float4*>(&s[wave][4 * lane]) = a;
   __syncthreads();
-  const int64_t c = (int64_t)blockIdx.y * 256 + 8 * threadIdx.x;
   if (threadIdx.x >= 32 || c >= d) return;
   float sum[8];
 #pragma unroll
@@ -530,9 +540,6 @@ __global__ __launch_bounds__(kBlock) void embed_join_kernel(
     const int x = 8 * threadIdx.x + j;
     sum[j] = (s[0][x] + s[1][x]) + (s[2][x] + s[3][x]);
   }
-  Piece<TO> there;
-  there.zero();
-  if constexpr (kAdd) there.load(grad + (int64_t)id * d + c);
   put_row<TO, kAdd>(grad + (int64_t)id * d + c, sum, scale, there);
 }
 
@@ -614,9 +621,13 @@ SortPlan sort_plan(const EmbedArgs& a) {
   return p;
 }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-// Tokens of a piece: few tokens make more waves of shorter chains (4000 tokens 23 us with
-// pieces of 8, 30 with 32), many tokens fewer sums that the join adds.
-int piece_of(const EmbedArgs& a) { return a.N <= kSmall ? 8 : kPiece; }
+// Tokens of a piece: few make more waves of shorter chains, many fewer sums that the join adds.
+// us with pieces of 8 / 16 / 32, added: 3000 tokens of 512 columns 19 / 21 / 26, 10000 31 / 30 /
+// 35, 24000 38 / 37 / 36; 3000 of 1024 21 / 23 / 29, 6000 33 / 32 / 35, 32000 75 / 67 / 62.
+int piece_of(const EmbedArgs& a) {
+  const int64_t waves = a.N * ((a.d + kWaveCols - 1) / kWaveCols);  // with pieces of one
+  return waves <= 8192 ? 8 : waves <= 20480 ? 16 : kPiece;
+}
 int64_t pieces_of(const EmbedArgs& a) { return (a.N + piece_of(a) - 1) / piece_of(a); }
 
 // Whether an id can have so many pieces that adding them one by one shows: with all tokens

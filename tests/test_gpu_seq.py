@@ -96,9 +96,10 @@ def test_embed_forward_shapes_and_values():
 EMBED_SHAPES = [(1, 1, 8), (3, 1, 64), (31, 5, 64), (32, 5, 128), (33, 2, 136), (64, 64, 200),
                 (500, 600, 520), (700, 3, 1000), (4096, 300, 64), (4097, 511, 72), (9000, 512, 64),
                 (9000, 40000, 72), (20000, 7, 40), (300, 131072, 64), (513, 50, 2560),
-                (8192, 700, 24), (8193, 700, 24), (9000, 300000, 8), (700, 1 << 20, 8),
+                (6144, 700, 24), (6145, 700, 24), (8192, 700, 24), (8193, 700, 24),
+                (9000, 300000, 8), (700, 1 << 20, 8),
                 (20, 1000, 2560), (64, 3, 1032), (65, 64, 200), (128, 3, 1032), (129, 64, 200),
-                (128, 300000, 8), (2, 1 << 20, 8)]
+                (128, 300000, 8), (2, 1 << 20, 8), (20480, 90, 8), (20481, 90, 8), (2100, 50, 2056)]
 
 
 @pytest.mark.parametrize("dtype,gd", [(BF16, F32), (BF16, BF16), (F32, F32)])
