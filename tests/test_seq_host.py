@@ -490,12 +490,12 @@ def test_no_packed_arithmetic(tmp_path):
 
 # ------------------------------------------- the recurrence's links, on the CPU
 def test_the_state_found_does_not_depend_on_when_it_is_looked_for():
-    """state_before of gatedrec.hip, its steps in Python: whatever part of the tiles in front has
-    published its state, its map or nothing, what is found is the same number to the bit, or
-    nothing yet; and with every tile in front published something is found."""
+    """state_before of gatedrec.hip, its steps in Python: whatever part of the groups of tiles in
+    front has published its state, its map or nothing, what is found is the same number to the
+    bit, or nothing yet; and with every group in front published something is found."""
     rng = np.random.default_rng(7)
     f32 = np.float32
-    kAhead = 8
+    kAhead = 6
 
     def apply(dec, h, u):
         near = np.signbit(dec)
@@ -507,7 +507,7 @@ def test_the_state_found_does_not_depend_on_when_it_is_looked_for():
            for _ in range(n)]
     u = [f32(rng.normal()) for _ in range(n)]
     states, s = [], f32(rng.normal())
-    for j in range(n):  # behind tile j
+    for j in range(n):  # behind group j
         s = apply(dec[j], s, u[j])
         states.append(s)
 
@@ -525,13 +525,50 @@ def test_the_state_found_does_not_depend_on_when_it_is_looked_for():
             for j in range(n):
                 kind = rng.choice(["unset", "map", "state"])
                 if j == 0 and kind == "map":
-                    kind = "state"  # the first tile has no map
+                    kind = "state"  # the first group's word has no map
                 word.append((kind, dec[j], states[j] if kind == "state" else u[j]))
             got = look(k, word)
             assert got is None or got == states[k - 1]
-    # maps alone behind the first tile's state: found as far as kAhead reaches, then in turn
+    # maps alone behind the first group's state: found as far as kAhead reaches, then in turn
     word = [("state", None, states[0])] + [("map", dec[j], u[j]) for j in range(1, n)]
     for j in range(1, n):
         before = look(j, word)
         assert before is not None and before == states[j - 1]
         word[j] = ("state", None, apply(dec[j], before, u[j]))
+
+
+def test_the_decay_over_two_runs():
+    """decay_both of gatedrec.hip, its steps in Python: a decay near 1 is kept as its distance from
+    1 (sign bit set), the product of any two to 2^-22 of itself and, near 1, of its distance."""
+    f32 = np.float32
+
+    def fma(a, b, c):
+        return f32(np.float64(a) * np.float64(b) + np.float64(c))
+
+    def both(d1, d2):
+        n1, n2 = np.signbit(d1), np.signbit(d2)
+        near = -abs(fma(d1, d2, f32(d1 + d2)))
+        if n1 and n2:
+            return f32(f32(1) + near) if near < -0.5 else near
+        return fma(d1, d2, d2 if n1 else d1 if n2 else f32(0))
+
+    def value(d):  # (a, 1 - a)
+        return (1 + np.float64(d), -np.float64(d)) if np.signbit(d) else (np.float64(d), 1 - np.float64(d))
+
+    rng = np.random.default_rng(8)
+    one = f32(-0.0)
+    some = [one, f32(0), f32(1e-30), f32(0.7), f32(-0.29), f32(-1e-7), f32(-1e-30)]
+    some += [f32(-(10.0 ** -e)) for e in rng.uniform(0.6, 8, 40)] + [f32(x) for x in rng.uniform(0, .7, 40)]
+    for a in some:
+        assert value(both(one, a)) == value(a) and np.signbit(both(one, a)) == np.signbit(a)
+        assert value(both(a, one)) == value(a)
+        for b in some:
+            got = both(a, b)
+            (va, ua), (vb, ub) = value(a), value(b)
+            # (below fp32's smallest, 2^-149, a product rounds to it or to 0)
+            assert abs(value(got)[0] - va * vb) <= 2.0 ** -22 * va * vb + 2.0 ** -149
+            if np.signbit(got):  # 1 - a b = (1 - a) + (1 - b) - (1 - a)(1 - b)
+                want = ua + ub - ua * ub
+                assert abs(value(got)[1] - want) <= 2.0 ** -22 * want + 2.0 ** -149
+    nan = f32("nan")
+    assert np.isnan(both(nan, one)) and np.isnan(both(one, nan)) and np.isnan(both(f32(0.5), nan))
