@@ -16,6 +16,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "piece.h"
 #include "seq.h"
@@ -200,14 +201,20 @@ __global__ __launch_bounds__(kBlock) void act8_operands_kernel(
     split_block(dy, dys, terms, part, rows, n, blockIdx.y - x_columns);
 }
 
-// Tiles of the gradient: a workgroup a CU, or two with a quarter of it each.
+// Tiles of the gradient: a workgroup a CU, or two with a quarter of it each; for dy's terms
+// one with a quarter, in whose stages the three terms' k-tiles lie side by side, so that x's
+// are loaded once for the three and a stage has three times the products (us, 1554 x 1024 x
+// 1536 32, 36 with one term after the other in two workgroups a CU; 136 x 200 x 2560 13 and 17,
+// 8192 x 2560 x 2560 318 and 349, 285 x 1000 x 7680 33 and 32).
 using WideTile = TileShape<256, 256, 2, 4>;
 using SmallTile = TileShape<128, 128, 2, 2>;
+using TermTile = TileShape<128, 128, 2, 4>;
 constexpr int kEpiCols = 64;
 constexpr int kEpiStride = kEpiCols + 8;  // floats per staged row
 
 // k-tiles [k0, k0 + n) of an operand, kParts times: of x again and again, of dy's terms
-// one after the other (part_stride bytes between them).
+// one after the other (part_stride bytes between them; wide tiles, of whose stages three terms
+// would not fit LDS).
 template <class Base, int kParts>
 struct PartLoader {
   static constexpr int kPer = Base::kPer;
@@ -230,6 +237,36 @@ struct PartLoader {
     const rsrc_t r = rsrc(kt);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) l.issue_one(r, stage, q);
+  }
+};
+// k-tiles of dy's three terms, side by side in a stage.
+template <class S>
+struct TermLoader {
+  using Base = DirectLoader<S::BN, S::kWaves>;
+  static constexpr int kPer = 3 * Base::kPer;
+  static constexpr int kBytes = S::BN * kRowBytes;
+  Base l;
+  int64_t part_stride;
+  struct Rsrc {
+    rsrc_t term[3];
+  };
+  __device__ __forceinline__ Rsrc rsrc(int64_t kt, bool live = true) const {
+    Rsrc r;
+    Base at = l;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+      r.term[t] = at.rsrc(kt, live);
+      at.base += part_stride;
+    }
+    return r;
+  }
+  __device__ __forceinline__ void issue_one(const Rsrc& r, lds_char* stage, int q) const {
+    l.issue_one(r.term[q / Base::kPer], stage + q / Base::kPer * kBytes, q % Base::kPer);
+  }
+  __device__ __forceinline__ void issue(int64_t kt, lds_char* stage) {
+    const Rsrc r = rsrc(kt);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) issue_one(r, stage, q);
   }
 };
 // kCols columns from n0 of an operand of N columns in blocks, k-tiles from k0.
@@ -348,9 +385,52 @@ struct GradMma {
   }
 };
 
+// A k-tile's products of x with dy's three terms side by side: x's fragments are read once
+// for the three.
+template <class S>
+struct TermMma {
+  using Plain = Mma16<S, false, false>;
+  static constexpr int kSteps = Plain::kSteps;
+  static constexpr int kEach = S::MB * S::NB, kPerStep = 3 * kEach;
+  static constexpr int kReads = S::MB + 3 * S::NB;
+  static_assert(kReads <= kPerStep, "a read after each matrix instruction at most");
+  __device__ __forceinline__ void init(const LanePos&) {}
+  struct Frag {
+    bf16x8_t a[S::MB], b[3][S::NB];
+    __device__ __forceinline__ void read(const lds_char* sA, const lds_char* sB, const LanePos& p,
+                                         int s, int m) {
+      if (m < S::MB)
+        a[m] = Plain::read_a(sA, p, m, s);
+      else
+        b[(m - S::MB) / S::NB][(m - S::MB) % S::NB] = Plain::read_b(
+            sB + (m - S::MB) / S::NB * (S::BN * kRowBytes), p, (m - S::MB) % S::NB, s);
+    }
+  };
+  template <class Hook>
+  __device__ __forceinline__ void ktile(Accum<S>& acc, const lds_char* sA, const lds_char* sB,
+                                        const LanePos& p, Hook&& hook) const {
+    Frag f[2];
+#pragma unroll
+    for (int m = 0; m < kReads; ++m) f[0].read(sA, sB, p, 0, m);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < kPerStep; ++m) {
+        const int t = m / kEach, i = m % kEach / S::NB, j = m % S::NB;
+        acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[s & 1].a[i], f[s & 1].b[t][j],
+                                                              acc.v[i][j], 0, 0, 0);
+        if (s + 1 < kSteps && m < kReads) f[(s + 1) & 1].read(sA, sB, p, s + 1, m);
+        hook(kPerStep * s + m);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+};
+
 // The mainloop of gemm_core.h on these fragments: k-tile kt + 1's loads one after each of
 // kt's first matrix instructions.
-template <class Mma, class S, class LA, class LB>
+template <class Mma, int kStageBytes, class S, class LA, class LB>
 __device__ __forceinline__ void grad_mainloop(Accum<S>& acc, LA& la, LB& lb, int64_t nk,
                                               lds_char* smem, const LanePos& p) {
   constexpr int kLoads = LA::kPer + LB::kPer;
@@ -362,10 +442,11 @@ __device__ __forceinline__ void grad_mainloop(Accum<S>& acc, LA& la, LB& lb, int
   wait_vmcnt<0>();
   __syncthreads();
   for (int64_t kt = 0; kt < nk; ++kt) {
-    const lds_char* cur = smem + (kt & 1) * S::kStageBytes;
-    lds_char* nxt = smem + ((kt + 1) & 1) * S::kStageBytes;
+    const lds_char* cur = smem + (kt & 1) * kStageBytes;
+    lds_char* nxt = smem + ((kt + 1) & 1) * kStageBytes;
     const bool more = kt + 1 < nk;
-    const rsrc_t ra = la.rsrc(kt + 1, more), rb = lb.rsrc(kt + 1, more);
+    const auto ra = la.rsrc(kt + 1, more);
+    const auto rb = lb.rsrc(kt + 1, more);
     mma.ktile(acc, cur, cur + S::BM * kRowBytes, p, [&](int q) {
       if (q < LA::kPer)
         la.issue_one(ra, nxt, q);
@@ -396,8 +477,10 @@ template <typename TO, class S, bool kTerms>
 __global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 act8_grad_kernel(GradArgs g) {
   static_assert(S::kLdsBytes >= S::BM * kEpiStride * 4, "epilogue stage fits the pipeline's LDS");
-  constexpr int kParts = kTerms ? 3 : 1;
-  __shared__ __attribute__((aligned(16))) char smem_raw[S::kLdsBytes];
+  constexpr bool kBeside = std::is_same_v<S, TermTile>;
+  constexpr int kParts = kTerms && !kBeside ? 3 : 1;
+  constexpr int kStageBytes = S::kStageBytes + (kBeside ? 2 * S::BN * kRowBytes : 0);
+  __shared__ __attribute__((aligned(16))) char smem_raw[2 * kStageBytes];
   lds_char* smem = (lds_char*)smem_raw;
   const int tiles_m = (int)((g.M + S::BM - 1) / S::BM), tiles_n = (int)((g.N + S::BN - 1) / S::BN);
   int tile, slice = -1;
@@ -417,14 +500,17 @@ act8_grad_kernel(GradArgs g) {
   const LanePos p = lane_pos<S>();
   const auto lx = block_loader<S, S::BM>(g.x, g.M, m0, k0);
   PartLoader<DirectLoader<S::BM, S::kWaves>, kParts> la{lx, n, 0};
-  if constexpr (kTerms) {
+  if constexpr (kBeside) {
+    TermLoader<S> lb{block_loader<S, S::BN>(g.dy, g.N, n0, k0), g.dy_part * 2};
+    grad_mainloop<TermMma<S>, kStageBytes>(acc, la, lb, n, smem, p);
+  } else if constexpr (kTerms) {
     const auto ly = block_loader<S, S::BN>(g.dy, g.N, n0, k0);
     PartLoader<DirectLoader<S::BN, S::kWaves>, kParts> lb{ly, n, g.dy_part * 2};
-    grad_mainloop<GradMma<S, false>>(acc, la, lb, n * kParts, smem, p);
+    grad_mainloop<GradMma<S, false>, kStageBytes>(acc, la, lb, n * kParts, smem, p);
   } else {
     PartLoader<RowLoader<S>, 1> lb;
     lb.l.init(g.dy, g.dys, g.rows, g.N, n0, k0);
-    grad_mainloop<GradMma<S, true>>(acc, la, lb, n, smem, p);
+    grad_mainloop<GradMma<S, true>, kStageBytes>(acc, la, lb, n, smem, p);
   }
   if (slice >= 0) {
     // as the accumulators hold them: act8_sum_kernel finds the rows and columns
@@ -561,11 +647,12 @@ Cut cut_of(const Act8Grad& g) {
   Cut best{};
   double least = -1;
   for (const int side : {256, 128}) {
-    const int64_t round = side == 256 ? 256 : 512, tiles = grad_tiles(g, side);
-    // us of a k-tile (small ones take twice the operands for their work: more where those
+    const bool beside = side == 128 && terms > 1;  // one workgroup a CU
+    const int64_t round = side == 256 || beside ? 256 : 512, tiles = grad_tiles(g, side);
+    // us of a k-tile or of three side by side (small ones take twice the operands for their work: more where those
     // come from memory) and around them, MB of a tile's sums
-    const double ktile = terms * (side == 256 ? 1.6 : cached ? 0.9 : 1.1);
-    const double around = side == 256 ? 14.0 : 5.0;
+    const double ktile = beside ? 1.0 : terms * (side == 256 ? 1.6 : cached ? 0.9 : 1.1);
+    const double around = side == 256 ? 14.0 : beside ? 6.0 : 5.0;
     const double sums = (double)side * side * 8e-6;
     const int64_t rest = tiles % round;
     const double before = (double)(tiles / round) * ((double)n * ktile + around);
@@ -598,24 +685,23 @@ GradPlan grad_plan(const Act8Grad& g) {
   return p;
 }
 
-template <class S>
+template <class S, bool kTerms>
 hipError_t launch_products(const Act8Grad& g, const GradArgs& a, hipStream_t s) {
   const int64_t rest = grad_tiles(g, S::BM) - a.whole;
   const dim3 grid((unsigned)(a.whole + rest * a.slices));
   const dim3 sums((unsigned)(rest * (S::BM * S::BN / (4 * kBlock))));
-  if (g.dt == Dtype::F32)
-    act8_grad_kernel<float, S, true><<<grid, S::kThreads, 0, s>>>(a);
-  else if (g.grad_dt == Dtype::F32)
-    act8_grad_kernel<float, S, false><<<grid, S::kThreads, 0, s>>>(a);
+  const auto go = [&](auto to) {
+    using TO = decltype(to);
+    act8_grad_kernel<TO, S, kTerms><<<grid, S::kThreads, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || rest == 0) return e;
+    act8_sum_kernel<TO, S><<<sums, kBlock, 0, s>>>(a);
+    return hipGetLastError();
+  };
+  if constexpr (kTerms)
+    return go(float{});
   else
-    act8_grad_kernel<uint16_t, S, false><<<grid, S::kThreads, 0, s>>>(a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || rest == 0) return e;
-  if (g.grad_dt == Dtype::F32)
-    act8_sum_kernel<float, S><<<sums, kBlock, 0, s>>>(a);
-  else
-    act8_sum_kernel<uint16_t, S><<<sums, kBlock, 0, s>>>(a);
-  return hipGetLastError();
+    return g.grad_dt == Dtype::F32 ? go(float{}) : go(uint16_t{});
 }
 
 }  // namespace
@@ -677,7 +763,9 @@ hipError_t launch_act8_weight_grad(const Act8Grad& g, const int8_t* codes, const
         split ? terms + t * g.d_out : nullptr, a.dy_part, g.d_out);
   });
   if (e != hipSuccess) return e;
-  return p.cut.side == 256 ? launch_products<WideTile>(g, a, s) : launch_products<SmallTile>(g, a, s);
+  if (p.cut.side == 256)
+    return split ? launch_products<WideTile, true>(g, a, s) : launch_products<WideTile, false>(g, a, s);
+  return split ? launch_products<TermTile, true>(g, a, s) : launch_products<SmallTile, false>(g, a, s);
 }
 
 }  // namespace ttt
