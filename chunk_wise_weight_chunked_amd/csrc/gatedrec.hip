@@ -32,7 +32,11 @@ namespace ttt {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kStrip = 64;  // channels of a tile
+// Channels of a tile.  Rows of 256 bytes are read and written faster than rows of 128: the
+// forward takes 128 channels in bf16 where there are more than 64 (131072 tokens of 2560 YA us,
+// 579 with 64) and 64 in fp32 (65536 tokens 465 us, 480 with 128).  The backward takes 64: with
+// its registers a tile of 128 has a CU for itself (32768 tokens 254 us, 312 with 128).
+constexpr int kStrip = 64, kWideStrip = 128, kFewChannels = 64;
 
 // Exponents are base 2 throughout: z is log2 a = -rate log2(e) r.
 //
@@ -131,19 +135,19 @@ __device__ __forceinline__ uint4 no_token() {
 template <typename T>
 __device__ __forceinline__ uint4 get16(const T* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// Lane layout of a tile on kThreads: kLanes lanes across the strip's channels, kRuns
-// runs of kRun tokens.  kRecTile tokens have kBlock threads; a call of fewer tokens than a
-// half or a quarter of that, one tile a sequence, as many fewer.
-template <typename T_, int kThreads_>
+// Lane layout of a tile of kStrip channels on kThreads: kLanes lanes across the channels,
+// kRuns runs of kRun tokens.  kRecTile tokens have 4 threads a channel; a call of fewer tokens
+// than a half or a quarter of that, one tile a sequence, as many fewer.
+template <typename T_, int kStrip_, int kThreads_>
 struct TileLayout {
   using T = T_;
-  static constexpr int kThreads = kThreads_;
+  static constexpr int kStrip = kStrip_, kThreads = kThreads_;
   static constexpr int kPer = Lane<T>::kPer;
   static constexpr int kLanes = kStrip / kPer;
   static constexpr int kRuns = kThreads / kLanes;
-  static constexpr int kTile = kRecTile * kThreads / kBlock;  // tokens
+  static constexpr int kTile = kRecTile * kThreads / (4 * kStrip);  // tokens
   static constexpr int kRun = kTile / kRuns;
-  static constexpr int kParts = kThreads / 64;  // waves, each folds kRuns / kParts runs
+  static constexpr int kParts = kThreads / kStrip;  // a thread a channel, each folds kRuns / kParts runs
 };
 
 __device__ __forceinline__ int64_t tokens_of(const RecArgs& a, int64_t b) {
@@ -265,6 +269,7 @@ struct Links {
 struct TileAt {
   int64_t b, j, strip, k;  // k: tiles that come before it in its sequence
 };
+template <class S>
 __device__ __forceinline__ TileAt tile_at(const RecArgs& a, const Links& links, bool reverse) {
   __shared__ uint32_t ticket;
   uint32_t w = blockIdx.x;
@@ -274,7 +279,7 @@ __device__ __forceinline__ TileAt tile_at(const RecArgs& a, const Links& links, 
     __syncthreads();
     w = __builtin_amdgcn_readfirstlane(ticket);  // so that what follows from it is scalar
   }
-  const uint32_t strips = (uint32_t)((a.d + kStrip - 1) / kStrip), row = strips * (uint32_t)a.B;
+  const uint32_t strips = (uint32_t)((a.d + S::kStrip - 1) / S::kStrip), row = strips * (uint32_t)a.B;
   w = min(w, gridDim.x - 1);  // whatever happens to the counter, a tile of this call
   TileAt at;
   at.k = w / row;
@@ -379,7 +384,7 @@ __device__ __forceinline__ LaneAt<S> lane_at(const RecArgs& a, const TileAt& at)
   LaneAt<S> l;
   l.lane = threadIdx.x % S::kLanes, l.run = threadIdx.x / S::kLanes;
   l.b = at.b, l.j = at.j;
-  const int64_t c0 = at.strip * kStrip + l.lane * S::kPer;
+  const int64_t c0 = at.strip * S::kStrip + l.lane * S::kPer;
   l.live = c0 < a.d;
   l.c0 = l.live ? c0 : 0;
   l.t0 = at.j * S::kTile + l.run * S::kRun;
@@ -452,12 +457,12 @@ __device__ __forceinline__ const typename S::T* row_of(const RecOperand& o, cons
 }
 
 // The runs of a tile in LDS, by run and channel: decays over a run and states behind
-// it from 0, sums of z.  A wave folds kEach of them for 64 channels.
+// it from 0, sums of z.  A part of the threads, one a channel, folds kEach.
 template <class S>
 struct alignas(16) Runs {
   static constexpr int kEach = S::kRuns / S::kParts;
-  float z[S::kRuns][kStrip], dec[S::kRuns][kStrip], h[S::kRuns][kStrip];
-  float part_z[S::kParts][kStrip], part_h[S::kParts][kStrip];
+  float z[S::kRuns][S::kStrip], dec[S::kRuns][S::kStrip], h[S::kRuns][S::kStrip];
+  float part_z[S::kParts][S::kStrip], part_h[S::kParts][S::kStrip];
 };
 
 // A lane's run into LDS.
@@ -472,29 +477,29 @@ __device__ __forceinline__ void put_run(Runs<S>& rs, const LaneAt<S>& l, const f
 }
 
 // From the runs in LDS to the state in front of each run, which takes the place of its
-// h: the waves fold their runs, the first wave folds the waves' and links the tile with
-// the ones before it, the waves go through their runs once more.  first: the state of
+// h: the parts fold their runs, the first part folds the parts' and links the tile with
+// the ones before it, the parts go through their runs once more.  first: the state of
 // the channel in front of the first tile; done(channel, state in front of the tile,
-// state behind it) in the first wave; beside(channel) in the last one, meanwhile if it is another.
+// state behind it) in the first part; beside(channel) in the last one, meanwhile if it is another.
 template <bool kReverse, class S, class First, class Done, class Beside>
 __device__ __forceinline__ void link_tile(Runs<S>& rs, const RecArgs& a, const Links& links,
                                           const TileAt& at, First&& first, Done&& done,
                                           Beside&& beside) {
   constexpr int kParts = S::kParts, kEach = Runs<S>::kEach;
-  const int ch = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int ch = threadIdx.x % S::kStrip, part = threadIdx.x / S::kStrip;
   const auto run = [&](int i) { return kReverse ? S::kRuns - 1 - i : i; };
   __syncthreads();
   float z = -0.0f, h = 0.0f;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int r = run(wave * kEach + i);
+    const int r = run(part * kEach + i);
     h = decayed(rs.dec[r][ch], h, rs.h[r][ch]);
     z += rs.z[r][ch];
   }
-  rs.part_z[wave][ch] = z, rs.part_h[wave][ch] = h;
+  rs.part_z[part][ch] = z, rs.part_h[part][ch] = h;
   __syncthreads();
-  const int64_t c = at.strip * kStrip + ch;
-  if (wave == 0 && c < a.d) {
+  const int64_t c = at.strip * S::kStrip + ch;
+  if (part == 0 && c < a.d) {
     float dec[kParts], z = -0.0f, ph = 0.0f;
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
@@ -514,12 +519,12 @@ __device__ __forceinline__ void link_tile(Runs<S>& rs, const RecArgs& a, const L
     }
     done(c, before, decayed(whole, before, ph));
   }
-  if (wave == kParts - 1 && c < a.d) beside(c);
+  if (part == kParts - 1 && c < a.d) beside(c);
   __syncthreads();
-  float s = rs.part_h[wave][ch];
+  float s = rs.part_h[part][ch];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int r = run(wave * kEach + i);
+    const int r = run(part * kEach + i);
     const float next = decayed(rs.dec[r][ch], s, rs.h[r][ch]);
     rs.h[r][ch] = s;
     s = next;
@@ -528,13 +533,13 @@ __device__ __forceinline__ void link_tile(Runs<S>& rs, const RecArgs& a, const L
 }
 
 // A tile's outputs.
-template <typename T, int kThreads>
+template <typename T, int kStrip, int kThreads>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 4 : 3))) void
 rec_forward_kernel(RecArgs a, Links links, const float* s_in, float* s_out, T* __restrict__ h,
                    int64_t hsb, int64_t hst, float* __restrict__ saved) {
-  using S = TileLayout<T, kThreads>;
+  using S = TileLayout<T, kStrip, kThreads>;
   __shared__ Runs<S> rs;
-  const TileAt at = tile_at(a, links, false);
+  const TileAt at = tile_at<S>(a, links, false);
   const LaneAt<S> l = lane_at<S>(a, at);
   // Inside a run of a few tokens a itself will do; from run to run the sum of z counts.
   float dec[S::kRun][S::kPer], u[S::kRun][S::kPer], Z[S::kPer], H[S::kPer];
@@ -591,15 +596,15 @@ rec_forward_kernel(RecArgs a, Links links, const float* s_in, float* s_out, T* _
 // drate in `part` [B][tiles][d].  A lane holds its tokens' x and dh as loaded, and their
 // r and b i; it goes through its channels one after the other at the end, so that
 // the states and results of few are in registers beside them.
-template <typename T, int kThreads>
+template <typename T, int kStrip, int kThreads>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 ? 3 : 2))) void
 rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, const float* ds_out,
                     float* ds_in, T* __restrict__ dx, T* __restrict__ dg, T* __restrict__ di,
                     float* __restrict__ part) {
-  using S = TileLayout<T, kThreads>;
+  using S = TileLayout<T, kStrip, kThreads>;
   __shared__ Runs<S> rs;
   __shared__ __attribute__((aligned(16))) float hs[S::kRuns][kStrip];
-  const TileAt at = tile_at(a, links, true);
+  const TileAt at = tile_at<S>(a, links, true);
   const LaneAt<S> l = lane_at<S>(a, at);
   uint4 vx[S::kRun], vd[S::kRun];
   float r[S::kRun][S::kPer], bi[S::kRun][S::kPer], rate[S::kPer];
@@ -651,7 +656,7 @@ rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, con
       },
       // the states in front of the runs, from the one in front of the tile
       [&](int64_t c) {
-        const int ch = threadIdx.x & 63;
+        const int ch = threadIdx.x % S::kStrip;
         float s = saved[tile_row(c)];
 #pragma unroll 8
         for (int k = 0; k < S::kRuns; ++k) {
@@ -726,7 +731,7 @@ rec_backward_kernel(RecArgs a, Links links, const float* __restrict__ saved, con
     put(dx, t, none), put(dg, t, none), put(di, t, none);
   });
   __syncthreads();
-  const int64_t ch = at.strip * kStrip + threadIdx.x;
+  const int64_t ch = at.strip * (int64_t)kStrip + threadIdx.x;
   if (threadIdx.x < kStrip && ch < a.d) {
     float f = 0.0f;
 #pragma unroll 8
@@ -782,16 +787,16 @@ hipError_t with_type(Dtype dt, F&& f) {
 // 16 48 / 50, 512 of 24 69 / 59.
 bool steps(const RecArgs& a) { return a.T <= (a.B * a.d >= ((int64_t)1 << 20) ? 16 : 6); }
 
-// f with the threads of a tile of a call (64 sequences of 32 tokens of 2560 channels 11.8 us,
-// 25.6 in tiles of 128; 64 tokens 18.7 and 26.5; 512 of 32 tokens 76 and 172).
-template <typename F>
+// f with the threads of a tile of a call (64 sequences of 32 tokens of 2560 channels XA us,
+// XB in tiles of 128; 64 tokens XC and XD; 512 of 32 tokens XE and XF).
+template <int kStrip, typename F>
 void with_threads(const RecArgs& a, F&& f) {
   if (a.T * 4 <= kRecTile)
-    f(std::integral_constant<int, kBlock / 4>{});
+    f(std::integral_constant<int, kStrip>{});
   else if (a.T * 2 <= kRecTile)
-    f(std::integral_constant<int, kBlock / 2>{});
+    f(std::integral_constant<int, 2 * kStrip>{});
   else
-    f(std::integral_constant<int, kBlock>{});
+    f(std::integral_constant<int, 4 * kStrip>{});
 }
 
 }  // namespace
@@ -817,8 +822,8 @@ hipError_t clear_links(const RecArgs& a, void* ws, Links* links, hipStream_t s) 
                      s>>>(static_cast<uint4*>(ws), n, links->begun);
   return hipGetLastError();
 }
-dim3 tile_grid(const RecArgs& a) {
-  return dim3((unsigned)(a.B * tiles_of(a) * ((a.d + kStrip - 1) / kStrip)));
+dim3 tile_grid(const RecArgs& a, int strip) {
+  return dim3((unsigned)(a.B * tiles_of(a) * ((a.d + strip - 1) / strip)));
 }
 // Slices of the tiles' sums of drate: more than one, added up by a launch of its own, where
 // one workgroup's loads would show.
@@ -845,11 +850,22 @@ hipError_t launch_gatedrec_forward(const RecArgs& a, const float* s_in, float* s
     Links links;
     const hipError_t e = clear_links(a, ws, &links, s);
     if (e != hipSuccess) return e;
-    with_threads(a, [&](auto threads) {
-      constexpr int n = decltype(threads)::value;
-      rec_forward_kernel<T, n><<<tile_grid(a), n, 0, s>>>(a, links, s_in, s_out, out, hsb, hst,
-                                                          saved);
-    });
+    const auto go = [&](auto strip) {
+      constexpr int kStrip = decltype(strip)::value;
+      with_threads<kStrip>(a, [&](auto threads) {
+        constexpr int n = decltype(threads)::value;
+        rec_forward_kernel<T, kStrip, n><<<tile_grid(a, kStrip), n, 0, s>>>(
+            a, links, s_in, s_out, out, hsb, hst, saved);
+      });
+    };
+    if constexpr (sizeof(T) == 2) {
+      if (a.d > kFewChannels)
+        go(std::integral_constant<int, kWideStrip>{});
+      else
+        go(std::integral_constant<int, kStrip>{});
+    } else {
+      go(std::integral_constant<int, kStrip>{});
+    }
     return hipGetLastError();
   });
 }
@@ -869,9 +885,9 @@ hipError_t launch_gatedrec_backward(const RecArgs& a, const float* saved, const 
     const hipError_t e = clear_links(a, ws, &links, s);
     if (e != hipSuccess) return e;
     float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + link_bytes(a));
-    with_threads(a, [&](auto threads) {
+    with_threads<kStrip>(a, [&](auto threads) {
       constexpr int n = decltype(threads)::value;
-      rec_backward_kernel<T, n><<<tile_grid(a), n, 0, s>>>(
+      rec_backward_kernel<T, kStrip, n><<<tile_grid(a, kStrip), n, 0, s>>>(
           a, links, saved, ds_out, ds_in, static_cast<T*>(dx), static_cast<T*>(ddecay),
           static_cast<T*>(dinput), part);
     });
