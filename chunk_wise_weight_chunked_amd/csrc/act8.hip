@@ -205,7 +205,8 @@ __global__ __launch_bounds__(kBlock) void act8_operands_kernel(
 // one with a quarter, in whose stages the three terms' k-tiles lie side by side, so that x's
 // are loaded once for the three and a stage has three times the products (us, 1554 x 1024 x
 // 1536 32, 36 with one term after the other in two workgroups a CU; 136 x 200 x 2560 13 and 17,
-// 8192 x 2560 x 2560 318 and 349, 285 x 1000 x 7680 33 and 32).
+// 8192 x 2560 x 2560 318 and 349, 285 x 1000 x 7680 33 and 32; where the operands come from
+// memory wide tiles are faster, 32768 x 2560 x 7680 3574 and 4060).
 using WideTile = TileShape<256, 256, 2, 4>;
 using SmallTile = TileShape<128, 128, 2, 2>;
 using TermTile = TileShape<128, 128, 2, 4>;
@@ -651,7 +652,7 @@ Cut cut_of(const Act8Grad& g) {
     const int64_t round = side == 256 || beside ? 256 : 512, tiles = grad_tiles(g, side);
     // us of a k-tile or of three side by side (small ones take twice the operands for their work: more where those
     // come from memory) and around them, MB of a tile's sums
-    const double ktile = beside ? 1.0 : terms * (side == 256 ? 1.6 : cached ? 0.9 : 1.1);
+    const double ktile = beside ? cached ? 1.0 : 1.7 : terms * (side == 256 ? 1.6 : cached ? 0.9 : 1.1);
     const double around = side == 256 ? 14.0 : beside ? 6.0 : 5.0;
     const double sums = (double)side * side * 8e-6;
     const int64_t rest = tiles % round;

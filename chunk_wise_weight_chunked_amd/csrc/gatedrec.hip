@@ -17,9 +17,9 @@
 // Both directions are bound by HBM and read their inputs once: a workgroup loads a
 // tile, publishes its map, takes the state in front of it from the tiles in front (through
 // their maps, from the nearest place whose state is known) and writes the tile's
-// results from its registers.  2560 channels in bf16: 131072 tokens 579 us, 4.6 TB/s; 32768
-// forward 160 us, backward 258 us, 4.5 TB/s with a vector instruction at work in 78% of the
-// SIMDs' cycles; in fp32 243 and 431 us, 5.5 TB/s.
+// results from its registers.  2560 channels in bf16: 131072 tokens 523 us, 5.1 TB/s; 32768
+// forward 143 us, backward 252 us, 4.7 TB/s with a vector instruction at work in 78% of the
+// SIMDs' cycles; in fp32 240 and 428 us, 5.6 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -33,9 +33,10 @@ namespace {
 
 constexpr int kBlock = 256;
 // Channels of a tile.  Rows of 256 bytes are read and written faster than rows of 128: the
-// forward takes 128 channels in bf16 where there are more than 64 (131072 tokens of 2560 YA us,
-// 579 with 64) and 64 in fp32 (65536 tokens 465 us, 480 with 128).  The backward takes 64: with
-// its registers a tile of 128 has a CU for itself (32768 tokens 254 us, 312 with 128).
+// forward takes 128 channels in bf16 where there are more than 64 (131072 tokens of 2560 523 us,
+// 580 with 64) and 64 in fp32 (65536 tokens 465 us, 480 with 128).  The backward takes 64: with
+// its registers a tile of 128 has a CU for itself (32768 tokens 252 us, 312 with 128; in tiles
+// of 64 tokens, of which 128 channels take no more, 260: it is the vector units that bound it).
 constexpr int kStrip = 64, kWideStrip = 128, kFewChannels = 64;
 
 // Exponents are base 2 throughout: z is log2 a = -rate log2(e) r.
@@ -782,13 +783,13 @@ hipError_t with_type(Dtype dt, F&& f) {
 }
 // Whether a call takes the recurrent form.  A lane's tokens take it 0.8 us each, or what
 // the memory takes for them; a tile takes 8 us whatever it holds, and many at once 2.5 ns
-// each.  us of 2560 channels, recurrent / tiles: 1 sequence of 8 tokens 9.9 / 8.0, 64 of 4 8.0 /
-// 10.0, 64 of 6 8.9 / 10.0, 64 of 8 10.5 / 10.1, 64 of 12 14.7 / 10.3, 512 of 8 27 / 47, 512 of
-// 16 48 / 50, 512 of 24 69 / 59.
+// each.  us of 2560 channels, recurrent / tiles: 1 sequence of 8 tokens 9.9 / 7.9, 64 of 4 7.8 /
+// 9.9, 64 of 6 8.9 / 10.0, 64 of 8 10.5 / 10.1, 64 of 12 14.6 / 10.6, 512 of 8 27 / 48, 512 of
+// 16 48 / 49, 512 of 24 69 / 55.
 bool steps(const RecArgs& a) { return a.T <= (a.B * a.d >= ((int64_t)1 << 20) ? 16 : 6); }
 
-// f with the threads of a tile of a call (64 sequences of 32 tokens of 2560 channels XA us,
-// XB in tiles of 128; 64 tokens XC and XD; 512 of 32 tokens XE and XF).
+// f with the threads of a tile of a call (64 sequences of 32 tokens of 2560 channels 11.8
+// us, 25.9 in tiles of 128; 64 tokens 17.6 and 26.8; 512 of 32 tokens 68 and 172).
 template <int kStrip, typename F>
 void with_threads(const RecArgs& a, F&& f) {
   if (a.T * 4 <= kRecTile)
