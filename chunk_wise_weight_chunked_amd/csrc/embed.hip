@@ -3,7 +3,7 @@
 //
 //   out[n] = scale table[ids[n]],   grad[v] (+)= scale sum_{n: ids[n] = v} dout[n]
 //
-// The lookup copies rows: bound by HBM.  The gradient sorts the tokens by id
+// The lookup copies rows: bound by memory and caches.  The gradient sorts the tokens by id
 // (least significant digit first, stable, so that equal ids keep the order of
 // their places), cuts the sorted tokens into pieces of 8 to 32 and lets a wave sum
 // a piece's rows in registers: an id whose tokens lie in one piece gets its row
@@ -11,9 +11,10 @@
 // are added in order by a last launch.  No atomic sums: the result does not
 // depend on what runs when.  Up to 64 tokens take one launch without a sort.
 //
-// The lookup of 131072 rows of 2560 bf16 values takes 185 us (4.35 TB/s, five bytes written
-// for each read).  The gradient of 32768 tokens of 2560 into 50001 fp32 rows takes 181 us: the
-// sort's launches, each some 4 to 8 us of waiting for the one before, and 4.2 TB/s.
+// The lookup of 131072 rows of 2560 bf16 values takes 185 us: 1.34 GB into and out of the L2s
+// at 7.3 TB/s, many rows again and again from the last-level cache.  The gradient of 32768
+// tokens of 2560 into 50001 fp32 rows takes 181 us: the sort's launches, each some 4 to 8 us
+// of waiting for the one before, and 4.2 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
