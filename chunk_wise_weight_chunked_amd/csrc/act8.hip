@@ -201,12 +201,15 @@ __global__ __launch_bounds__(kBlock) void act8_operands_kernel(
     split_block(dy, dys, terms, part, rows, n, blockIdx.y - x_columns);
 }
 
-// Tiles of the gradient: a workgroup a CU, or two with a quarter of it each; for dy's terms
-// one with a quarter, in whose stages the three terms' k-tiles lie side by side, so that x's
-// are loaded once for the three and a stage has three times the products (us, 1554 x 1024 x
-// 1536 32, 36 with one term after the other in two workgroups a CU; 136 x 200 x 2560 13 and 17,
-// 8192 x 2560 x 2560 318 and 349, 285 x 1000 x 7680 33 and 32; where the operands come from
-// memory wide tiles are faster, 32768 x 2560 x 7680 3574 and 4060).
+// Tiles of the gradient: a workgroup a CU, or two with a quarter of it each.  For dy's terms a
+// quarter, in whose stages the three terms' k-tiles lie side by side, so that x's are loaded
+// once for the three and a stage has three times the products: with two stages, one workgroup a
+// CU, or where there are more tiles than CUs with one stage, two workgroups that cover each
+// other's loads and results.  us, one term after the other in two workgroups a CU / side by
+// side in two stages / in one: 1554 x 1024 x 1536 36 / 32 / 35, 136 x 200 x 2560 17 / 13 / 14,
+// 8192 x 2560 x 2560 349 / 317 / 302, 3000 x 2560 x 2560 137 / 132 / 115, 199 x 4096 x 1536 26 /
+// 28 / 23; where the operands come from memory wide tiles are faster, 32768 x 2560 x 7680 3574
+// and 4060.
 using WideTile = TileShape<256, 256, 2, 4>;
 using SmallTile = TileShape<128, 128, 2, 2>;
 using TermTile = TileShape<128, 128, 2, 4>;
@@ -430,14 +433,25 @@ struct TermMma {
 };
 
 // The mainloop of gemm_core.h on these fragments: k-tile kt + 1's loads one after each of
-// kt's first matrix instructions.
-template <class Mma, int kStageBytes, class S, class LA, class LB>
+// kt's first matrix instructions.  In one stage a k-tile's loads, then its products.
+template <class Mma, int kStages, int kStageBytes, class S, class LA, class LB>
 __device__ __forceinline__ void grad_mainloop(Accum<S>& acc, LA& la, LB& lb, int64_t nk,
                                               lds_char* smem, const LanePos& p) {
   constexpr int kLoads = LA::kPer + LB::kPer;
   static_assert(kLoads <= Mma::kSteps * S::MB * S::NB, "the loads fit the k-tile's MFMAs");
   Mma mma;
   mma.init(p);
+  if constexpr (kStages == 1) {
+    for (int64_t kt = 0; kt < nk; ++kt) {
+      la.issue(kt, smem);
+      lb.issue(kt, smem + S::BM * kRowBytes);
+      wait_vmcnt<0>();
+      __syncthreads();
+      mma.ktile(acc, smem, smem + S::BM * kRowBytes, p, [](int) {});
+      __syncthreads();
+    }
+    return;
+  }
   la.issue(0, smem);
   lb.issue(0, smem + S::BM * kRowBytes);
   wait_vmcnt<0>();
@@ -474,14 +488,15 @@ struct GradArgs {
   bool accumulate;
 };
 
-template <typename TO, class S, bool kTerms>
-__global__ __launch_bounds__(S::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void
+template <typename TO, class S, bool kTerms, int kStages>
+__global__ __launch_bounds__(S::kThreads)
+__attribute__((amdgpu_waves_per_eu(kStages == 1 ? 4 : 2))) void
 act8_grad_kernel(GradArgs g) {
-  static_assert(S::kLdsBytes >= S::BM * kEpiStride * 4, "epilogue stage fits the pipeline's LDS");
   constexpr bool kBeside = std::is_same_v<S, TermTile>;
   constexpr int kParts = kTerms && !kBeside ? 3 : 1;
   constexpr int kStageBytes = S::kStageBytes + (kBeside ? 2 * S::BN * kRowBytes : 0);
-  __shared__ __attribute__((aligned(16))) char smem_raw[2 * kStageBytes];
+  static_assert(kStages * kStageBytes >= S::BM * kEpiStride * 4, "epilogue stage fits the pipeline's LDS");
+  __shared__ __attribute__((aligned(16))) char smem_raw[kStages * kStageBytes];
   lds_char* smem = (lds_char*)smem_raw;
   const int tiles_m = (int)((g.M + S::BM - 1) / S::BM), tiles_n = (int)((g.N + S::BN - 1) / S::BN);
   int tile, slice = -1;
@@ -503,15 +518,15 @@ act8_grad_kernel(GradArgs g) {
   PartLoader<DirectLoader<S::BM, S::kWaves>, kParts> la{lx, n, 0};
   if constexpr (kBeside) {
     TermLoader<S> lb{block_loader<S, S::BN>(g.dy, g.N, n0, k0), g.dy_part * 2};
-    grad_mainloop<TermMma<S>, kStageBytes>(acc, la, lb, n, smem, p);
+    grad_mainloop<TermMma<S>, kStages, kStageBytes>(acc, la, lb, n, smem, p);
   } else if constexpr (kTerms) {
     const auto ly = block_loader<S, S::BN>(g.dy, g.N, n0, k0);
     PartLoader<DirectLoader<S::BN, S::kWaves>, kParts> lb{ly, n, g.dy_part * 2};
-    grad_mainloop<GradMma<S, false>, kStageBytes>(acc, la, lb, n * kParts, smem, p);
+    grad_mainloop<GradMma<S, false>, kStages, kStageBytes>(acc, la, lb, n * kParts, smem, p);
   } else {
     PartLoader<RowLoader<S>, 1> lb;
     lb.l.init(g.dy, g.dys, g.rows, g.N, n0, k0);
-    grad_mainloop<GradMma<S, true>, kStageBytes>(acc, la, lb, n, smem, p);
+    grad_mainloop<GradMma<S, true>, kStages, kStageBytes>(acc, la, lb, n, smem, p);
   }
   if (slice >= 0) {
     // as the accumulators hold them: act8_sum_kernel finds the rows and columns
@@ -625,6 +640,9 @@ int64_t grad_tiles(const Act8Grad& g, int64_t side) {
   return ((g.d_in + side - 1) / side) * ((g.d_out + side - 1) / side);
 }
 
+// Whether small tiles of dy's terms take a CU in pairs.
+bool many_tiles(const Act8Grad& g) { return grad_tiles(g, TermTile::BM) > 256; }
+
 // How the gradient is cut: tiles of 256 or 128, `whole` of them a workgroup's each, the
 // others in `slices` of `slice` k-tiles.
 struct Cut {
@@ -648,12 +666,13 @@ Cut cut_of(const Act8Grad& g) {
   Cut best{};
   double least = -1;
   for (const int side : {256, 128}) {
-    const bool beside = side == 128 && terms > 1;  // one workgroup a CU
-    const int64_t round = side == 256 || beside ? 256 : 512, tiles = grad_tiles(g, side);
+    const bool beside = side == 128 && terms > 1, alone = beside && !many_tiles(g);
+    const int64_t round = side == 256 || alone ? 256 : 512, tiles = grad_tiles(g, side);
     // us of a k-tile or of three side by side (small ones take twice the operands for their work: more where those
     // come from memory) and around them, MB of a tile's sums
-    const double ktile = beside ? cached ? 1.0 : 1.7 : terms * (side == 256 ? 1.6 : cached ? 0.9 : 1.1);
-    const double around = side == 256 ? 14.0 : beside ? 6.0 : 5.0;
+    const double ktile = beside ? (alone ? 1.0 : 1.9) * (cached ? 1.0 : 1.7)
+                                : terms * (side == 256 ? 1.6 : cached ? 0.9 : 1.1);
+    const double around = side == 256 ? 14.0 : alone ? 6.0 : 5.0;
     const double sums = (double)side * side * 8e-6;
     const int64_t rest = tiles % round;
     const double before = (double)(tiles / round) * ((double)n * ktile + around);
@@ -686,14 +705,14 @@ GradPlan grad_plan(const Act8Grad& g) {
   return p;
 }
 
-template <class S, bool kTerms>
+template <class S, bool kTerms, int kStages>
 hipError_t launch_products(const Act8Grad& g, const GradArgs& a, hipStream_t s) {
   const int64_t rest = grad_tiles(g, S::BM) - a.whole;
   const dim3 grid((unsigned)(a.whole + rest * a.slices));
   const dim3 sums((unsigned)(rest * (S::BM * S::BN / (4 * kBlock))));
   const auto go = [&](auto to) {
     using TO = decltype(to);
-    act8_grad_kernel<TO, S, kTerms><<<grid, S::kThreads, 0, s>>>(a);
+    act8_grad_kernel<TO, S, kTerms, kStages><<<grid, S::kThreads, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || rest == 0) return e;
     act8_sum_kernel<TO, S><<<sums, kBlock, 0, s>>>(a);
@@ -765,8 +784,11 @@ hipError_t launch_act8_weight_grad(const Act8Grad& g, const int8_t* codes, const
   });
   if (e != hipSuccess) return e;
   if (p.cut.side == 256)
-    return split ? launch_products<WideTile, true>(g, a, s) : launch_products<WideTile, false>(g, a, s);
-  return split ? launch_products<TermTile, true>(g, a, s) : launch_products<SmallTile, false>(g, a, s);
+    return split ? launch_products<WideTile, true, 2>(g, a, s)
+                 : launch_products<WideTile, false, 2>(g, a, s);
+  if (!split) return launch_products<SmallTile, false, 2>(g, a, s);
+  return many_tiles(g) ? launch_products<TermTile, true, 1>(g, a, s)
+                       : launch_products<TermTile, true, 2>(g, a, s);
 }
 
 }  // namespace ttt
