@@ -213,8 +213,6 @@ __global__ __launch_bounds__(kBlock) void act8_operands_kernel(
 using WideTile = TileShape<256, 256, 2, 4>;
 using SmallTile = TileShape<128, 128, 2, 2>;
 using TermTile = TileShape<128, 128, 2, 4>;
-constexpr int kEpiCols = 64;
-constexpr int kEpiStride = kEpiCols + 8;  // floats per staged row
 
 // k-tiles [k0, k0 + n) of an operand, kParts times: of x again and again, of dy's terms
 // one after the other (part_stride bytes between them; wide tiles, of whose stages three terms
@@ -492,11 +490,14 @@ template <typename TO, class S, bool kTerms, int kStages>
 __global__ __launch_bounds__(S::kThreads)
 __attribute__((amdgpu_waves_per_eu(kStages == 1 ? 4 : 2))) void
 act8_grad_kernel(GradArgs g) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host's pass takes the name alone
   constexpr bool kBeside = std::is_same_v<S, TermTile>;
   constexpr int kParts = kTerms && !kBeside ? 3 : 1;
   constexpr int kStageBytes = S::kStageBytes + (kBeside ? 2 * S::BN * kRowBytes : 0);
-  static_assert(kStages * kStageBytes >= S::BM * kEpiStride * 4, "epilogue stage fits the pipeline's LDS");
-  __shared__ __attribute__((aligned(16))) char smem_raw[kStages * kStageBytes];
+  constexpr int kEpiCols = 64, kEpiStride = kEpiCols + 8;  // floats per staged row of results
+  constexpr int kEpiBytes = S::BM * kEpiStride * 4;
+  constexpr int kBytes = kStages * kStageBytes > kEpiBytes ? kStages * kStageBytes : kEpiBytes;
+  __shared__ __attribute__((aligned(16))) char smem_raw[kBytes];
   lds_char* smem = (lds_char*)smem_raw;
   const int tiles_m = (int)((g.M + S::BM - 1) / S::BM), tiles_n = (int)((g.N + S::BN - 1) / S::BN);
   int tile, slice = -1;
@@ -577,6 +578,7 @@ act8_grad_kernel(GradArgs g) {
       Piece<TO>::store(to, v);
     }
   }
+#endif
 }
 
 // The tiles that came in slices, added in order: a lane has 4 rows of a column, as they
@@ -640,8 +642,15 @@ int64_t grad_tiles(const Act8Grad& g, int64_t side) {
   return ((g.d_in + side - 1) / side) * ((g.d_out + side - 1) / side);
 }
 
-// Whether small tiles of dy's terms take a CU in pairs.
-bool many_tiles(const Act8Grad& g) { return grad_tiles(g, TermTile::BM) > 256; }
+// Whether small tiles take one stage, and so twice as many workgroups a CU, which cover each
+// other's loads and results: with dy's terms where there are more tiles than CUs, else where
+// there are more tiles than two a CU and the sums are short (us with one stage / two: 200 x 2560 x
+// 4096 20 / 23, 300 x 5120 x 7680 51 / 57, 700 x 2568 x 3336 29 / 35, 1776 x 4096 x 1536 44 / 41,
+// 2048 x 2560 x 2560 48 / 42).
+bool one_stage(const Act8Grad& g) {
+  const int64_t tiles = grad_tiles(g, SmallTile::BM);
+  return g.dt == Dtype::F32 ? tiles > 256 : tiles > 512 && ktiles_of(g) <= 16;
+}
 
 // How the gradient is cut: tiles of 256 or 128, `whole` of them a workgroup's each, the
 // others in `slices` of `slice` k-tiles.
@@ -666,12 +675,14 @@ Cut cut_of(const Act8Grad& g) {
   Cut best{};
   double least = -1;
   for (const int side : {256, 128}) {
-    const bool beside = side == 128 && terms > 1, alone = beside && !many_tiles(g);
-    const int64_t round = side == 256 || alone ? 256 : 512, tiles = grad_tiles(g, side);
+    const bool beside = side == 128 && terms > 1, single = side == 128 && one_stage(g);
+    const bool alone = beside && !single;
+    const int64_t round = side == 256 || alone ? 256 : single && !beside ? 1024 : 512;
+    const int64_t tiles = grad_tiles(g, side);
     // us of a k-tile or of three side by side (small ones take twice the operands for their work: more where those
     // come from memory) and around them, MB of a tile's sums
     const double ktile = beside ? (alone ? 1.0 : 1.9) * (cached ? 1.0 : 1.7)
-                                : terms * (side == 256 ? 1.6 : cached ? 0.9 : 1.1);
+                                : terms * (side == 256 ? 1.6 : (cached ? 0.9 : 1.1) * (single ? 2 : 1));
     const double around = side == 256 ? 14.0 : alone ? 6.0 : 5.0;
     const double sums = (double)side * side * 8e-6;
     const int64_t rest = tiles % round;
@@ -710,18 +721,18 @@ hipError_t launch_products(const Act8Grad& g, const GradArgs& a, hipStream_t s) 
   const int64_t rest = grad_tiles(g, S::BM) - a.whole;
   const dim3 grid((unsigned)(a.whole + rest * a.slices));
   const dim3 sums((unsigned)(rest * (S::BM * S::BN / (4 * kBlock))));
-  const auto go = [&](auto to) {
-    using TO = decltype(to);
-    act8_grad_kernel<TO, S, kTerms, kStages><<<grid, S::kThreads, 0, s>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || rest == 0) return e;
-    act8_sum_kernel<TO, S><<<sums, kBlock, 0, s>>>(a);
-    return hipGetLastError();
-  };
-  if constexpr (kTerms)
-    return go(float{});
-  else
-    return g.grad_dt == Dtype::F32 ? go(float{}) : go(uint16_t{});
+  const bool f32 = kTerms || g.grad_dt == Dtype::F32;
+  if (f32)
+    act8_grad_kernel<float, S, kTerms, kStages><<<grid, S::kThreads, 0, s>>>(a);
+  else if constexpr (!kTerms)
+    act8_grad_kernel<uint16_t, S, kTerms, kStages><<<grid, S::kThreads, 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || rest == 0) return e;
+  if (f32)
+    act8_sum_kernel<float, S><<<sums, kBlock, 0, s>>>(a);
+  else if constexpr (!kTerms)
+    act8_sum_kernel<uint16_t, S><<<sums, kBlock, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -786,9 +797,11 @@ hipError_t launch_act8_weight_grad(const Act8Grad& g, const int8_t* codes, const
   if (p.cut.side == 256)
     return split ? launch_products<WideTile, true, 2>(g, a, s)
                  : launch_products<WideTile, false, 2>(g, a, s);
-  if (!split) return launch_products<SmallTile, false, 2>(g, a, s);
-  return many_tiles(g) ? launch_products<TermTile, true, 1>(g, a, s)
-                       : launch_products<TermTile, true, 2>(g, a, s);
+  if (!split)
+    return one_stage(g) ? launch_products<SmallTile, false, 1>(g, a, s)
+                        : launch_products<SmallTile, false, 2>(g, a, s);
+  return one_stage(g) ? launch_products<TermTile, true, 1>(g, a, s)
+                      : launch_products<TermTile, true, 2>(g, a, s);
 }
 
 }  // namespace ttt

@@ -536,7 +536,8 @@ def test_act8_weight_grad(rows, d_in, d_out, dtype, gd):
 @pytest.mark.parametrize("rows,d_in,d_out,dtype,gd", [
     (8229, 2600, 6664, BF16, F32), (8229, 2600, 6664, BF16, BF16), (8229, 2600, 6664, F32, F32),
     (33001, 1032, 4104, BF16, F32), (17001, 1032, 4104, F32, F32), (130, 3000, 6000, BF16, F32),
-    (700, 2568, 3336, F32, F32), (4000, 4104, 2056, BF16, F32)])
+    (700, 2568, 3336, F32, F32), (4000, 4104, 2056, BF16, F32),
+    (700, 2568, 3336, BF16, F32), (700, 2568, 3336, BF16, BF16), (1100, 4104, 2056, BF16, F32)])
 def test_act8_weight_grad_large(rows, d_in, d_out, dtype, gd):
     say(rows, d_in, d_out, dtype, gd)
     g = torch.Generator(device="cuda")

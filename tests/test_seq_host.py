@@ -478,7 +478,7 @@ def test_no_load_into_lds_is_in_flight_at_a_barrier(tmp_path):
                 assert not flying, (name, x)
                 barriers += "s_barrier" in x
         assert not flying, name
-    assert found == 7 and barriers >= 3 * found and reads >= 4 * 4, (found, barriers, reads)
+    assert found == 9 and barriers >= 3 * found and reads >= 4 * 4, (found, barriers, reads)
 
 
 @pytest.mark.skipif(not os.path.exists("/opt/rocm/bin/hipcc"), reason="hipcc not available")
