@@ -82,10 +82,11 @@ __device__ __forceinline__ float root_arg(float z, float a, float floor) {
 }
 
 constexpr float kLog2e = 0x1.715476p+0f;
-// -log2(e) rate; z is never positive: a rate below 0 counts as NaN.  2^100 is as good as
-// any above it, and 0 times it is 0.
+// -log2(e) rate; z is never positive: a rate below 0 counts as NaN, and one of 0 of either sign
+// gives -0, a z that decay_of keeps the sign of.  2^100 is as good as any above it, and 0 times
+// it is 0.
 __device__ __forceinline__ float log_rate(float r) {
-  return r >= 0.0f ? -kLog2e * fminf(r, 0x1p100f) : __builtin_nanf("");
+  return r >= 0.0f ? -kLog2e * fminf(fabsf(r), 0x1p100f) : __builtin_nanf("");
 }
 __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));

@@ -405,6 +405,33 @@ def test_gatedrec_values_out_of_the_ordinary(T):
     assert all(torch.equal(a, b) for a, b in zip(clean[:3], (x, dg, ig)) if a.isfinite().all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [1, 6, 40, 400])
+def test_gatedrec_rates_of_minus_zero(T, dtype):
+    """-0.0 (minus the logarithm of 1) is a rate of 0: the state and what comes from behind are
+    kept, bit for bit as with 0.0."""
+    B, d = 2, 72
+    g, x, dg, ig, rate, st = rec_inputs(B, T, d, dtype, T)
+    dh, ds = normal(g, B, T, d, dtype=dtype), normal(g, B, d)
+    rate[::2] = 0.0
+    minus = torch.where(rate == 0, -rate, rate)
+    assert torch.signbit(minus[::2]).all()
+    results = []
+    for r in (rate, minus):
+        h, S, saved = seq.gatedrec_forward(x, dg, ig, r, state=st, save=True)
+        got = seq.gatedrec_backward(x, dg, ig, r, dh, saved, dstate_out=ds)
+        results.append([h, S, saved, *got.values()])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    h, S, saved = results[1][:3]
+    kept = [c for c in range(0, d, 2)]
+    assert torch.equal(S[:, kept], st[:, kept])
+    assert (h[..., kept] == st[:, None, kept].to(dtype)).all()
+    assert (saved[..., kept] == st[:, None, kept]).all()
+    want = ref.gatedrec_grads(*(f64(t) for t in (x, dg, ig, minus, dh, st, ds)))
+    assert rel(f64(got["state"]), want[4]) <= TOL_F32
+    assert rel(f64(got["rate"]), want[3]) <= TOL_F32
+
+
 def test_gatedrec_in_pieces():
     """A sequence fed in calls of any lengths gives one call's outputs to rounding."""
     B, T, d = 2, 700, 136
