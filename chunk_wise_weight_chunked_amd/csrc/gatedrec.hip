@@ -91,14 +91,10 @@ __device__ __forceinline__ float log_rate(float r) {
 __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
 }
-// 2^-32 of it, beside 2^32 b
-__device__ __forceinline__ float sigmoid_scaled(float x) {
-  return __builtin_amdgcn_rcpf(
-      __builtin_fmaf(__builtin_amdgcn_exp2f(-kLog2e * x), 0x1p32f, 0x1p32f));
-}
-// b i from z, a and the input gate
+// b i from z, a and the input gate.  The root's 2^32 is taken off b, which is never below 2^-75,
+// and not off i, which may be any normal number (2^-126 at a gate of -87).
 __device__ __forceinline__ float gated(float z, float a, float gate) {
-  return __builtin_amdgcn_sqrtf(root_arg(z, a, 0.0f)) * sigmoid_scaled(gate);
+  return __builtin_amdgcn_sqrtf(root_arg(z, a, 0.0f)) * 0x1p-32f * sigmoid(gate);
 }
 
 // Two values as bf16 (RNE), by one instruction.

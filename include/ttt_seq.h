@@ -71,7 +71,8 @@ ttt_status_t ttt_embed_backward(const ttt_embed_desc_t* desc, const void* ids, c
  *   h_t = a_t h_{t-1} + b_t i_t x_t
  * from h = state_in (or 0).  The state is one fp32 value a channel; everything is
  * computed in fp32 (a decay near 1 by its distance from 1, so that long memories
- * lose nothing to its rounding) and h rounded once.
+ * lose nothing to its rounding) and h rounded once.  A sigmoid below 2^-126, fp32's
+ * smallest normal number (a gate below -87.3), counts as 0.
  *
  *   batch, seq_len  B sequences of T tokens, 1 <= B <= 2^20, T >= 1, B T <= 2^29
  *   d         channels, a multiple of 8, 8 <= d <= 2^20; B d <= 2^28, B T d <= 2^35

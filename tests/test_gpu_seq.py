@@ -432,6 +432,35 @@ def test_gatedrec_rates_of_minus_zero(T, dtype):
     assert rel(f64(got["rate"]), want[3]) <= TOL_F32
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [6, 40, 400])
+def test_gatedrec_input_gates_far_down(T, dtype):
+    """An input gate counts for as long as its sigmoid is a normal number of fp32 (2^-126 at a gate
+    of -87.3): a channel a gate, x and dh large enough for the results to be normal too."""
+    gates = torch.tensor([-20.0, -40.0, -60.0, -64.0, -66.0, -67.0, -68.0, -70.0, -75.0, -80.0,
+                          -84.0, -85.0, -86.0, -87.0, -50.0, -30.0])
+    d = len(gates)
+    g, x, dg, _, rate, _ = rec_inputs(2, T, d, dtype, T + 1)
+    ig = gates.to(dtype).cuda().expand(2, T, d)
+    x, dh = x * 2.0 ** 30, normal(g, 2, T, d, dtype=dtype, std=2.0 ** 30)
+    h, S, saved = seq.gatedrec_forward(x, dg, ig, rate, save=True)
+    got = seq.gatedrec_backward(x, dg, ig, rate, dh, saved)
+    a = [f64(t) for t in (x, dg, ig, rate)]
+    h64, S64 = ref.gatedrec(*a)
+    want = ref.gatedrec_grads(*a, f64(dh))
+    pairs = [("h", h, h64), ("state", S, S64)]
+    pairs += [(n, got[n], w) for n, w in zip(("x", "decay_gate", "input_gate"), want)]
+    for c, gate in enumerate(ig[0, 0].tolist()):
+        # e^-gate is 2 to a product of the gate and log2 e, which are rounded by 2^-24 and 2^-26
+        # of it: as much of the exponent is off.  ddecay is the difference of two such terms
+        # that do not depend on each other: sqrt(2) of what one may be off.
+        far = 1.25 * abs(gate) * 2.0 ** -24
+        for n, t, w in pairs:
+            e = rel(f64(t)[..., c], w[..., c])
+            tol = (TOL_F32 if n == "state" else TOL[dtype]) + far
+            assert e <= tol * (2 ** 0.5 if n == "decay_gate" else 1), (n, gate, e)
+
+
 def test_gatedrec_in_pieces():
     """A sequence fed in calls of any lengths gives one call's outputs to rounding."""
     B, T, d = 2, 700, 136
