@@ -840,6 +840,49 @@ def test_rows_behind_the_last_are_left_alone():
     assert rest(grad, d * m) and rest(ws, ws.numel() - 64)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N", [6, 400])
+def test_inputs_keep_their_bits(N, dtype):
+    """What a call only reads is the same to the bit behind it, infinities and NaN included."""
+    g = gen(27)
+    d, V, m = 72, 50, 40
+    x, dg, ig, dh, dy = (normal(g, 1, N, n, dtype=dtype) for n in (d, d, d, d, m))
+    rate, st, ds = torch.full((d,), 0.05, device="cuda"), normal(g, 1, d), normal(g, 1, d)
+    ids, lengths = some_ids(g, N, V, torch.int64)[None].cuda(), torch.tensor([N - 1]).int().cuda()
+    table = normal(g, V, d, dtype=dtype)
+    rate[0], rate[1], rate[2] = -0.0, 1e30, -1.0
+    for i, t in enumerate((x, dg, ig, dh, dy, table[None], st[None], ds[None])):
+        t[0, -1, 3 + i], t[0, 0, 4 + i], t[0, 0, 5 + i] = float("inf"), -float("inf"), float("nan")
+    codes, exps = seq.act8_store(x)
+    inputs = [x, dg, ig, dh, dy, rate, st, ds, ids, lengths, table, codes, exps]
+    bits = lambda t: t.contiguous().view(torch.uint8)  # noqa: E731
+    keep = [t.clone() for t in inputs]
+
+    def check(name):
+        for t, k in zip(inputs, keep):
+            assert torch.equal(bits(t), bits(k)), name
+
+    seq.embed_forward(ids, table, 2.0)
+    check("embed_forward")
+    seq.embed_backward(dh, ids, V, 2.0)
+    seq.embed_backward(dh, ids, V, grad=normal(g, V, d))
+    check("embed_backward")
+    for ln in (None, lengths):
+        _, _, saved = seq.gatedrec_forward(x, dg, ig, rate, state=st, lengths=ln, save=True)
+        check("gatedrec_forward")
+        old = saved.clone()
+        seq.gatedrec_backward(x, dg, ig, rate, dh, saved, dstate_out=ds, lengths=ln)
+        check("gatedrec_backward")
+        assert torch.equal(bits(saved), bits(old))
+    seq.act8_store(x)
+    check("act8_store")
+    seq.act8_load(codes, exps, dtype)
+    check("act8_load")
+    seq.act8_weight_grad(codes, exps, dy)
+    seq.act8_weight_grad(codes, exps, dy, grad=normal(g, d, m))
+    check("act8_weight_grad")
+
+
 # ---------------------------------------------------------- offsets beyond 32 bits
 def test_embed_tables_beyond_32_bits():
     g = torch.Generator(device="cuda")
