@@ -26,6 +26,7 @@
 #include <algorithm>
 
 #include "gemm_core.h"
+#include "rec_link.h"
 #include "seq.h"
 
 namespace ttt {
@@ -38,35 +39,6 @@ constexpr int kBlock = 256;
 // its registers a tile of 128 has a CU for itself (32768 tokens 252 us, 312 with 128; in tiles
 // of 64 tokens, of which 128 channels take no more, 260: it is the vector units that bound it).
 constexpr int kStrip = 64, kWideStrip = 128, kFewChannels = 64;
-
-// Exponents are base 2 throughout: z is log2 a = -rate log2(e) r.
-//
-// A decay over a run of tokens as one float: 2^z itself (sign bit clear) or, where
-// z > -1/2, 2^z - 1 (sign bit set, -0 for z = 0).  The second keeps what a decay near 1
-// loses by its rounding, which would be repeated for as long as the channel remembers.
-// The polynomial is 2^z - 1 to 3.3e-8 of it (Chebyshev nodes in [-1/2, 0]).
-__device__ __forceinline__ float decay_of(float z) {
-  float p = __builtin_fmaf(z, 0x1.2ee444p-10f, 0x1.38ae68p-7f);
-  p = __builtin_fmaf(z, p, 0x1.c6947ap-5f);
-  p = __builtin_fmaf(z, p, 0x1.ebfb70p-3f);
-  p = __builtin_fmaf(z, p, 0x1.62e430p-1f);
-  const float near = z * p, far = __builtin_amdgcn_exp2f(z);
-  return z > -0.5f ? near : far;  // a z of -0 gives -0
-}
-__device__ __forceinline__ bool near_one(float dec) { return __float_as_uint(dec) >> 31; }
-// The decay over two runs.
-__device__ __forceinline__ float decay_both(float d1, float d2) {
-  const bool n1 = near_one(d1), n2 = near_one(d2);
-  // a1 a2 - 1, never positive, and a1 a2 where that is far from 0
-  const float near = -fabsf(__builtin_fmaf(d1, d2, d1 + d2));
-  const float both = near < -0.5f ? 1.0f + near : near;
-  const float far = __builtin_fmaf(d1, d2, n1 ? d2 : n2 ? d1 : 0.0f);
-  return n1 && n2 ? both : far;
-}
-// a h + u
-__device__ __forceinline__ float decayed(float dec, float h, float u) {
-  return __builtin_fmaf(dec, h, u) + (near_one(dec) ? h : 0.0f);
-}
 
 // 2^64 (1 - a^2) from a and its z: near a = 1 by the same polynomial of 2 z.  The roots'
 // instructions take values below 2^-126 as 0, which 2^64 times the smallest is not: b
@@ -81,13 +53,6 @@ __device__ __forceinline__ float root_arg(float z, float a, float floor) {
   return z > -0.25f ? near : far;
 }
 
-constexpr float kLog2e = 0x1.715476p+0f;
-// -log2(e) rate; z is never positive: a rate below 0 counts as NaN, and one of 0 of either sign
-// gives -0, a z that decay_of keeps the sign of.  2^100 is as good as any above it, and 0 times
-// it is 0.
-__device__ __forceinline__ float log_rate(float r) {
-  return r >= 0.0f ? -kLog2e * fminf(fabsf(r), 0x1p100f) : __builtin_nanf("");
-}
 __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
 }
@@ -216,33 +181,16 @@ __global__ __launch_bounds__(kBlock) void rec_step_kernel(RecArgs a, const float
 }
 
 // ------------------------------------------------- tiles and what links them
-// A tile leaves a word for the tiles behind it (backward: in front of it), one for each
-// channel: its map, the decay over the tile and the state behind it from 0.  kGroup tiles
-// make a group, whose word is the group's map or, once it is known, the state behind it,
-// marked by +inf, which no decay is.  So the state in front of a tile comes through the
-// groups in front of its own, from the nearest that has its state, and through its own group's
-// maps: always by the same products, whatever was there first, and over 48 tiles in the
-// time that a word takes from one workgroup to another (about 1 us: 131072 tokens of 64
-// channels take 45 us, 133 where tiles take their states from the 8 in front of them;
-// 32768 of 200 with gradients 89 and 118, of 2560 440 and 434).
-// Both halves of a word come and go in one 64-bit access, so it needs no other ordering; it
-// starts as kUnset, a NaN that no decay is stored as.
-constexpr int kGroup = 8;
-constexpr uint64_t kUnset = ~0ull;
-constexpr uint32_t kState = 0x7f800000u;
-__device__ __forceinline__ uint64_t word_of(float dec, float h) {
-  const uint32_t hi = dec != dec ? 0x7fc00000u : __float_as_uint(dec);
-  return (uint64_t)hi << 32 | __float_as_uint(h);
-}
-__device__ __forceinline__ uint64_t state_word(float h) {
-  return (uint64_t)kState << 32 | __float_as_uint(h);
-}
-__device__ __forceinline__ void put_word(uint64_t* p, uint64_t w) {
-  __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ uint64_t get_word(const uint64_t* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
+// How words come and go between workgroups (rec_link.h).
+struct DeviceWords {
+  __device__ __forceinline__ static void put(uint64_t* p, uint64_t w) {
+    __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __device__ __forceinline__ static uint64_t get(const uint64_t* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __device__ __forceinline__ static void pause() { __builtin_amdgcn_s_sleep(1); }
+};
 
 // Words unset, the counter of begun tiles at 0.
 __global__ __launch_bounds__(kBlock) void rec_clear_kernel(uint4* __restrict__ words, int64_t n,
@@ -253,20 +201,10 @@ __global__ __launch_bounds__(kBlock) void rec_clear_kernel(uint4* __restrict__ w
     words[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
 
-struct Links {
-  uint64_t* maps;    // [B][tiles][d], null where there is one tile
-  uint64_t* states;  // [B][groups][d]: group g's has the word of g - 1, the first one a state
-  uint32_t* begun;
-  int64_t tiles, groups;
-};
-
 // The workgroup's tile.  Tiles are handed out in the order in which workgroups begin,
 // those of all sequences and strips at one place before those behind it (backward: in
 // front of it): every tile that this one waits for is at work already, and the first
 // of a sequence waits for none, so that all waits end whatever the order of workgroups.
-struct TileAt {
-  int64_t b, j, strip, k;  // k: tiles that come before it in its sequence
-};
 template <class S>
 __device__ __forceinline__ TileAt tile_at(const RecArgs& a, const Links& links, bool reverse) {
   __shared__ uint32_t ticket;
@@ -285,84 +223,6 @@ __device__ __forceinline__ TileAt tile_at(const RecArgs& a, const Links& links, 
   at.strip = w % strips;
   at.j = reverse ? links.tiles - 1 - at.k : at.k;
   return at;
-}
-
-// Waits end by themselves (tile_at); only where another call clears the same words
-// meanwhile, which no workspace allows, they end here, after some seconds and with NaN.
-constexpr int kTries = 1 << 22;
-
-// The map over a group's first n tiles (1 <= n < kGroup), from their words, `step` words apart.
-__device__ __forceinline__ void map_before(const uint64_t* word, int64_t step, int n, float* dec,
-                                           float* h) {
-  for (int tries = 0; tries < kTries; ++tries) {
-    uint64_t w[kGroup - 1];
-#pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i)
-      if (i < n) w[i] = get_word(word + i * step);
-    bool all = true;
-    *dec = -0.0f, *h = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i) {
-      if (i >= n) break;
-      const float d = __uint_as_float((uint32_t)(w[i] >> 32));
-      all = all && w[i] != kUnset;
-      *dec = decay_both(*dec, d);
-      *h = decayed(d, *h, __uint_as_float((uint32_t)w[i]));
-    }
-    if (all) return;
-    __builtin_amdgcn_s_sleep(1);
-  }
-  *dec = *h = __builtin_nanf("");
-}
-
-// The state in front of a group, from its word and those of the k groups in front of it at
-// `word`, `word` - step, ...: from the nearest of kAhead that is a state, the maps behind
-// that one applied in order.
-__device__ __forceinline__ float state_before(const uint64_t* word, int64_t step, int64_t k) {
-  constexpr int kAhead = 6;
-  for (int tries = 0; tries < kTries; ++tries) {
-    uint64_t w[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) w[i] = get_word(word - (i < k ? i : k) * step);
-    bool found = false;
-    float s = 0.0f;
-#pragma unroll
-    for (int i = kAhead - 1; i >= 0; --i) {
-      const uint32_t hi = (uint32_t)(w[i] >> 32);
-      const float f = __uint_as_float((uint32_t)w[i]);
-      found = hi == kState || (found && w[i] != kUnset);
-      s = hi == kState ? f : decayed(__uint_as_float(hi), s, f);
-    }
-    if (found) return s;
-    __builtin_amdgcn_s_sleep(1);
-  }
-  return __builtin_nanf("");
-}
-
-// The state in front of a tile of a channel, from the tile's map: what the tiles behind it
-// need is left to them, as soon as it is known.
-template <class First>
-__device__ __forceinline__ float link(const Links& links, const TileAt& at, int64_t d, int64_t c,
-                                      float dec, float h, First&& first) {
-  const int64_t g = at.k / kGroup;
-  const int in = (int)(at.k % kGroup);
-  uint64_t* const map = links.maps + (at.b * links.tiles + at.k) * d + c;
-  uint64_t* const state = links.states + (at.b * links.groups + g) * d + c;
-  const bool last = in == kGroup - 1 && g + 1 < links.groups;
-  if (in < kGroup - 1 && at.k + 1 < links.tiles) put_word(map, word_of(dec, h));
-  float before = -0.0f, from0 = 0.0f;  // the map over the group's tiles in front
-  if (in > 0) map_before(map - in * d, d, in, &before, &from0);
-  const float all = decay_both(before, dec), all0 = decayed(dec, from0, h);
-  if (last) put_word(state + d, word_of(all, all0));
-  float s;
-  if (at.k == 0) {
-    s = first(c);
-    put_word(state, state_word(s));
-  } else {
-    s = state_before(state, d, g);
-  }
-  if (last) put_word(state + d, state_word(decayed(all, s, all0)));
-  return in > 0 ? decayed(before, s, from0) : s;
 }
 
 // What a lane of a tile works on.
@@ -507,7 +367,7 @@ __device__ __forceinline__ void link_tile(Runs<S>& rs, const RecArgs& a, const L
       z += zp;
     }
     const float whole = decay_of(z);
-    float s = links.maps ? link(links, at, a.d, c, whole, ph, first) : first(c);
+    float s = links.maps ? link<DeviceWords>(links, at, a.d, c, whole, ph, first) : first(c);
     const float before = s;
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
