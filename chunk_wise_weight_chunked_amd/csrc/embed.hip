@@ -81,8 +81,8 @@ struct SortIn {
 // come behind its own: the sort leaves most of the chip idle, and the zeros need no more
 // than the memory's bandwidth.
 struct Zeros {
-  uint4* p;       // null: none
-  int64_t n;
+  uint4* p;
+  int64_t n;      // 0: none, and no workgroups behind the launch's own
   int32_t own;    // the launch's own workgroups
   template <int kThreads>
   __device__ __forceinline__ bool fill() const {
